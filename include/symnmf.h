@@ -23,7 +23,8 @@
  *     comes with the library's code object on each device it runs on.)
  *   - All device work is enqueued on `hip_stream` (a hipStream_t; NULL is the
  *     null stream). Calls that fill _host outputs synchronise that stream
- *     before they return; symnmf_labels is asynchronous.
+ *     before they return; symnmf_labels and the sequence operators
+ *     (symnmf_embed ... symnmf_token_logprobs_grad) are asynchronous.
  *   - Return value: 0 = OK, > 0 = warning, < 0 = error (enum below). Arguments
  *     are validated on the host before any device work is enqueued; an
  *     invalid call returns SYMNMF_E_INVALID / SYMNMF_E_WORKSPACE and touches
@@ -88,8 +89,15 @@ enum symnmf_op {
     SYMNMF_OP_SH = 3,
     SYMNMF_OP_KMEANS = 4, /* k_or_p = k */
     SYMNMF_OP_SQ = 5,     /* k_or_p = w */
-    SYMNMF_OP_SH_SYM = 6  /* k_or_p = k */
+    SYMNMF_OP_SH_SYM = 6, /* k_or_p = k */
+    SYMNMF_OP_EMBED_GRAD = 7,    /* n = rows of the table, k_or_p = width, T = count */
+    SYMNMF_OP_GATED_SCAN = 8,    /* n = width, k_or_p = batch, T = steps (and its gradient) */
+    SYMNMF_OP_TOKEN_LOGPROBS = 9 /* n = vocab, k_or_p = top, T = count */
 };
+
+/* Element and index types of the sequence operators (symnmf_embed ff.). */
+enum symnmf_dtype { SYMNMF_F32 = 0, SYMNMF_BF16 = 1, SYMNMF_F16 = 2 };
+enum symnmf_index { SYMNMF_I32 = 0, SYMNMF_I64 = 1 };
 
 /* u(seed, c) above: the top 24 bits of output c+1 of SplitMix64 (Steele, Lea
  * and Flood, OOPSLA 2014) started at state `seed`, times 2^-24. */
@@ -345,6 +353,109 @@ int symnmf_spherical_kmeans(const float* S, int64_t n, int64_t lds, int32_t k,
                             float* centroids, int32_t* iters_host,
                             int32_t* converged_host, double* objective_host,
                             void* ws, size_t ws_bytes, void* hip_stream);
+
+/* ---- sequence operators ---------------------------------------------------
+ * A stream of events (the instrument that had a tail day, the cluster an
+ * instrument moved to) as a sequence of tokens: their loadings looked up in a
+ * table (H, or one learned from it), filtered through time, and the next
+ * event scored. All of them are asynchronous, take float32, bfloat16 or
+ * float16 elements (enum symnmf_dtype), compute and sum in float32 and round
+ * each output once. Strides are in elements; channels (and the columns of a
+ * row) have unit stride, and no stride is negative. Faster where pointers and
+ * strides are multiples of 16 bytes; any element alignment works. Outputs must
+ * not overlap inputs unless said otherwise. */
+
+/* out[i, :] = scale * table[ids[i], :] for i < count (table rows x width, ld
+ * ldt; out count x width, ld ldo; ids dense int32 or int64). An id < 0 is an
+ * empty slot: its row is zero. An id >= rows is an error that shows: its row
+ * is NaN (nothing is read). count = 0 is a no-op.
+ * Errors: E_INVALID, E_HIP. */
+int symnmf_embed(const void* table, int table_type, int64_t rows, int64_t width, int64_t ldt,
+                 const void* ids, int id_type, int64_t count, float scale, void* out, int out_type,
+                 int64_t ldo, void* hip_stream);
+
+/* The table's gradient: dtable[v, :] = scale * sum over i with ids[i] = v of
+ * dout[i, :], added in a fixed order (tokens sorted by id, equal ids in token
+ * order, partial sums of fixed length joined in order): the same bits on every
+ * call. Rows that no token names are zero. accumulate = 1 adds to dtable
+ * instead (rows without tokens are left alone). Ids outside [0, rows) give
+ * nothing, and their rows of dout are not read.
+ * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
+int symnmf_embed_grad(const void* dout, int dout_type, int64_t count, int64_t width, int64_t ldd,
+                      const void* ids, int id_type, float scale, int accumulate, void* dtable,
+                      int dtable_type, int64_t rows, int64_t ldt, void* ws, size_t ws_bytes,
+                      void* hip_stream);
+
+/* Gated linear recurrence, per batch row b and channel:
+ *   a_t = sigmoid(gate_t), h_t = a_t h_{t-1} + (1 - a_t) x_t, h_{-1} = h0
+ * (an exponential moving average whose decay is given, or learned, per step
+ * and channel). x and gate: element (b, t, c) at b * x_batch + t * x_step + c;
+ * a stride of 0 broadcasts (one decay per channel: gate strides 0, 0). h
+ * (batch x steps x width, dense) receives h_t in the inputs' type.
+ *   lengths (nullable, batch int32): steps t >= lengths[b] are masked; their
+ *     x and gate are not read, their h is 0 and the state passes them
+ *     unchanged. Values are clamped to [0, steps].
+ *   h0 (nullable: zeros), h_last (nullable): batch x width float32, the
+ *     state before the first step and after the last one.
+ *   states (nullable): batch x ceil(steps / 128) x width float32, the state
+ *     before every 128th step, which the gradient starts from.
+ * A gate of -inf drops the state (h_t = x_t), one of +inf keeps it. One step
+ * of a live stream is steps = 1 with h0 and h_last; h0 and h_last may be the
+ * same buffer then. Time is scanned in parallel with a fixed order of
+ * operations. 1 <= batch <= 65535, steps >= 0.
+ * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
+int symnmf_gated_scan(int type, int64_t batch, int64_t steps, int64_t width, const void* x,
+                      int64_t x_batch, int64_t x_step, const void* gate, int64_t gate_batch,
+                      int64_t gate_step, const int32_t* lengths, const float* h0, void* h,
+                      float* h_last, float* states, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Gradient of symnmf_gated_scan from dh (the gradient at h; strides like x's)
+ * and dh_last (nullable, batch x width float32: the gradient at h_last):
+ *   lam_t = dh_t + a_{t+1} lam_{t+1},  dx_t = (1 - a_t) lam_t,
+ *   dgate_t = lam_t (h_{t-1} - x_t) a_t (1 - a_t),  dh0 = a_0 lam_0,
+ * with h rebuilt in float32 from the forward's `states`. dx and dgate
+ * (batch x steps x width, dense, the inputs' type) are given per element, 0 at
+ * masked steps; the gradient of a broadcast gate is their sum over what it was
+ * broadcast over, left to the caller. dh0 (nullable): batch x width float32.
+ * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
+int symnmf_gated_scan_grad(int type, int64_t batch, int64_t steps, int64_t width, const void* x,
+                           int64_t x_batch, int64_t x_step, const void* gate, int64_t gate_batch,
+                           int64_t gate_step, const int32_t* lengths, const float* states,
+                           const void* dh, int64_t dh_batch, int64_t dh_step,
+                           const float* dh_last, void* dx, void* dgate, float* dh0, void* ws,
+                           size_t ws_bytes, void* hip_stream);
+
+/* Log probabilities of given tokens: per row i < count of logits (count x
+ * vocab, ld), under p = softmax(scale * logits[i, :]),
+ *   logp[i] = ln p[tokens[i]], entropy[i] = -sum p ln p (nullable),
+ *   lse[i] = ln sum exp(scale * logits) (nullable), and the `top` (0 to 32)
+ * most likely columns: top_ids[i, :] (int32, most likely first, equal logits
+ * by column) with top_logp[i, :], both count x top dense. scale > 0 (1 /
+ * temperature).
+ * A logit of -inf excludes its column: probability 0, never an alternative;
+ * where fewer than `top` columns are left the rest is id -1 with -inf. A row
+ * with no column left has lse = logp = -inf and entropy 0. A row that holds
+ * NaN or +inf gives NaN. A token < 0 is no token: logp 0. A token >= vocab
+ * gives NaN.
+ * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
+int symnmf_token_logprobs(const void* logits, int type, int64_t count, int64_t vocab, int64_t ld,
+                          const void* tokens, int token_type, float scale, float* logp,
+                          float* entropy, float* lse, int32_t top, float* top_logp,
+                          int32_t* top_ids, void* ws, size_t ws_bytes, void* hip_stream);
+
+/* Gradient at the logits from the gradients dlogp (count) and dentropy
+ * (count, nullable) at logp and entropy, with the forward's lse and entropy
+ * (nullable unless dentropy is given):
+ *   dlogits_j = scale (dlogp ([j = token] - p_j) - dentropy p_j (ln p_j + entropy)),
+ * in the logits' type (count x vocab, ld ldd; it may be the logits' own
+ * buffer with ldd = ld). Rows without a token have the entropy's part alone, rows with
+ * no column left are zero. The alternatives carry no gradient.
+ * Errors: E_INVALID, E_HIP. */
+int symnmf_token_logprobs_grad(const void* logits, int type, int64_t count, int64_t vocab,
+                               int64_t ld, const void* tokens, int token_type, float scale,
+                               const float* lse, const float* entropy, const float* dlogp,
+                               const float* dentropy, void* dlogits, int64_t ldd,
+                               void* hip_stream);
 
 const char* symnmf_status_string(int status);
 int symnmf_abi_version(void);

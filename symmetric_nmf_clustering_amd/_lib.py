@@ -26,6 +26,11 @@ AUTO, FULL, BLOCK_SVRG = 0, 1, 2
 INIT_UNIFORM, INIT_SCALE_MATCHED, INIT_CALLER = 0, 1, 2
 SH_ROWS, SH_UPPER = 0, 1
 OP_BUILD_S, OP_PROBE, OP_FIT, OP_SH, OP_KMEANS, OP_SQ, OP_SH_SYM = 0, 1, 2, 3, 4, 5, 6
+OP_EMBED_GRAD, OP_GATED_SCAN, OP_TOKEN_LOGPROBS = 7, 8, 9
+F32, BF16, F16 = 0, 1, 2
+I32, I64 = 0, 1
+SCAN_CHUNK = 128  # steps between the states a gated scan keeps for its gradient
+MAX_TOP = 32      # most alternatives per row of token_logprobs
 (PROF_SH_FULL, PROF_SH_SAMPLED, PROF_SH_PROBE, PROF_BUILD_GRAM, PROF_UPDATE,
  PROF_SH_KMEANS, PROF_SH_SYM) = 0, 1, 2, 3, 4, 5, 6
 PROF_NAMES = {
@@ -102,6 +107,9 @@ _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
 _D = ctypes.c_double
+_F = ctypes.c_float
+_I = ctypes.c_int
+_Z = ctypes.c_size_t
 SIGNATURES = [
     ("symnmf_abi_version", ctypes.c_int, []),
     ("symnmf_status_string", ctypes.c_char_p, [ctypes.c_int]),
@@ -129,6 +137,19 @@ SIGNATURES = [
     ("symnmf_spherical_kmeans", ctypes.c_int,
      [_P, _I64, _I64, _I32, _I32, ctypes.c_uint64, _P, _P, ctypes.POINTER(_I32),
       ctypes.POINTER(_I32), ctypes.POINTER(_D), _P, ctypes.c_size_t, _P]),
+    ("symnmf_embed", _I,
+     [_P, _I, _I64, _I64, _I64, _P, _I, _I64, _F, _P, _I, _I64, _P]),
+    ("symnmf_embed_grad", _I,
+     [_P, _I, _I64, _I64, _I64, _P, _I, _F, _I, _P, _I, _I64, _I64, _P, _Z, _P]),
+    ("symnmf_gated_scan", _I,
+     [_I, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    ("symnmf_gated_scan_grad", _I,
+     [_I, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _I64, _I64, _P, _P, _P, _P,
+      _P, _Z, _P]),
+    ("symnmf_token_logprobs", _I,
+     [_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _I32, _P, _P, _P, _Z, _P]),
+    ("symnmf_token_logprobs_grad", _I,
+     [_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _P, _P, _I64, _P]),
     ("symnmf_profile_enable", None, [ctypes.c_int]),
     ("symnmf_profile_reset", None, []),
     ("symnmf_profile_read", ctypes.c_int,

@@ -342,6 +342,288 @@ def spherical_kmeans(S: torch.Tensor, k: int, *, max_iters: int = 100, seed: int
     return KmeansResult(lab, C, it.value, bool(conv.value), obj.value, st)
 
 
+# ---- sequence operators ------------------------------------------------------
+_DTYPES = {torch.float32: L.F32, torch.bfloat16: L.BF16, torch.float16: L.F16}
+_INDEX = {torch.int32: L.I32, torch.int64: L.I64}
+
+
+def _seq_tensor(t, name: str, types=_DTYPES, dtype=None, shape=None, device=None) -> int:
+    """Checks a device tensor of a sequence operator and returns its type code."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a HIP device tensor")
+    if t.dtype not in types or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or ' or '.join(str(d) for d in types)}, "
+                         f"not {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, not {t.device}")
+    return types[t.dtype]
+
+
+def _here(device):
+    """The stream to launch on: torch's current one, of the tensors' device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _rows_ld(t: torch.Tensor, name: str) -> int:
+    """Leading dimension of a 2-D tensor of rows with unit column stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+def embed(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
+          dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """scale * table[ids] (rows x width table of float32, bfloat16 or float16;
+    int32 or int64 ids of any shape), of shape ids.shape + (width,) in ``dtype``
+    (default: the table's). A negative id is an empty slot (a row of zeros); an
+    id past the table gives a row of NaN."""
+    tt = _seq_tensor(table, "table")
+    it = _seq_tensor(ids, "ids", _INDEX, device=table.device)
+    ld = _rows_ld(table, "table")
+    rows, width = table.shape
+    if rows < 1 or width < 1:
+        raise ValueError("table must not be empty")
+    out = torch.empty((*ids.shape, width), dtype=dtype or table.dtype, device=table.device)
+    ot = _seq_tensor(out, "out")
+    ids = ids.contiguous()
+    st = L.load().symnmf_embed(table.data_ptr(), tt, rows, width, ld, ids.data_ptr(), it,
+                               ids.numel(), scale, out.data_ptr(), ot, width,
+                               _here(table.device))
+    L.check(st, "symnmf_embed")
+    return out
+
+
+def embed_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 1.0,
+               dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+               accumulate: bool = False) -> torch.Tensor:
+    """Gradient of ``embed`` at its table: scale * the sum of dout's rows by id
+    (dout of shape ids.shape + (width,)), a rows x width tensor of ``dtype`` or
+    ``out`` itself (accumulate=True adds to what ``out`` holds). Summed in
+    float32 in a fixed order. Ids outside the table give nothing."""
+    dt = _seq_tensor(dout, "dout")
+    it = _seq_tensor(ids, "ids", _INDEX, device=dout.device)
+    if dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
+        raise ValueError("dout must have the shape of ids and one more dimension")
+    width = dout.shape[-1]
+    if rows < 1 or width < 1:
+        raise ValueError("the table must not be empty")
+    if accumulate and out is None:
+        raise ValueError("accumulate=True needs out")
+    if out is None:
+        out = torch.empty((rows, width), dtype=dtype, device=dout.device)
+    ot = _seq_tensor(out, "out", shape=(rows, width), device=dout.device)
+    ldo = _rows_ld(out, "out")
+    flat = dout.reshape(-1, width)
+    if width > 1 and flat.stride(1) != 1:
+        flat = flat.contiguous()
+    ldd = _rows_ld(flat, "dout") if flat.shape[0] else width
+    ids = ids.contiguous()
+    ws = workspace(workspace_bytes(L.OP_EMBED_GRAD, rows, width, ids.numel()), dout.device)
+    st = L.load().symnmf_embed_grad(flat.data_ptr(), dt, ids.numel(), width, ldd, ids.data_ptr(), it,
+                                    scale, int(accumulate), out.data_ptr(), ot, rows, ldo,
+                                    ws.data_ptr(), ws.numel(), _here(dout.device))
+    L.check(st, "symnmf_embed_grad")
+    return out
+
+
+def _scan_view(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None):
+    """(batch stride, step stride) of a batch x steps x width tensor."""
+    if like is None:
+        _seq_tensor(t, name)
+        if t.dim() != 3:
+            raise ValueError(f"{name} must be batch x steps x width")
+    else:
+        _seq_tensor(t, name, dtype=like.dtype, shape=like.shape, device=like.device)
+    if t.numel() == 0:
+        return 0, 0
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} needs unit channel stride")
+    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _state_ptr(t: Optional[torch.Tensor], name: str, shape, device):
+    if t is None:
+        return None
+    _seq_tensor(t, name, dtype=torch.float32, shape=shape, device=device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _lengths_ptr(lengths: Optional[torch.Tensor], batch: int, device):
+    if lengths is None:
+        return None
+    _seq_tensor(lengths, "lengths", {torch.int32: 0}, shape=(batch,), device=device)
+    if not lengths.is_contiguous():
+        raise ValueError("lengths must be contiguous")
+    return lengths.data_ptr()
+
+
+def gated_scan(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None, return_states: bool = False):
+    """h_t = a_t h_{t-1} + (1 - a_t) x_t over the steps of x (batch x steps x
+    width), a = sigmoid(gate), from the state ``h0`` (batch x width float32;
+    default zeros). ``gate`` has x's shape and type; an expanded view (one decay
+    per channel, say) is read as it is. Steps at and past ``lengths[b]`` (int32)
+    are masked: h is 0 there and the state passes. Returns (h, the last state in
+    float32), and with ``return_states`` the states ``gated_scan_grad`` needs."""
+    x_b, x_t = _scan_view(x, "x")
+    g_b, g_t = _scan_view(gate, "gate", x)
+    batch, steps, width = x.shape
+    dev = x.device
+    if batch < 1 or width < 1:
+        raise ValueError("x must have at least one batch row and one channel")
+    h = torch.empty((batch, steps, width), dtype=x.dtype, device=dev)
+    last = torch.empty((batch, width), dtype=torch.float32, device=dev)
+    states = None
+    if return_states:
+        states = torch.empty((batch, -(-steps // L.SCAN_CHUNK), width), dtype=torch.float32,
+                             device=dev)
+    ws = workspace(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
+    st = L.load().symnmf_gated_scan(
+        _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
+        _lengths_ptr(lengths, batch, dev), _state_ptr(h0, "h0", (batch, width), dev),
+        h.data_ptr(), last.data_ptr(), None if states is None else states.data_ptr(),
+        ws.data_ptr(), ws.numel(), _here(dev))
+    L.check(st, "symnmf_gated_scan")
+    return (h, last, states) if return_states else (h, last)
+
+
+def gated_step(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor):
+    """One step of ``gated_scan`` for live streams: x and gate batch x width,
+    state batch x width float32. Returns (h in x's type, the new state)."""
+    if x.dim() != 2 or gate.dim() != 2:
+        raise ValueError("x and gate must be batch x width")
+    h, last = gated_scan(x.unsqueeze(1), gate.unsqueeze(1), h0=state)
+    return h.squeeze(1), last
+
+
+def gated_scan_grad(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, dh: torch.Tensor,
+                    dh_last: Optional[torch.Tensor] = None,
+                    lengths: Optional[torch.Tensor] = None):
+    """Gradient of ``gated_scan`` from dh (at h) and ``dh_last`` (at the last
+    state), with the forward's ``states``. Returns (dx, dgate, dh0): dx and
+    dgate per element in x's type, dh0 batch x width float32. The gradient of
+    an expanded gate is dgate's sum over the expanded dimensions."""
+    x_b, x_t = _scan_view(x, "x")
+    g_b, g_t = _scan_view(gate, "gate", x)
+    d_b, d_t = _scan_view(dh, "dh", x)
+    batch, steps, width = x.shape
+    dev = x.device
+    if batch < 1 or width < 1:
+        raise ValueError("x must have at least one batch row and one channel")
+    dx = torch.empty((batch, steps, width), dtype=x.dtype, device=dev)
+    dgate = torch.empty_like(dx)
+    dh0 = torch.empty((batch, width), dtype=torch.float32, device=dev)
+    ws = workspace(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
+    st = L.load().symnmf_gated_scan_grad(
+        _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
+        _lengths_ptr(lengths, batch, dev),
+        _state_ptr(states, "states", (batch, -(-steps // L.SCAN_CHUNK), width), dev),
+        dh.data_ptr(), d_b, d_t, _state_ptr(dh_last, "dh_last", (batch, width), dev),
+        dx.data_ptr(), dgate.data_ptr(), dh0.data_ptr(), ws.data_ptr(), ws.numel(), _here(dev))
+    L.check(st, "symnmf_gated_scan_grad")
+    return dx, dgate, dh0
+
+
+@dataclass
+class TokenLogprobs:
+    logp: torch.Tensor
+    entropy: torch.Tensor
+    lse: torch.Tensor
+    top_logp: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+
+
+def _tokens(tokens: torch.Tensor, n: int, device):
+    it = _seq_tensor(tokens, "tokens", _INDEX, shape=(n,), device=device)
+    return tokens.contiguous(), it
+
+
+def _row_values(t: Optional[torch.Tensor], name: str, n: int, device):
+    if t is None:
+        return None
+    _seq_tensor(t, name, dtype=torch.float32, shape=(n,), device=device)
+    return t.contiguous()
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,
+                   scale: float = 1.0) -> TokenLogprobs:
+    """Per row of logits (count x vocab float32, bfloat16 or float16), under
+    softmax(scale * logits): the log probability of the row's token, the
+    entropy, the log of the normaliser and the ``top`` (at most 32) most likely
+    columns with their log probabilities (equal logits: lowest column first).
+    All float32, ids int32. Logits of -inf are excluded columns; a negative
+    token stands for none (logp 0)."""
+    lt = _seq_tensor(logits, "logits")
+    ld = _rows_ld(logits, "logits")
+    n, vocab = logits.shape
+    dev = logits.device
+    if vocab < 1 or not 0 <= top <= L.MAX_TOP:
+        raise ValueError(f"logits need a column, and top must be 0 to {L.MAX_TOP}")
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
+    tokens, it = _tokens(tokens, n, dev)
+    buf = torch.empty((3, n), dtype=torch.float32, device=dev)
+    top_logp = top_ids = None
+    if top:
+        top_logp = torch.empty((n, top), dtype=torch.float32, device=dev)
+        top_ids = torch.empty((n, top), dtype=torch.int32, device=dev)
+    ws = workspace(workspace_bytes(L.OP_TOKEN_LOGPROBS, vocab, top, n), dev)
+    at = buf.data_ptr()
+    st = L.load().symnmf_token_logprobs(
+        logits.data_ptr(), lt, n, vocab, ld, tokens.data_ptr(), it, scale, at, at + 4 * n,
+        at + 8 * n, top, top_logp.data_ptr() if top else None, top_ids.data_ptr() if top else None,
+        ws.data_ptr(), ws.numel(), _here(dev))
+    L.check(st, "symnmf_token_logprobs")
+    return TokenLogprobs(buf[0], buf[1], buf[2], top_logp, top_ids)
+
+
+def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
+                        entropy: Optional[torch.Tensor], dlogp: torch.Tensor,
+                        dentropy: Optional[torch.Tensor] = None, scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient at the logits from the gradients at ``token_logprobs``'s logp
+    and (optionally) entropy, with its lse and entropy. In the logits' type;
+    ``out`` may be the logits themselves."""
+    lt = _seq_tensor(logits, "logits")
+    ld = _rows_ld(logits, "logits")
+    n, vocab = logits.shape
+    dev = logits.device
+    if vocab < 1:
+        raise ValueError("logits need a column")
+    if not (scale > 0 and math.isfinite(scale)):
+        raise ValueError("scale must be positive and finite")
+    if dentropy is not None and entropy is None:
+        raise ValueError("dentropy needs the entropy")
+    tokens, it = _tokens(tokens, n, dev)
+    if lse is None or dlogp is None:
+        raise ValueError("lse and dlogp are needed")
+    lse = _row_values(lse, "lse", n, dev)
+    entropy = _row_values(entropy, "entropy", n, dev)
+    dlogp = _row_values(dlogp, "dlogp", n, dev)
+    dentropy = _row_values(dentropy, "dentropy", n, dev)
+    if out is None:
+        out = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
+    _seq_tensor(out, "out", dtype=logits.dtype, shape=logits.shape, device=dev)
+    ldd = _rows_ld(out, "out")
+    if out.data_ptr() == logits.data_ptr() and ldd != ld:
+        raise ValueError("out shares the logits' memory in another layout")
+    st = L.load().symnmf_token_logprobs_grad(
+        logits.data_ptr(), lt, n, vocab, ld, tokens.data_ptr(), it, scale, lse.data_ptr(),
+        None if entropy is None else entropy.data_ptr(), dlogp.data_ptr(),
+        None if dentropy is None else dentropy.data_ptr(), out.data_ptr(), ldd, _here(dev))
+    L.check(st, "symnmf_token_logprobs_grad")
+    return out
+
+
 # ---- kernel timing ---------------------------------------------------------
 def profile_enable(on: bool = True):
     L.load().symnmf_profile_enable(1 if on else 0)

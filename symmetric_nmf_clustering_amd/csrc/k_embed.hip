@@ -1,0 +1,515 @@
+// Event embedding: out[i] = scale * table[ids[i]], and its gradient
+//   dtable[v] = scale * sum_{i : ids[i] = v} dout[i].
+//
+// The gradient sorts the tokens by id (stable, so a row's terms stay in the
+// order of the tokens), cuts the sorted list into chunks and lets one group
+// of threads add each chunk's rows in order in fp32. A row whose terms lie in
+// one chunk is written at once; the others leave one partial per chunk, which
+// a second kernel adds in chunk order. No floating-point atomics: the result
+// is the same on every run.
+#include "common.h"
+#include "seq.h"
+
+namespace symnmf {
+namespace {
+
+// ---- lookup ------------------------------------------------------------------
+
+// One row per group of `lx` lanes (a power of two <= 256), V elements a lane
+// and step. An id < 0 is an empty slot (zeros); one past the table gives NaN.
+template <class TI, class TO, class ID, int V>
+__global__ __launch_bounds__(256) void embed_kernel(const TI* __restrict__ table, int64_t rows,
+                                                    int width, int64_t ldt,
+                                                    const ID* __restrict__ ids, int64_t count,
+                                                    float scale, TO* __restrict__ out, int64_t ldo,
+                                                    int lx_log2) {
+    const int lx = 1 << lx_log2;
+    const int lane = threadIdx.x & (lx - 1);
+    const int64_t i = (int64_t)blockIdx.x * (256 >> lx_log2) + (threadIdx.x >> lx_log2);
+    if (i >= count) return;
+    const int64_t id = (int64_t)ids[i];
+    const bool in = id >= 0 && id < rows;
+    const float fill = id < 0 ? 0.f : __builtin_nanf("");
+    const TI* src = table + (in ? id : 0) * ldt;
+    TO* dst = out + i * ldo;
+    for (int c = lane * V; c < width; c += lx * V) {
+        if (V == 1 || c + V <= width) {
+            Vec<TO, V> o;
+            if (in) {
+                const Vec<TI, V> v = load_vec<TI, V>(src + c);
+#pragma unroll
+                for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(to_f32(v.e[u]) * scale);
+            } else {
+#pragma unroll
+                for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(fill);
+            }
+            store_vec<TO, V>(dst + c, o);
+        } else {
+            for (int u = c; u < width; ++u)
+                dst[u] = from_f32<TO>(in ? to_f32(src[u]) * scale : fill);
+        }
+    }
+}
+
+// ---- gradient ------------------------------------------------------------------
+
+constexpr int kSortMaxBits = 9;              // digit of one sort pass
+constexpr int kSortMaxBins = 1 << kSortMaxBits;
+constexpr int kSortMaxBlocks = 128;
+
+// How a list of `count` ids below `rows` is sorted: passes of `bits` bits from
+// the lowest, `nblk` blocks of `tile` tokens.
+struct SortPlan {
+    int bits, passes, nblk, tile;
+};
+SortPlan sort_plan(int64_t rows, int64_t count) {
+    SortPlan p;
+    int need = 1;
+    while (need < 32 && (rows >> need) > 0) ++need;  // the key `rows` (no row) included
+    p.passes = (need + kSortMaxBits - 1) / kSortMaxBits;
+    p.bits = (need + p.passes - 1) / p.passes;
+    int64_t tile = 1024;
+    while ((count + tile - 1) / tile > kSortMaxBlocks) tile *= 2;
+    p.tile = (int)tile;
+    p.nblk = (int)((count + tile - 1) / tile);
+    return p;
+}
+
+// Sorted entries per chunk of the sum: 32 keeps a chunk's reads in a few round
+// trips, more where there are so many tokens that the partials would grow.
+int chunk_len(int64_t count) { return count <= 65536 ? 32 : 128; }
+
+template <class ID>
+__device__ __forceinline__ uint32_t key_of(ID id, int64_t rows) {
+    return id >= 0 && (int64_t)id < rows ? (uint32_t)id : (uint32_t)rows;
+}
+
+// First pass's keys come from the ids, later ones from the previous pass.
+template <class ID>
+struct FirstKeys {
+    const ID* ids;
+    int64_t rows;
+    __device__ uint32_t key(int64_t i) const { return key_of(ids[i], rows); }
+    __device__ int32_t pos(int64_t i) const { return (int32_t)i; }
+};
+struct NextKeys {
+    const uint32_t* keys;
+    const int32_t* at;
+    __device__ uint32_t key(int64_t i) const { return keys[i]; }
+    __device__ int32_t pos(int64_t i) const { return at[i]; }
+};
+
+// hist[b][digit] of block b's tile. The first pass also clears the table's
+// presence flags.
+template <class SRC>
+__global__ __launch_bounds__(256) void sort_hist_kernel(SRC src, int64_t count, int tile, int shift,
+                                                        int bins, int32_t* __restrict__ hist,
+                                                        uint8_t* __restrict__ present,
+                                                        int64_t rows) {
+    __shared__ int32_t h[kSortMaxBins];
+    for (int b = threadIdx.x; b < bins; b += 256) h[b] = 0;
+    if (present)
+        for (int64_t v = (int64_t)blockIdx.x * 256 + threadIdx.x; v < rows;
+             v += (int64_t)gridDim.x * 256)
+            present[v] = 0;
+    __syncthreads();
+    const int64_t lo = (int64_t)blockIdx.x * tile;
+    const int64_t hi = lo + tile < count ? lo + tile : count;
+    for (int64_t i = lo + threadIdx.x; i < hi; i += 256)
+        atomicAdd(&h[(src.key(i) >> shift) & (bins - 1)], 1);  // counts: order-free
+    __syncthreads();
+    for (int b = threadIdx.x; b < bins; b += 256) hist[(int64_t)blockIdx.x * bins + b] = h[b];
+}
+
+// Moves a tile's tokens to their places, in order: the place of a token is the
+// number of tokens with a smaller digit, plus those with its digit in earlier
+// blocks, earlier waves' quarters of the tile and earlier lanes of its wave.
+template <class SRC>
+__global__ __launch_bounds__(256) void sort_scatter_kernel(
+    SRC src, int64_t count, int tile, int shift, int bits, const int32_t* __restrict__ hist,
+    uint32_t* __restrict__ keys_out, int32_t* __restrict__ pos_out, uint8_t* __restrict__ present,
+    int64_t rows) {
+    __shared__ int32_t at[4][kSortMaxBins];  // counts, then next place, by wave and digit
+    __shared__ int32_t wtot[4];
+    const int bins = 1 << bits, t = threadIdx.x, lane = t & 63, w = t >> 6;
+    const int nblk = gridDim.x, blk = blockIdx.x;
+    for (int b = t; b < 4 * kSortMaxBins; b += 256) (&at[0][0])[b] = 0;
+    // this block's first place for each digit: thread t owns the digits 2t, 2t + 1
+    int before[2] = {0, 0}, total[2] = {0, 0};
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int b = 2 * t + u;
+        if (b < bins)
+            for (int k = 0; k < nblk; ++k) {
+                const int v = hist[(int64_t)k * bins + b];
+                total[u] += v;
+                if (k < blk) before[u] += v;
+            }
+    }
+    int incl = total[0] + total[1];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 63) wtot[w] = incl;
+    __syncthreads();
+    int base = incl - total[0] - total[1];
+    for (int k = 0; k < w; ++k) base += wtot[k];
+    const int first0 = base + before[0], first1 = base + total[0] + before[1];
+    // counts of each wave's quarter
+    const int quarter = tile / 4;
+    const int64_t lo = (int64_t)blk * tile + (int64_t)w * quarter;
+    int64_t hi = lo + quarter;
+    if (hi > count) hi = count;
+    for (int64_t i = lo + lane; i < hi; i += 64)
+        atomicAdd(&at[w][(src.key(i) >> shift) & (bins - 1)], 1);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int b = 2 * t + u;
+        if (b < bins) {
+            int p = u ? first1 : first0;
+            for (int k = 0; k < 4; ++k) {
+                const int n = at[k][b];
+                at[k][b] = p;
+                p += n;
+            }
+        }
+    }
+    __syncthreads();
+    for (int64_t r = lo; r < hi; r += 64) {  // uniform over the wave
+        const int64_t i = r + lane;
+        const bool on = i < hi;
+        const uint32_t key = on ? src.key(i) : 0u;
+        const int d = (int)((key >> shift) & (uint32_t)(bins - 1));
+        uint64_t same = __ballot(on);
+        for (int b = 0; b < bits; ++b) {
+            const uint64_t one = __ballot((d >> b) & 1);
+            same &= ((d >> b) & 1) ? one : ~one;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1ull));
+        int place = 0;
+        if (on) place = at[w][d] + rank;
+        wave_lds_sync();
+        if (on && rank == 0) at[w][d] += __popcll(same);
+        wave_lds_sync();
+        if (on) {
+            keys_out[place] = key;
+            pos_out[place] = src.pos(i);
+            if (present && (int64_t)key < rows) present[key] = 1;
+        }
+    }
+}
+
+template <class TO, int V>
+__device__ __forceinline__ void put_row(TO* dst, int c, int width, const float (&acc)[V],
+                                        float scale, int accumulate) {
+    if (V == 1 || c + V <= width) {
+        Vec<TO, V> o;
+        if (accumulate) {
+            const Vec<TO, V> old = load_vec<TO, V>(dst + c);
+#pragma unroll
+            for (int u = 0; u < V; ++u)
+                o.e[u] = from_f32<TO>(to_f32(old.e[u]) + scale * acc[u]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(scale * acc[u]);
+        }
+        store_vec<TO, V>(dst + c, o);
+    } else {
+        for (int u = 0; u < V; ++u)
+            if (c + u < width) {
+                const float old = accumulate ? to_f32(dst[c + u]) : 0.f;
+                dst[c + u] = from_f32<TO>(old + scale * acc[u]);
+            }
+    }
+}
+
+// Group of lx lanes per chunk and column tile (blockIdx.y). Blocks past the
+// chunks write the rows no token names (zeros).
+template <class TD, class TO, int V>
+__global__ __launch_bounds__(256) void embed_grad_sum_kernel(
+    const TD* __restrict__ dout, int64_t ldd, int width, const uint32_t* __restrict__ keys,
+    const int32_t* __restrict__ pos, int64_t count, int clen, int64_t nchunks, int sum_blocks,
+    float scale, int accumulate, TO* __restrict__ dtable, int64_t ldt, int64_t rows,
+    const uint8_t* __restrict__ present, float* __restrict__ part, int ldpart, int lx_log2) {
+    const int lx = 1 << lx_log2, groups = 256 >> lx_log2;
+    const int lane = threadIdx.x & (lx - 1), grp = threadIdx.x >> lx_log2;
+    const int c = ((int)blockIdx.y * lx + lane) * V;
+    if ((int)blockIdx.x >= sum_blocks) {
+        const int64_t fill_blocks = gridDim.x - sum_blocks;
+        if (c >= width) return;
+        const float zero[V] = {};
+        for (int64_t v = ((int64_t)blockIdx.x - sum_blocks) * groups + grp; v < rows;
+             v += fill_blocks * groups)
+            if (!present[v]) put_row<TO, V>(dtable + v * ldt, c, width, zero, 1.f, 0);
+        return;
+    }
+    const int64_t chunk = (int64_t)blockIdx.x * groups + grp;
+    if (chunk >= nchunks || c >= width) return;
+    const int64_t lo = chunk * clen;
+    const int64_t hi = lo + clen < count ? lo + clen : count;
+    const bool whole = V == 1 || c + V <= width;
+    float acc[V] = {};
+    uint32_t cur = keys[lo];
+    bool head = lo > 0 && keys[lo - 1] == cur;  // the first row began in an earlier chunk
+    for (int64_t e = lo; e < hi; ++e) {
+        const uint32_t key = keys[e];
+        if (key != cur) {
+            if (head) {
+#pragma unroll
+                for (int u = 0; u < V; ++u)
+                    if (c + u < width) part[2 * chunk * ldpart + c + u] = acc[u];
+            } else if ((int64_t)cur < rows) {
+                put_row<TO, V>(dtable + (int64_t)cur * ldt, c, width, acc, scale, accumulate);
+            }
+            head = false;
+            cur = key;
+#pragma unroll
+            for (int u = 0; u < V; ++u) acc[u] = 0.f;
+        }
+        if ((int64_t)cur >= rows) break;  // the empty slots, sorted last
+        const TD* src = dout + (int64_t)pos[e] * ldd;
+        if (whole) {
+            const Vec<TD, V> v = load_vec<TD, V>(src + c);
+#pragma unroll
+            for (int u = 0; u < V; ++u) acc[u] += to_f32(v.e[u]);
+        } else {
+            for (int u = 0; u < V; ++u)
+                if (c + u < width) acc[u] += to_f32(src[c + u]);
+        }
+    }
+    if ((int64_t)cur >= rows) return;
+    const bool tail = hi < count && keys[hi] == cur;
+    if (head || tail) {
+        const int64_t slot = 2 * chunk + (head ? 0 : 1);
+#pragma unroll
+        for (int u = 0; u < V; ++u)
+            if (c + u < width) part[slot * ldpart + c + u] = acc[u];
+    } else {
+        put_row<TO, V>(dtable + (int64_t)cur * ldt, c, width, acc, scale, accumulate);
+    }
+}
+
+// A row that began in this chunk and goes on: its tail partial here, then the
+// head partials of the chunks that follow, in order.
+template <class TO>
+__global__ __launch_bounds__(256) void embed_grad_fold_kernel(
+    const uint32_t* __restrict__ keys, int64_t count, int clen, int64_t nchunks, float scale,
+    int accumulate, TO* __restrict__ dtable, int64_t ldt, int64_t rows, int width,
+    const float* __restrict__ part, int ldpart) {
+    const int64_t chunk = blockIdx.x;
+    const int64_t lo = chunk * clen, hi = lo + clen;
+    if (hi >= count) return;
+    const uint32_t key = keys[hi];
+    if ((int64_t)key >= rows || keys[hi - 1] != key) return;   // no row goes on
+    if (keys[lo] == key && lo > 0 && keys[lo - 1] == key) return;  // it began earlier
+    // the chunks after this one that hold terms of it begin with its key
+    int64_t more = 0;
+    for (;;) {
+        const int64_t j = chunk + 1 + more + threadIdx.x;
+        const int n = __syncthreads_count(j < nchunks && keys[j * clen] == key);
+        more += n;
+        if (n < 256) break;
+    }
+    for (int c = blockIdx.y * 256 + threadIdx.x; c < width; c += gridDim.y * 256) {
+        float s[1] = {part[(2 * chunk + 1) * ldpart + c] +
+                      ordered_strided_sum(part + 2 * (chunk + 1) * ldpart + c,
+                                          (int)more, 2 * (int64_t)ldpart)};
+        put_row<TO, 1>(dtable + (int64_t)key * ldt, c, width, s, scale, accumulate);
+    }
+}
+
+inline int log2_up(int64_t v, int most) {
+    int l = 0;
+    while (l < most && (int64_t(1) << l) < v) ++l;
+    return l;
+}
+inline bool vec_ok(const void* p, int64_t ld, int bytes, int v) {
+    return reinterpret_cast<uintptr_t>(p) % (size_t)(bytes * v) == 0 && ld % v == 0;
+}
+
+template <class TI, class TO, class ID, int V>
+hipError_t embed_run(const EmbedArgs& a, hipStream_t st) {
+    const int lg = log2_up((a.width + V - 1) / V, 8);
+    const int64_t per = 256 >> lg;
+    hipLaunchKernelGGL((embed_kernel<TI, TO, ID, V>), dim3((unsigned)((a.count + per - 1) / per)),
+                       dim3(256), 0, st, (const TI*)a.table, a.rows, (int)a.width, a.ldt,
+                       (const ID*)a.ids, a.count, a.scale, (TO*)a.out, a.ldo, lg);
+    return hipGetLastError();
+}
+template <class TI, class TO, class ID>
+hipError_t embed_vec(const EmbedArgs& a, hipStream_t st) {
+    constexpr int V = sizeof(TI) == 4 || sizeof(TO) == 4 ? 4 : 8;
+    if (vec_ok(a.table, a.ldt, sizeof(TI), V) && vec_ok(a.out, a.ldo, sizeof(TO), V))
+        return embed_run<TI, TO, ID, V>(a, st);
+    return embed_run<TI, TO, ID, 1>(a, st);
+}
+template <class TI, class TO>
+hipError_t embed_id(const EmbedArgs& a, hipStream_t st) {
+    return a.id_type == kI32 ? embed_vec<TI, TO, int32_t>(a, st)
+                             : embed_vec<TI, TO, int64_t>(a, st);
+}
+template <class TI>
+hipError_t embed_out(const EmbedArgs& a, hipStream_t st) {
+    return a.out_type == kF32    ? embed_id<TI, float>(a, st)
+           : a.out_type == kBF16 ? embed_id<TI, bf16_t>(a, st)
+                                 : embed_id<TI, f16_t>(a, st);
+}
+
+struct GradLayout {
+    uint32_t *k0, *k1;
+    int32_t *p0, *p1, *hist;
+    uint8_t* present;
+    float* part;
+    int ldpart;
+    size_t bytes;
+};
+GradLayout grad_layout(void* ws, int64_t rows, int64_t width, int64_t count) {
+    GradLayout L;
+    const SortPlan p = sort_plan(rows, count);
+    const int64_t nchunks = (count + chunk_len(count) - 1) / chunk_len(count);
+    L.ldpart = (int)((width + 3) / 4 * 4);
+    size_t off = 0;
+    auto take = [&](size_t n) {
+        char* q = ws ? static_cast<char*>(ws) + off : nullptr;
+        off += (n + 255) / 256 * 256;
+        return (void*)q;
+    };
+    L.k0 = (uint32_t*)take(4 * (size_t)count);
+    L.k1 = (uint32_t*)take(4 * (size_t)count);
+    L.p0 = (int32_t*)take(4 * (size_t)count);
+    L.p1 = (int32_t*)take(4 * (size_t)count);
+    L.hist = (int32_t*)take(4 * (size_t)p.nblk << p.bits);
+    L.present = (uint8_t*)take((size_t)rows);
+    L.part = (float*)take(8 * (size_t)nchunks * (size_t)L.ldpart);
+    L.bytes = off;
+    return L;
+}
+
+template <class ID>
+hipError_t sort_ids(const EmbedGradArgs& a, const GradLayout& L, const uint32_t** keys,
+                    const int32_t** pos, hipStream_t st) {
+    const SortPlan p = sort_plan(a.rows, a.count);
+    uint32_t* ko[2] = {L.k0, L.k1};
+    int32_t* po[2] = {L.p0, L.p1};
+    for (int s = 0; s < p.passes; ++s) {
+        uint32_t* kd = ko[s & 1];
+        int32_t* pd = po[s & 1];
+        const int shift = s * p.bits;
+        uint8_t* first = s == 0 ? L.present : nullptr;
+        uint8_t* final = s == p.passes - 1 ? L.present : nullptr;
+        const dim3 g((unsigned)p.nblk), b(256);
+        if (s == 0) {
+            FirstKeys<ID> src{(const ID*)a.ids, a.rows};
+            hipLaunchKernelGGL((sort_hist_kernel<FirstKeys<ID>>), g, b, 0, st, src, a.count, p.tile,
+                               shift, 1 << p.bits, L.hist, first, a.rows);
+            hipLaunchKernelGGL((sort_scatter_kernel<FirstKeys<ID>>), g, b, 0, st, src, a.count,
+                               p.tile, shift, p.bits, L.hist, kd, pd, final, a.rows);
+        } else {
+            NextKeys src{ko[(s - 1) & 1], po[(s - 1) & 1]};
+            hipLaunchKernelGGL((sort_hist_kernel<NextKeys>), g, b, 0, st, src, a.count, p.tile,
+                               shift, 1 << p.bits, L.hist, first, a.rows);
+            hipLaunchKernelGGL((sort_scatter_kernel<NextKeys>), g, b, 0, st, src, a.count, p.tile,
+                               shift, p.bits, L.hist, kd, pd, final, a.rows);
+        }
+        *keys = kd;
+        *pos = pd;
+    }
+    return hipGetLastError();
+}
+
+template <class TD, class TO, int V>
+hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
+                    const int32_t* pos, hipStream_t st) {
+    const int clen = chunk_len(a.count);
+    const int64_t nchunks = (a.count + clen - 1) / clen;
+    const int64_t nv = (a.width + V - 1) / V;
+    const int lg = log2_up(nv, 8);
+    const int64_t groups = 256 >> lg;
+    const int64_t sum_blocks = (nchunks + groups - 1) / groups;
+    int64_t fill = 0;
+    if (!a.accumulate) {
+        fill = (a.rows + groups - 1) / groups;
+        if (fill > 8192) fill = 8192;
+    }
+    const unsigned cols = (unsigned)((nv + (1 << lg) - 1) >> lg);
+    hipLaunchKernelGGL((embed_grad_sum_kernel<TD, TO, V>),
+                       dim3((unsigned)(sum_blocks + fill), cols), dim3(256), 0, st,
+                       (const TD*)a.dout, a.ldd, (int)a.width, keys, pos, a.count, clen, nchunks,
+                       (int)sum_blocks, a.scale, a.accumulate, (TO*)a.dtable, a.ldt, a.rows,
+                       L.present, L.part, L.ldpart, lg);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || nchunks < 2) return e;
+    const unsigned fy = (unsigned)((a.width + 255) / 256);
+    hipLaunchKernelGGL((embed_grad_fold_kernel<TO>), dim3((unsigned)nchunks, fy), dim3(256), 0, st,
+                       keys, a.count, clen, nchunks, a.scale, a.accumulate, (TO*)a.dtable, a.ldt,
+                       a.rows, (int)a.width, L.part, L.ldpart);
+    return hipGetLastError();
+}
+template <class TD, class TO>
+hipError_t grad_vec(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
+                    const int32_t* pos, hipStream_t st) {
+    constexpr int V = sizeof(TD) == 4 || sizeof(TO) == 4 ? 4 : 8;
+    if (vec_ok(a.dout, a.ldd, sizeof(TD), V) && vec_ok(a.dtable, a.ldt, sizeof(TO), V))
+        return grad_run<TD, TO, V>(a, L, keys, pos, st);
+    return grad_run<TD, TO, 1>(a, L, keys, pos, st);
+}
+template <class TD>
+hipError_t grad_out(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
+                    const int32_t* pos, hipStream_t st) {
+    return a.dtable_type == kF32    ? grad_vec<TD, float>(a, L, keys, pos, st)
+           : a.dtable_type == kBF16 ? grad_vec<TD, bf16_t>(a, L, keys, pos, st)
+                                    : grad_vec<TD, f16_t>(a, L, keys, pos, st);
+}
+
+// dtable = 0 where there are no tokens at all.
+template <class TO>
+__global__ __launch_bounds__(256) void zero_rows_kernel(TO* __restrict__ t, int64_t rows, int width,
+                                                        int64_t ldt) {
+    const int64_t n = rows * width;
+    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
+        t[e / width * ldt + e % width] = from_f32<TO>(0.f);
+}
+
+}  // namespace
+
+hipError_t launch_embed(const EmbedArgs& a, hipStream_t st) {
+    return a.table_type == kF32    ? embed_out<float>(a, st)
+           : a.table_type == kBF16 ? embed_out<bf16_t>(a, st)
+                                   : embed_out<f16_t>(a, st);
+}
+
+size_t embed_grad_ws_bytes(int64_t rows, int64_t width, int64_t count) {
+    if (count == 0) return 256;
+    return grad_layout(nullptr, rows, width, count).bytes;
+}
+
+hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
+    if (a.count == 0) {
+        if (a.accumulate) return hipSuccess;
+        const dim3 g(1024), b(256);
+        if (a.dtable_type == kF32)
+            hipLaunchKernelGGL((zero_rows_kernel<float>), g, b, 0, st, (float*)a.dtable, a.rows,
+                               (int)a.width, a.ldt);
+        else if (a.dtable_type == kBF16)
+            hipLaunchKernelGGL((zero_rows_kernel<bf16_t>), g, b, 0, st, (bf16_t*)a.dtable, a.rows,
+                               (int)a.width, a.ldt);
+        else
+            hipLaunchKernelGGL((zero_rows_kernel<f16_t>), g, b, 0, st, (f16_t*)a.dtable, a.rows,
+                               (int)a.width, a.ldt);
+        return hipGetLastError();
+    }
+    const GradLayout L = grad_layout(a.ws, a.rows, a.width, a.count);
+    const uint32_t* keys = nullptr;
+    const int32_t* pos = nullptr;
+    hipError_t e = a.id_type == kI32 ? sort_ids<int32_t>(a, L, &keys, &pos, st)
+                                     : sort_ids<int64_t>(a, L, &keys, &pos, st);
+    if (e != hipSuccess) return e;
+    return a.dout_type == kF32    ? grad_out<float>(a, L, keys, pos, st)
+           : a.dout_type == kBF16 ? grad_out<bf16_t>(a, L, keys, pos, st)
+                                  : grad_out<f16_t>(a, L, keys, pos, st);
+}
+
+}  // namespace symnmf

@@ -21,6 +21,7 @@
 
 #include "common.h"
 #include "kernels.h"
+#include "seq.h"
 #include "symnmf.h"
 
 using namespace symnmf;
@@ -611,7 +612,7 @@ size_t symnmf_workspace_bytes(int op, int64_t n, int32_t k_or_p, int64_t T,
             return fit_layout(nullptr, n, k_or_p, p->max_iters, p->block_rows, p->sh_pass,
                               nullptr);
         }
-        default: return 0;
+        default: return seq_workspace_bytes(op, n, k_or_p, T);
     }
 }
 
