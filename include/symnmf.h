@@ -431,7 +431,7 @@ int symnmf_gated_scan_grad(int type, int64_t batch, int64_t steps, int64_t width
  *   lse[i] = ln sum exp(scale * logits) (nullable), and the `top` (0 to 32)
  * most likely columns: top_ids[i, :] (int32, most likely first, equal logits
  * by column) with top_logp[i, :], both count x top dense. scale > 0 (1 /
- * temperature).
+ * temperature); 1 <= vocab <= 4 000 000.
  * A logit of -inf excludes its column: probability 0, never an alternative;
  * where fewer than `top` columns are left the rest is id -1 with -inf. A row
  * with no column left has lse = logp = -inf and entropy 0. A row that holds

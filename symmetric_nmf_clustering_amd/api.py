@@ -362,10 +362,32 @@ def _seq_tensor(t, name: str, types=_DTYPES, dtype=None, shape=None, device=None
 
 
 def _here(device):
-    """The stream to launch on: torch's current one, of the tensors' device."""
-    if device.index != torch.cuda.current_device():
+    """The stream to launch on: torch's current one, of the tensors' device. The
+    raw handle (0.1 us) rather than a Stream object made for the call (2.7 us,
+    a quarter of a small call)."""
+    index = torch.cuda.current_device()
+    if device.index != index:
         raise ValueError(f"the tensors are on {device}, which is not the current device")
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _rows_out(n: int, width: int, dtype, device) -> torch.Tensor:
+    # a dense n x width output (empty_strided: the cheapest allocation call)
+    return torch.empty_strided((n, width), (width, 1), dtype=dtype, device=device)
+
+
+_no_scratch: dict = {}
+
+
+def _scratch(nbytes: int, device) -> torch.Tensor:
+    """Workspace of a call. One of the least size is never touched (the query's
+    answer for "none"), so all such calls of a device share one."""
+    if nbytes > 256:
+        return workspace(nbytes, device)
+    ws = _no_scratch.get(device)
+    if ws is None:
+        ws = _no_scratch[device] = workspace(256, device)
+    return ws
 
 
 def _rows_ld(t: torch.Tensor, name: str) -> int:
@@ -425,7 +447,7 @@ def embed_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 
         flat = flat.contiguous()
     ldd = _rows_ld(flat, "dout") if flat.shape[0] else width
     ids = ids.contiguous()
-    ws = workspace(workspace_bytes(L.OP_EMBED_GRAD, rows, width, ids.numel()), dout.device)
+    ws = _scratch(workspace_bytes(L.OP_EMBED_GRAD, rows, width, ids.numel()), dout.device)
     st = L.load().symnmf_embed_grad(flat.data_ptr(), dt, ids.numel(), width, ldd, ids.data_ptr(), it,
                                     scale, int(accumulate), out.data_ptr(), ot, rows, ldo,
                                     ws.data_ptr(), ws.numel(), _here(dout.device))
@@ -477,32 +499,43 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tensor] =
     x_b, x_t = _scan_view(x, "x")
     g_b, g_t = _scan_view(gate, "gate", x)
     batch, steps, width = x.shape
-    dev = x.device
-    if batch < 1 or width < 1:
-        raise ValueError("x must have at least one batch row and one channel")
-    h = torch.empty((batch, steps, width), dtype=x.dtype, device=dev)
-    last = torch.empty((batch, width), dtype=torch.float32, device=dev)
+    h = torch.empty((batch, steps, width), dtype=x.dtype, device=x.device)
     states = None
     if return_states:
         states = torch.empty((batch, -(-steps // L.SCAN_CHUNK), width), dtype=torch.float32,
-                             device=dev)
-    ws = workspace(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
+                             device=x.device)
+    last = _scan_call(x, gate, (batch, steps, width), (x_b, x_t, g_b, g_t), lengths, h0, h, states)
+    return (h, last, states) if return_states else (h, last)
+
+
+def _scan_call(x, gate, sizes, strides, lengths, h0, h, states):
+    batch, steps, width = sizes
+    x_b, x_t, g_b, g_t = strides
+    dev = x.device
+    if batch < 1 or width < 1:
+        raise ValueError("x must have at least one batch row and one channel")
+    last = _rows_out(batch, width, torch.float32, dev)
+    ws = _scratch(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
     st = L.load().symnmf_gated_scan(
         _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
         _lengths_ptr(lengths, batch, dev), _state_ptr(h0, "h0", (batch, width), dev),
         h.data_ptr(), last.data_ptr(), None if states is None else states.data_ptr(),
         ws.data_ptr(), ws.numel(), _here(dev))
     L.check(st, "symnmf_gated_scan")
-    return (h, last, states) if return_states else (h, last)
+    return last
 
 
 def gated_step(x: torch.Tensor, gate: torch.Tensor, state: torch.Tensor):
     """One step of ``gated_scan`` for live streams: x and gate batch x width,
     state batch x width float32. Returns (h in x's type, the new state)."""
-    if x.dim() != 2 or gate.dim() != 2:
-        raise ValueError("x and gate must be batch x width")
-    h, last = gated_scan(x.unsqueeze(1), gate.unsqueeze(1), h0=state)
-    return h.squeeze(1), last
+    _seq_tensor(x, "x")
+    _seq_tensor(gate, "gate", dtype=x.dtype, shape=x.shape, device=x.device)
+    if x.dim() != 2 or (x.shape[1] > 1 and (x.stride(1) != 1 or gate.stride(1) != 1)):
+        raise ValueError("x and gate must be batch x width with unit channel stride")
+    batch, width = x.shape
+    h = _rows_out(batch, width, x.dtype, x.device)
+    strides = (x.stride(0), 0, gate.stride(0), 0) if batch > 1 else (0, 0, 0, 0)
+    return h, _scan_call(x, gate, (batch, 1, width), strides, None, state, h, None)
 
 
 def gated_scan_grad(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, dh: torch.Tensor,
@@ -522,7 +555,7 @@ def gated_scan_grad(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, d
     dx = torch.empty((batch, steps, width), dtype=x.dtype, device=dev)
     dgate = torch.empty_like(dx)
     dh0 = torch.empty((batch, width), dtype=torch.float32, device=dev)
-    ws = workspace(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
+    ws = _scratch(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
     st = L.load().symnmf_gated_scan_grad(
         _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
         _lengths_ptr(lengths, batch, dev),
@@ -571,19 +604,19 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,
     if not (scale > 0 and math.isfinite(scale)):
         raise ValueError("scale must be positive and finite")
     tokens, it = _tokens(tokens, n, dev)
-    buf = torch.empty((3, n), dtype=torch.float32, device=dev)
+    logp = torch.empty_strided((n,), (1,), dtype=torch.float32, device=dev)
+    entropy, lse = torch.empty_like(logp), torch.empty_like(logp)
     top_logp = top_ids = None
     if top:
-        top_logp = torch.empty((n, top), dtype=torch.float32, device=dev)
-        top_ids = torch.empty((n, top), dtype=torch.int32, device=dev)
-    ws = workspace(workspace_bytes(L.OP_TOKEN_LOGPROBS, vocab, top, n), dev)
-    at = buf.data_ptr()
+        top_logp = _rows_out(n, top, torch.float32, dev)
+        top_ids = _rows_out(n, top, torch.int32, dev)
+    ws = _scratch(workspace_bytes(L.OP_TOKEN_LOGPROBS, vocab, top, n), dev)
     st = L.load().symnmf_token_logprobs(
-        logits.data_ptr(), lt, n, vocab, ld, tokens.data_ptr(), it, scale, at, at + 4 * n,
-        at + 8 * n, top, top_logp.data_ptr() if top else None, top_ids.data_ptr() if top else None,
-        ws.data_ptr(), ws.numel(), _here(dev))
+        logits.data_ptr(), lt, n, vocab, ld, tokens.data_ptr(), it, scale, logp.data_ptr(),
+        entropy.data_ptr(), lse.data_ptr(), top, top_logp.data_ptr() if top else None,
+        top_ids.data_ptr() if top else None, ws.data_ptr(), ws.numel(), _here(dev))
     L.check(st, "symnmf_token_logprobs")
-    return TokenLogprobs(buf[0], buf[1], buf[2], top_logp, top_ids)
+    return TokenLogprobs(logp, entropy, lse, top_logp, top_ids)
 
 
 def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.Tensor,
@@ -611,7 +644,7 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.T
     dlogp = _row_values(dlogp, "dlogp", n, dev)
     dentropy = _row_values(dentropy, "dentropy", n, dev)
     if out is None:
-        out = torch.empty((n, vocab), dtype=logits.dtype, device=dev)
+        out = _rows_out(n, vocab, logits.dtype, dev)
     _seq_tensor(out, "out", dtype=logits.dtype, shape=logits.shape, device=dev)
     ldd = _rows_ld(out, "out")
     if out.data_ptr() == logits.data_ptr() and ldd != ld:

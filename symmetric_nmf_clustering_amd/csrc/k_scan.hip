@@ -454,8 +454,13 @@ hipError_t grad_vec(const ScanArgs& a, hipStream_t st) {
 
 }  // namespace
 
-size_t scan_ws_bytes(int64_t batch, int64_t, int64_t width) {
-    return (size_t)(2 * kMaxSeg) * 4 * (size_t)batch * (size_t)width + 256;
+// Two numbers per channel and time segment, for as many segments as plan() can
+// make: each holds two units or more, a unit kScanChunk steps or more.
+size_t scan_ws_bytes(int64_t batch, int64_t steps, int64_t width) {
+    int64_t nseg = (steps + kScanChunk - 1) / kScanChunk / 2;
+    if (nseg > kMaxSeg) nseg = kMaxSeg;
+    if (nseg < 2) return 256;
+    return (size_t)(2 * nseg) * 4 * (size_t)batch * (size_t)width;
 }
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t st) {

@@ -50,7 +50,7 @@ size_t seq_workspace_bytes(int op, int64_t n, int32_t k, int64_t T) {
             if (!scan_sizes_ok(k, T, n)) return 0;
             return scan_ws_bytes(k, T, n);
         case SYMNMF_OP_TOKEN_LOGPROBS:
-            if (n < 1 || n > kMaxCount || k < 0 || k > kMaxTop || T < 0 || T > kMaxCount) return 0;
+            if (n < 1 || n > kMaxVocab || k < 0 || k > kMaxTop || T < 0 || T > kMaxCount) return 0;
             return logprob_ws_bytes(n, k, T);
         default: return 0;
     }
@@ -167,7 +167,7 @@ int symnmf_token_logprobs(const void* logits, int type, int64_t count, int64_t v
                           float* entropy, float* lse, int32_t top, float* top_logp,
                           int32_t* top_ids, void* ws, size_t ws_bytes, void* hip_stream) {
     if (!type_ok(type) || !index_ok(token_type) || !in(count, 0, kMaxCount) ||
-        !in(vocab, 1, kMaxCount) || ld < vocab || !(scale > 0.f) || !std::isfinite(scale) ||
+        !in(vocab, 1, kMaxVocab) || ld < vocab || !(scale > 0.f) || !std::isfinite(scale) ||
         !in(top, 0, kMaxTop))
         return SYMNMF_E_INVALID;
     if (count == 0) return SYMNMF_OK;
@@ -201,7 +201,7 @@ int symnmf_token_logprobs_grad(const void* logits, int type, int64_t count, int6
                                const float* dentropy, void* dlogits, int64_t ldd,
                                void* hip_stream) {
     if (!type_ok(type) || !index_ok(token_type) || !in(count, 0, kMaxCount) ||
-        !in(vocab, 1, kMaxCount) || ld < vocab || ldd < vocab || !(scale > 0.f) ||
+        !in(vocab, 1, kMaxVocab) || ld < vocab || ldd < vocab || !(scale > 0.f) ||
         !std::isfinite(scale))
         return SYMNMF_E_INVALID;
     if (count == 0) return SYMNMF_OK;

@@ -122,6 +122,7 @@ hipError_t launch_scan(const ScanArgs& a, hipStream_t st);
 hipError_t launch_scan_grad(const ScanArgs& a, hipStream_t st);
 
 constexpr int kMaxTop = 32;  // most alternatives a row can be asked for
+constexpr int64_t kMaxVocab = 4000000;  // 64 slices of 256 KiB hold a float32 row
 
 struct LogprobArgs {
     int type;
