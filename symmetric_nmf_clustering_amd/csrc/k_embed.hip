@@ -75,10 +75,6 @@ SortPlan sort_plan(int64_t rows, int64_t count) {
     return p;
 }
 
-// Sorted entries per chunk of the sum: 32 keeps a chunk's reads in a few round
-// trips, more where there are so many tokens that the partials would grow.
-int chunk_len(int64_t count) { return count <= 65536 ? 32 : 128; }
-
 template <class ID>
 __device__ __forceinline__ uint32_t key_of(ID id, int64_t rows) {
     return id >= 0 && (int64_t)id < rows ? (uint32_t)id : (uint32_t)rows;
@@ -99,8 +95,94 @@ struct NextKeys {
     __device__ int32_t pos(int64_t i) const { return at[i]; }
 };
 
-// hist[b][digit] of block b's tile. The first pass also clears the table's
-// presence flags.
+// The next place of a digit's token in the wave's table `at` (digit -> next
+// place), for 64 tokens at once and in lane order: equal digits find each other
+// by one ballot per bit, the first of them moves the table on.
+__device__ __forceinline__ int wave_place(int32_t* at, uint32_t digits, int bits, bool on) {
+    const int d = (int)(digits & ((1u << bits) - 1u));
+    uint64_t same = __ballot(on);
+#pragma unroll
+    for (int b = 0; b < kSortMaxBits; ++b)
+        if (b < bits) {  // uniform
+            const uint64_t one = __ballot((d >> b) & 1);
+            same &= ~(one ^ (uint64_t)(int64_t)-((d >> b) & 1));
+        }
+    const int rank = __popcll(same & ((1ull << (threadIdx.x & 63)) - 1ull));
+    const int place = on ? at[d] + rank : 0;
+    wave_lds_sync();
+    if (on && rank == 0) at[d] += __popcll(same);
+    wave_lds_sync();
+    return place;
+}
+
+// Zeros over a table of `rows` rows of `row_words` 4-byte words, `ld_words`
+// apart (any type: zero is all bits clear), or of 2-byte elements where the
+// layout is not one of whole words.
+struct ZeroFill {
+    void* p;
+    int64_t rows, width, ld;  // in units of `unit` bytes
+    int unit;                 // 16, 4 or 2
+    template <class W>
+    __device__ void put(int64_t part, int64_t parts) const {
+        W zero{};
+        W* q = static_cast<W*>(p);
+        const int64_t step = parts * blockDim.x;
+        int64_t e = part * blockDim.x + threadIdx.x;
+        if (ld == width) {
+            for (; e < rows * width; e += step) q[e] = zero;
+        } else {
+            for (; e < rows * width; e += step) q[e / width * ld + e % width] = zero;
+        }
+    }
+    __device__ void run(int64_t part, int64_t parts) const {
+        if (unit == 16)
+            put<uint4>(part, parts);
+        else if (unit == 4)
+            put<uint32_t>(part, parts);
+        else
+            put<uint16_t>(part, parts);
+    }
+};
+
+constexpr int kFillRows = 8;  // rows a thread clears, their flags read together
+
+// Zeros over the rows that no token names, as 2^lx lanes a row; `words` of `unit`
+// bytes to a row.
+struct AbsentFill {
+    void* p;
+    const uint8_t* present;
+    int64_t words, ld;
+    int unit, lx;
+    int64_t rows;
+    __host__ __device__ int64_t per_block() const { return (int64_t)(256 >> lx) * kFillRows; }
+    __host__ __device__ int64_t blocks() const { return (rows + per_block() - 1) / per_block(); }
+    template <class W>
+    __device__ void put(int64_t part) const {
+        const int lane = threadIdx.x & ((1 << lx) - 1), groups = 256 >> lx;
+        const int64_t v0 = part * per_block() + (threadIdx.x >> lx);
+        uint8_t is[kFillRows];
+#pragma unroll
+        for (int u = 0; u < kFillRows; ++u)
+            is[u] = v0 + u * groups < rows ? present[v0 + u * groups] : 1;
+        W zero{};
+#pragma unroll
+        for (int u = 0; u < kFillRows; ++u)
+            if (!is[u]) {
+                W* q = static_cast<W*>(p) + (v0 + u * groups) * ld;
+                for (int64_t c = lane; c < words; c += 1 << lx) q[c] = zero;
+            }
+    }
+    __device__ void run(int64_t part) const {
+        if (unit == 16)
+            put<uint4>(part);
+        else if (unit == 4)
+            put<uint32_t>(part);
+        else
+            put<uint16_t>(part);
+    }
+};
+
+// hist[b][digit] of block b's tile. The first pass also clears the table's presence flags, which its scatter sets.
 template <class SRC>
 __global__ __launch_bounds__(256) void sort_hist_kernel(SRC src, int64_t count, int tile, int shift,
                                                         int bins, int32_t* __restrict__ hist,
@@ -135,16 +217,25 @@ __global__ __launch_bounds__(256) void sort_scatter_kernel(
     const int nblk = gridDim.x, blk = blockIdx.x;
     for (int b = t; b < 4 * kSortMaxBins; b += 256) (&at[0][0])[b] = 0;
     // this block's first place for each digit: thread t owns the digits 2t, 2t + 1
+    // (bins is even); sixteen blocks' counts in flight
     int before[2] = {0, 0}, total[2] = {0, 0};
+    if (2 * t < bins) {
+        const int2* h2 = reinterpret_cast<const int2*>(hist) + t;
+        for (int k0 = 0; k0 < nblk; k0 += 16) {
+            int2 v[16];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int b = 2 * t + u;
-        if (b < bins)
-            for (int k = 0; k < nblk; ++k) {
-                const int v = hist[(int64_t)k * bins + b];
-                total[u] += v;
-                if (k < blk) before[u] += v;
+            for (int u = 0; u < 16; ++u)
+                v[u] = k0 + u < nblk ? h2[(int64_t)(k0 + u) * (bins / 2)] : make_int2(0, 0);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                total[0] += v[u].x;
+                total[1] += v[u].y;
+                if (k0 + u < blk) {
+                    before[0] += v[u].x;
+                    before[1] += v[u].y;
+                }
             }
+        }
     }
     int incl = total[0] + total[1];
 #pragma unroll
@@ -162,8 +253,15 @@ __global__ __launch_bounds__(256) void sort_scatter_kernel(
     const int64_t lo = (int64_t)blk * tile + (int64_t)w * quarter;
     int64_t hi = lo + quarter;
     if (hi > count) hi = count;
-    for (int64_t i = lo + lane; i < hi; i += 64)
-        atomicAdd(&at[w][(src.key(i) >> shift) & (bins - 1)], 1);
+    constexpr int K = 4;  // rounds of 64 tokens whose keys are loaded together
+    for (int64_t r = lo; r < hi; r += 64 * K) {
+        uint32_t key[K];
+#pragma unroll
+        for (int u = 0; u < K; ++u) key[u] = r + 64 * u + lane < hi ? src.key(r + 64 * u + lane) : 0u;
+#pragma unroll
+        for (int u = 0; u < K; ++u)
+            if (r + 64 * u + lane < hi) atomicAdd(&at[w][(key[u] >> shift) & (bins - 1)], 1);
+    }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -178,29 +276,86 @@ __global__ __launch_bounds__(256) void sort_scatter_kernel(
         }
     }
     __syncthreads();
-    for (int64_t r = lo; r < hi; r += 64) {  // uniform over the wave
-        const int64_t i = r + lane;
-        const bool on = i < hi;
-        const uint32_t key = on ? src.key(i) : 0u;
-        const int d = (int)((key >> shift) & (uint32_t)(bins - 1));
-        uint64_t same = __ballot(on);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t one = __ballot((d >> b) & 1);
-            same &= ((d >> b) & 1) ? one : ~one;
+    for (int64_t r = lo; r < hi; r += 64 * K) {  // uniform over the wave
+        uint32_t key[K];
+        int32_t pos[K];
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+            const int64_t i = r + 64 * u + lane;
+            key[u] = i < hi ? src.key(i) : 0u;
+            pos[u] = i < hi ? src.pos(i) : 0;
         }
-        const int rank = __popcll(same & ((1ull << lane) - 1ull));
-        int place = 0;
-        if (on) place = at[w][d] + rank;
-        wave_lds_sync();
-        if (on && rank == 0) at[w][d] += __popcll(same);
-        wave_lds_sync();
-        if (on) {
-            keys_out[place] = key;
-            pos_out[place] = src.pos(i);
-            if (present && (int64_t)key < rows) present[key] = 1;
+#pragma unroll
+        for (int u = 0; u < K; ++u) {
+            const bool on = r + 64 * u + lane < hi;
+            const int place = wave_place(at[w], key[u] >> shift, bits, on);
+            if (on) {
+                keys_out[place] = key[u];
+                pos_out[place] = pos[u];
+                if (present && (int64_t)key[u] < rows) present[key[u]] = 1;
+            }
         }
     }
 }
+
+// Short lists: a token's place is the number of tokens that go before it, counted
+// directly: 16 tokens per workgroup, 16 threads to a token, every id in LDS.
+// One launch, quadratic but wide: 5000 tokens take 10.8 us, where one workgroup's
+// passes in LDS took 16.3 and the four launches of the long lists' sort 23.6. The
+// launch's other workgroups clear the table.
+constexpr int64_t kSmallCount = 8192;
+constexpr int kRankTokens = 16;
+
+template <class ID>
+__global__ __launch_bounds__(256) void sort_small_kernel(const ID* __restrict__ ids, int64_t rows,
+                                                         int count, int nblk,
+                                                         uint32_t* __restrict__ keys_out,
+                                                         int32_t* __restrict__ pos_out,
+                                                         ZeroFill zf) {
+    __shared__ __align__(16) uint32_t key[kSmallCount];
+    const int t = threadIdx.x;
+    if ((int)blockIdx.x >= nblk) {
+        zf.run((int)blockIdx.x - nblk, (int)gridDim.x - nblk);
+        return;
+    }
+    const int padded = (count + 63) / 64 * 64;  // 16 threads x 4 ids
+    for (int i0 = t; i0 < padded; i0 += 256 * 8) {
+        uint32_t k[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            k[u] = i0 + 256 * u < count ? key_of(ids[i0 + 256 * u], rows) : 0xffffffffu;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (i0 + 256 * u < padded) key[i0 + 256 * u] = k[u];
+    }
+    __syncthreads();
+    const int i = min((int)blockIdx.x * kRankTokens + (t >> 4), count - 1);
+    const bool on = (int)blockIdx.x * kRankTokens + (t >> 4) < count;
+    const uint32_t mine = key[i];
+    // equal ids stay in token order: before the four that hold i, up to `mine`
+    // counts, from there on only what is smaller (and the few between)
+    int n = 0;
+#pragma unroll 4
+    for (int j = 4 * (t & 15); j < padded; j += 64) {
+        const uint4 k = *reinterpret_cast<const uint4*>(key + j);
+        const uint32_t below = mine + (j + 4 <= i ? 1u : 0u);
+        n += (k.x < below) + (k.y < below) + (k.z < below) + (k.w < below);
+    }
+    if ((t & 15) == 0)
+        for (int j = i & ~3; j < i; ++j) n += key[j] == mine;
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+    if ((t & 15) == 0 && on) {
+        keys_out[n] = mine;
+        pos_out[n] = i;
+    }
+}
+
+// Sorted tokens per chunk of the sum. Short lists are cut finely, for enough
+// threads to hide the reads' latency; long ones coarsely, for few partials.
+int chunk_len(int64_t count) { return count <= kSmallCount ? 8 : count <= 131072 ? 32 : 128; }
+
+constexpr int kSumRows = 8;  // tokens whose rows a thread has in flight
 
 template <class TO, int V>
 __device__ __forceinline__ void put_row(TO* dst, int c, int width, const float (&acc)[V],
@@ -227,23 +382,18 @@ __device__ __forceinline__ void put_row(TO* dst, int c, int width, const float (
 }
 
 // Group of lx lanes per chunk and column tile (blockIdx.y). Blocks past the
-// chunks write the rows no token names (zeros).
+// chunks clear the rest of the rows no token names.
 template <class TD, class TO, int V>
 __global__ __launch_bounds__(256) void embed_grad_sum_kernel(
     const TD* __restrict__ dout, int64_t ldd, int width, const uint32_t* __restrict__ keys,
     const int32_t* __restrict__ pos, int64_t count, int clen, int64_t nchunks, int sum_blocks,
     float scale, int accumulate, TO* __restrict__ dtable, int64_t ldt, int64_t rows,
-    const uint8_t* __restrict__ present, float* __restrict__ part, int ldpart, int lx_log2) {
+    AbsentFill af, float* __restrict__ part, int ldpart, int lx_log2) {
     const int lx = 1 << lx_log2, groups = 256 >> lx_log2;
     const int lane = threadIdx.x & (lx - 1), grp = threadIdx.x >> lx_log2;
     const int c = ((int)blockIdx.y * lx + lane) * V;
     if ((int)blockIdx.x >= sum_blocks) {
-        const int64_t fill_blocks = gridDim.x - sum_blocks;
-        if (c >= width) return;
-        const float zero[V] = {};
-        for (int64_t v = ((int64_t)blockIdx.x - sum_blocks) * groups + grp; v < rows;
-             v += fill_blocks * groups)
-            if (!present[v]) put_row<TO, V>(dtable + v * ldt, c, width, zero, 1.f, 0);
+        if (blockIdx.y == 0) af.run((int)blockIdx.x - sum_blocks);
         return;
     }
     const int64_t chunk = (int64_t)blockIdx.x * groups + grp;
@@ -254,30 +404,48 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(
     float acc[V] = {};
     uint32_t cur = keys[lo];
     bool head = lo > 0 && keys[lo - 1] == cur;  // the first row began in an earlier chunk
-    for (int64_t e = lo; e < hi; ++e) {
-        const uint32_t key = keys[e];
-        if (key != cur) {
-            if (head) {
+    for (int64_t e0 = lo; e0 < hi; e0 += kSumRows) {
+        // the rows of kSumRows tokens on their way together
+        uint32_t key[kSumRows];
+        int32_t at[kSumRows];
+        Vec<TD, V> v[kSumRows];
 #pragma unroll
-                for (int u = 0; u < V; ++u)
-                    if (c + u < width) part[2 * chunk * ldpart + c + u] = acc[u];
-            } else if ((int64_t)cur < rows) {
-                put_row<TO, V>(dtable + (int64_t)cur * ldt, c, width, acc, scale, accumulate);
-            }
-            head = false;
-            cur = key;
-#pragma unroll
-            for (int u = 0; u < V; ++u) acc[u] = 0.f;
+        for (int q = 0; q < kSumRows; ++q) {
+            key[q] = e0 + q < hi ? keys[e0 + q] : (uint32_t)rows;
+            at[q] = e0 + q < hi ? pos[e0 + q] : 0;
         }
-        if ((int64_t)cur >= rows) break;  // the empty slots, sorted last
-        const TD* src = dout + (int64_t)pos[e] * ldd;
-        if (whole) {
-            const Vec<TD, V> v = load_vec<TD, V>(src + c);
 #pragma unroll
-            for (int u = 0; u < V; ++u) acc[u] += to_f32(v.e[u]);
-        } else {
-            for (int u = 0; u < V; ++u)
-                if (c + u < width) acc[u] += to_f32(src[c + u]);
+        for (int q = 0; q < kSumRows; ++q) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[q].e[u] = from_f32<TD>(0.f);
+            if ((int64_t)key[q] < rows) {
+                const TD* src = dout + (int64_t)at[q] * ldd + c;
+                if (whole) {
+                    v[q] = load_vec<TD, V>(src);
+                } else {
+                    for (int u = 0; u < V; ++u)
+                        if (c + u < width) v[q].e[u] = src[u];
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kSumRows; ++q) {
+            if (e0 + q >= hi) break;
+            if (key[q] != cur) {
+                if (head) {
+#pragma unroll
+                    for (int u = 0; u < V; ++u)
+                        if (c + u < width) part[2 * chunk * ldpart + c + u] = acc[u];
+                } else if ((int64_t)cur < rows) {
+                    put_row<TO, V>(dtable + (int64_t)cur * ldt, c, width, acc, scale, accumulate);
+                }
+                head = false;
+                cur = key[q];
+#pragma unroll
+                for (int u = 0; u < V; ++u) acc[u] = 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < V; ++u) acc[u] += to_f32(v[q].e[u]);
         }
     }
     if ((int64_t)cur >= rows) return;
@@ -298,7 +466,7 @@ template <class TO>
 __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
     const uint32_t* __restrict__ keys, int64_t count, int clen, int64_t nchunks, float scale,
     int accumulate, TO* __restrict__ dtable, int64_t ldt, int64_t rows, int width,
-    const float* __restrict__ part, int ldpart) {
+    const float* __restrict__ part, int ldpart, int vec) {
     const int64_t chunk = blockIdx.x;
     const int64_t lo = chunk * clen, hi = lo + clen;
     if (hi >= count) return;
@@ -313,11 +481,36 @@ __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
         more += n;
         if (n < 256) break;
     }
-    for (int c = blockIdx.y * 256 + threadIdx.x; c < width; c += gridDim.y * 256) {
-        float s[1] = {part[(2 * chunk + 1) * ldpart + c] +
-                      ordered_strided_sum(part + 2 * (chunk + 1) * ldpart + c,
-                                          (int)more, 2 * (int64_t)ldpart)};
-        put_row<TO, 1>(dtable + (int64_t)key * ldt, c, width, s, scale, accumulate);
+    const int64_t step = 2 * (int64_t)ldpart;
+    for (int c = (blockIdx.y * 256 + threadIdx.x) * 4; c < width; c += gridDim.y * 1024) {
+        // 16 partials in flight, added in order; rows of partials are padded to
+        // a multiple of 4 (what the padding holds is not stored)
+        const float* p = part + 2 * (chunk + 1) * (int64_t)ldpart + c;
+        float4 s = *reinterpret_cast<const float4*>(part + (2 * chunk + 1) * (int64_t)ldpart + c);
+        for (int64_t j = 0; j < more; j += 16) {
+            float4 v[16];
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                if (j + u < more) v[u] = *reinterpret_cast<const float4*>(p + (j + u) * step);
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+                if (j + u < more) {
+                    s.x += v[u].x;
+                    s.y += v[u].y;
+                    s.z += v[u].z;
+                    s.w += v[u].w;
+                }
+        }
+        const float r[4] = {s.x, s.y, s.z, s.w};
+        TO* dst = dtable + (int64_t)key * ldt;
+        if (vec) {
+            put_row<TO, 4>(dst, c, width, r, scale, accumulate);
+        } else {
+            for (int u = 0; u < 4; ++u) {
+                const float one[1] = {r[u]};
+                if (c + u < width) put_row<TO, 1>(dst, c + u, width, one, scale, accumulate);
+            }
+        }
     }
 }
 
@@ -381,17 +574,63 @@ GradLayout grad_layout(void* ws, int64_t rows, int64_t width, int64_t count) {
     L.k1 = (uint32_t*)take(4 * (size_t)count);
     L.p0 = (int32_t*)take(4 * (size_t)count);
     L.p1 = (int32_t*)take(4 * (size_t)count);
-    L.hist = (int32_t*)take(4 * (size_t)p.nblk << p.bits);
-    L.present = (uint8_t*)take((size_t)rows);
+    const bool small = count <= kSmallCount;
+    L.hist = (int32_t*)take(small ? 0 : 4 * (size_t)p.nblk << p.bits);
+    L.present = (uint8_t*)take(small ? 0 : (size_t)rows);
     L.part = (float*)take(8 * (size_t)nchunks * (size_t)L.ldpart);
     L.bytes = off;
     return L;
+}
+
+ZeroFill zero_fill(const EmbedGradArgs& a) {
+    const int eb = dtype_bytes(a.dtable_type);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.dtable);
+    ZeroFill z{a.dtable, a.rows, a.width, a.ldt, eb};
+    if (a.ldt == a.width && a.rows * a.width * eb % 16 == 0) {  // one run of memory
+        z.width = a.rows * a.width;
+        z.rows = 1;
+        z.ld = z.width;
+    }
+    for (int u = 16; u > eb; u /= 2)
+        if (u != 8 && at % u == 0 && z.width * eb % u == 0 && (z.rows == 1 || z.ld * eb % u == 0)) {
+            z.width = z.width * eb / u;
+            z.ld = z.ld * eb / u;
+            z.unit = u;
+            break;
+        }
+    return z;
+}
+
+// The rows to clear one by one (none when adding, or where a short list's sort
+// clears the whole table).
+AbsentFill absent_fill(const EmbedGradArgs& a, const uint8_t* present) {
+    const int eb = dtype_bytes(a.dtable_type);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(a.dtable);
+    int unit = eb;
+    for (int u : {4, 16})
+        if (u > eb && at % u == 0 && a.width * eb % u == 0 && a.ldt * eb % u == 0) unit = u;
+    AbsentFill f{a.dtable, present, a.width * eb / unit, a.ldt * eb / unit, unit, 0, 0};
+    f.lx = log2_up(f.words, 8);
+    f.rows = a.accumulate || a.count <= kSmallCount ? 0 : a.rows;
+    return f;
 }
 
 template <class ID>
 hipError_t sort_ids(const EmbedGradArgs& a, const GradLayout& L, const uint32_t** keys,
                     const int32_t** pos, hipStream_t st) {
     const SortPlan p = sort_plan(a.rows, a.count);
+    if (a.count <= kSmallCount) {
+        const ZeroFill zf = zero_fill(a);
+        const int nblk = (int)((a.count + kRankTokens - 1) / kRankTokens);
+        // a workgroup per 16 KiB to clear, up to sixteen per CU
+        int64_t fill = a.accumulate ? 0 : (zf.rows * zf.width * zf.unit + 16383) / 16384;
+        if (fill > 4096) fill = 4096;
+        hipLaunchKernelGGL((sort_small_kernel<ID>), dim3((unsigned)(nblk + fill)), dim3(256), 0, st,
+                           (const ID*)a.ids, a.rows, (int)a.count, nblk, L.k0, L.p0, zf);
+        *keys = L.k0;
+        *pos = L.p0;
+        return hipGetLastError();
+    }
     uint32_t* ko[2] = {L.k0, L.k1};
     int32_t* po[2] = {L.p0, L.p1};
     for (int s = 0; s < p.passes; ++s) {
@@ -399,20 +638,19 @@ hipError_t sort_ids(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
         int32_t* pd = po[s & 1];
         const int shift = s * p.bits;
         uint8_t* first = s == 0 ? L.present : nullptr;
-        uint8_t* final = s == p.passes - 1 ? L.present : nullptr;
         const dim3 g((unsigned)p.nblk), b(256);
         if (s == 0) {
             FirstKeys<ID> src{(const ID*)a.ids, a.rows};
             hipLaunchKernelGGL((sort_hist_kernel<FirstKeys<ID>>), g, b, 0, st, src, a.count, p.tile,
                                shift, 1 << p.bits, L.hist, first, a.rows);
             hipLaunchKernelGGL((sort_scatter_kernel<FirstKeys<ID>>), g, b, 0, st, src, a.count,
-                               p.tile, shift, p.bits, L.hist, kd, pd, final, a.rows);
+                               p.tile, shift, p.bits, L.hist, kd, pd, first, a.rows);
         } else {
             NextKeys src{ko[(s - 1) & 1], po[(s - 1) & 1]};
             hipLaunchKernelGGL((sort_hist_kernel<NextKeys>), g, b, 0, st, src, a.count, p.tile,
                                shift, 1 << p.bits, L.hist, first, a.rows);
             hipLaunchKernelGGL((sort_scatter_kernel<NextKeys>), g, b, 0, st, src, a.count, p.tile,
-                               shift, p.bits, L.hist, kd, pd, final, a.rows);
+                               shift, p.bits, L.hist, kd, pd, first, a.rows);
         }
         *keys = kd;
         *pos = pd;
@@ -422,56 +660,49 @@ hipError_t sort_ids(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
 
 template <class TD, class TO, int V>
 hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
-                    const int32_t* pos, hipStream_t st) {
+                    const int32_t* pos, const AbsentFill& af, hipStream_t st) {
     const int clen = chunk_len(a.count);
     const int64_t nchunks = (a.count + clen - 1) / clen;
     const int64_t nv = (a.width + V - 1) / V;
     const int lg = log2_up(nv, 8);
     const int64_t groups = 256 >> lg;
     const int64_t sum_blocks = (nchunks + groups - 1) / groups;
-    int64_t fill = 0;
-    if (!a.accumulate) {
-        fill = (a.rows + groups - 1) / groups;
-        if (fill > 8192) fill = 8192;
-    }
+    const int64_t fill = af.blocks();
     const unsigned cols = (unsigned)((nv + (1 << lg) - 1) >> lg);
     hipLaunchKernelGGL((embed_grad_sum_kernel<TD, TO, V>),
                        dim3((unsigned)(sum_blocks + fill), cols), dim3(256), 0, st,
                        (const TD*)a.dout, a.ldd, (int)a.width, keys, pos, a.count, clen, nchunks,
                        (int)sum_blocks, a.scale, a.accumulate, (TO*)a.dtable, a.ldt, a.rows,
-                       L.present, L.part, L.ldpart, lg);
+                       af, L.part, L.ldpart, lg);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || nchunks < 2) return e;
-    const unsigned fy = (unsigned)((a.width + 255) / 256);
+    const unsigned fy = (unsigned)((a.width + 1023) / 1024);
+    const int vec = vec_ok(a.dtable, a.ldt, sizeof(TO), 4);
     hipLaunchKernelGGL((embed_grad_fold_kernel<TO>), dim3((unsigned)nchunks, fy), dim3(256), 0, st,
                        keys, a.count, clen, nchunks, a.scale, a.accumulate, (TO*)a.dtable, a.ldt,
-                       a.rows, (int)a.width, L.part, L.ldpart);
+                       a.rows, (int)a.width, L.part, L.ldpart, vec);
     return hipGetLastError();
 }
 template <class TD, class TO>
 hipError_t grad_vec(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
-                    const int32_t* pos, hipStream_t st) {
+                    const int32_t* pos, const AbsentFill& af, hipStream_t st) {
+    // float32 on either side: 4 elements a thread, so more threads share a row's
+    // reads (bf16 rows of 1024 into a float32 table: 125 us against 136 with 8)
     constexpr int V = sizeof(TD) == 4 || sizeof(TO) == 4 ? 4 : 8;
     if (vec_ok(a.dout, a.ldd, sizeof(TD), V) && vec_ok(a.dtable, a.ldt, sizeof(TO), V))
-        return grad_run<TD, TO, V>(a, L, keys, pos, st);
-    return grad_run<TD, TO, 1>(a, L, keys, pos, st);
+        return grad_run<TD, TO, V>(a, L, keys, pos, af, st);
+    return grad_run<TD, TO, 1>(a, L, keys, pos, af, st);
 }
 template <class TD>
 hipError_t grad_out(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
-                    const int32_t* pos, hipStream_t st) {
-    return a.dtable_type == kF32    ? grad_vec<TD, float>(a, L, keys, pos, st)
-           : a.dtable_type == kBF16 ? grad_vec<TD, bf16_t>(a, L, keys, pos, st)
-                                    : grad_vec<TD, f16_t>(a, L, keys, pos, st);
+                    const int32_t* pos, const AbsentFill& af, hipStream_t st) {
+    return a.dtable_type == kF32    ? grad_vec<TD, float>(a, L, keys, pos, af, st)
+           : a.dtable_type == kBF16 ? grad_vec<TD, bf16_t>(a, L, keys, pos, af, st)
+                                    : grad_vec<TD, f16_t>(a, L, keys, pos, af, st);
 }
 
 // dtable = 0 where there are no tokens at all.
-template <class TO>
-__global__ __launch_bounds__(256) void zero_rows_kernel(TO* __restrict__ t, int64_t rows, int width,
-                                                        int64_t ldt) {
-    const int64_t n = rows * width;
-    for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256)
-        t[e / width * ldt + e % width] = from_f32<TO>(0.f);
-}
+__global__ __launch_bounds__(256) void zero_kernel(ZeroFill zf) { zf.run(blockIdx.x, gridDim.x); }
 
 }  // namespace
 
@@ -489,27 +720,19 @@ size_t embed_grad_ws_bytes(int64_t rows, int64_t width, int64_t count) {
 hipError_t launch_embed_grad(const EmbedGradArgs& a, hipStream_t st) {
     if (a.count == 0) {
         if (a.accumulate) return hipSuccess;
-        const dim3 g(1024), b(256);
-        if (a.dtable_type == kF32)
-            hipLaunchKernelGGL((zero_rows_kernel<float>), g, b, 0, st, (float*)a.dtable, a.rows,
-                               (int)a.width, a.ldt);
-        else if (a.dtable_type == kBF16)
-            hipLaunchKernelGGL((zero_rows_kernel<bf16_t>), g, b, 0, st, (bf16_t*)a.dtable, a.rows,
-                               (int)a.width, a.ldt);
-        else
-            hipLaunchKernelGGL((zero_rows_kernel<f16_t>), g, b, 0, st, (f16_t*)a.dtable, a.rows,
-                               (int)a.width, a.ldt);
+        hipLaunchKernelGGL(zero_kernel, dim3(1024), dim3(256), 0, st, zero_fill(a));
         return hipGetLastError();
     }
     const GradLayout L = grad_layout(a.ws, a.rows, a.width, a.count);
     const uint32_t* keys = nullptr;
     const int32_t* pos = nullptr;
+    AbsentFill af = absent_fill(a, L.present);
     hipError_t e = a.id_type == kI32 ? sort_ids<int32_t>(a, L, &keys, &pos, st)
                                      : sort_ids<int64_t>(a, L, &keys, &pos, st);
     if (e != hipSuccess) return e;
-    return a.dout_type == kF32    ? grad_out<float>(a, L, keys, pos, st)
-           : a.dout_type == kBF16 ? grad_out<bf16_t>(a, L, keys, pos, st)
-                                  : grad_out<f16_t>(a, L, keys, pos, st);
+    return a.dout_type == kF32    ? grad_out<float>(a, L, keys, pos, af, st)
+           : a.dout_type == kBF16 ? grad_out<bf16_t>(a, L, keys, pos, af, st)
+                                  : grad_out<f16_t>(a, L, keys, pos, af, st);
 }
 
 }  // namespace symnmf
