@@ -525,11 +525,12 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
 // ---- gradient ----------------------------------------------------------------------
 
 // dlogits_j = scale (w ([j = tok] - p_j) - q p_j (logp_j + H)), w = dlogp (0
-// without a token), q = dentropy. grid: (column tiles, rows).
+// without a token), q = dentropy. grid: (column tiles, groups of rows).
+// Rows of few columns share a workgroup, 2^lx lanes to each.
 template <class T>
-__global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int aligned) {
+__global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int aligned, int lx) {
     constexpr int V = 16 / sizeof(T);
-    const int64_t row = (int64_t)blockIdx.y + (int64_t)blockIdx.z * 65535;
+    const int64_t row = ((int64_t)blockIdx.y << (8 - lx)) + (threadIdx.x >> lx);
     if (row >= p.count) return;
     const T* z = (const T*)p.logits + row * p.ld;
     T* d = (T*)p.dlogits + row * p.ldd;
@@ -547,8 +548,8 @@ __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int al
         if (c == tok) g += w;
         return empty ? 0.f : scale * g;
     };
-    const int64_t step = (int64_t)gridDim.x * 256 * V;
-    for (int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V - sh; c < p.vocab; c += step) {
+    const int64_t step = ((int64_t)gridDim.x << lx) * V;
+    for (int64_t c = (((int64_t)blockIdx.x << lx) + (threadIdx.x & ((1 << lx) - 1))) * V - sh; c < p.vocab; c += step) {
         if (aligned && c >= 0 && c + V <= p.vocab) {
             const Vec<T, V> v = load_vec<T, V>(z + c);
             Vec<T, V> o;
@@ -622,13 +623,29 @@ hipError_t grad_run(const LogprobArgs& a, hipStream_t st) {
     const int aligned =
         reinterpret_cast<uintptr_t>(a.logits) % 16 == reinterpret_cast<uintptr_t>(a.dlogits) % 16 &&
         (a.ld - a.ldd) % V == 0;
-    int64_t tiles = (a.vocab + V + 256 * V * 4 - 1) / (256 * V * 4);
-    if (tiles < 1) tiles = 1;
-    const unsigned gy = (unsigned)(a.count < 65535 ? a.count : 65535);
-    const unsigned gz = (unsigned)((a.count + 65534) / 65535);
-    hipLaunchKernelGGL((logprob_grad_kernel<T>), dim3((unsigned)tiles, gy, gz), dim3(256), 0, st, a,
-                       aligned);
-    return hipGetLastError();
+    const int64_t vecs = (a.vocab + V - 1 + V - 1) / V;  // whatever the row's alignment
+    int lx = 0;
+    while (lx < 8 && ((int64_t)1 << lx) < vecs) ++lx;
+    const int64_t tiles = (vecs + 1023) / 1024, rows = (a.count + (256 >> lx) - 1) >> (8 - lx);
+    // rows in a grid dimension of at most 65535: the rest in further launches
+    for (int64_t r = 0; r < rows; r += 65535) {
+        LogprobArgs q = a;
+        const int64_t skip = r << (8 - lx);
+        q.count -= skip;
+        q.logits = (const T*)a.logits + skip * a.ld;
+        q.dlogits = (T*)a.dlogits + skip * a.ldd;
+        q.tokens = (const char*)a.tokens + skip * (a.token_type == kI32 ? 4 : 8);
+        q.lse += skip;
+        if (q.entropy) q.entropy += skip;
+        q.dlogp += skip;
+        if (q.dentropy) q.dentropy += skip;
+        const int64_t n = rows - r < 65535 ? rows - r : 65535;
+        hipLaunchKernelGGL((logprob_grad_kernel<T>), dim3((unsigned)tiles, (unsigned)n), dim3(256),
+                           0, st, q, aligned, lx);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
