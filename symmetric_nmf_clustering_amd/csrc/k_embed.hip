@@ -32,22 +32,22 @@ __global__ __launch_bounds__(256) void embed_kernel(const TI* __restrict__ table
     const float fill = id < 0 ? 0.f : __builtin_nanf("");
     const TI* src = table + (in ? id : 0) * ldt;
     TO* dst = out + i * ldo;
-    for (int c = lane * V; c < width; c += lx * V) {
-        if (V == 1 || c + V <= width) {
-            Vec<TO, V> o;
-            if (in) {
-                const Vec<TI, V> v = load_vec<TI, V>(src + c);
+    if (width < V) {
+        for (int c = lane; c < width; c += lx) dst[c] = from_f32<TO>(in ? to_f32(src[c]) * scale : fill);
+        return;
+    }
+    for (int c0 = lane * V; c0 < width; c0 += lx * V) {
+        const int c = min(c0, width - V);  // the last access of a row ends with it
+        Vec<TO, V> o;
+        if (in) {
+            const Vec<TI, V> v = load_vec<TI, V>(src + c);
 #pragma unroll
-                for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(to_f32(v.e[u]) * scale);
-            } else {
-#pragma unroll
-                for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(fill);
-            }
-            store_vec<TO, V>(dst + c, o);
+            for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(to_f32(v.e[u]) * scale);
         } else {
-            for (int u = c; u < width; ++u)
-                dst[u] = from_f32<TO>(in ? to_f32(src[u]) * scale : fill);
+#pragma unroll
+            for (int u = 0; u < V; ++u) o.e[u] = from_f32<TO>(fill);
         }
+        store_vec<TO, V>(dst + c, o);
     }
 }
 
@@ -360,7 +360,7 @@ constexpr int kSumRows = 8;  // tokens whose rows a thread has in flight
 template <class TO, int V>
 __device__ __forceinline__ void put_row(TO* dst, int c, int width, const float (&acc)[V],
                                         float scale, int accumulate) {
-    if (V == 1 || c + V <= width) {
+    if (c + V <= width) {
         Vec<TO, V> o;
         if (accumulate) {
             const Vec<TO, V> old = load_vec<TO, V>(dst + c);
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(
     if (chunk >= nchunks || c >= width) return;
     const int64_t lo = chunk * clen;
     const int64_t hi = lo + clen < count ? lo + clen : count;
-    const bool whole = V == 1 || c + V <= width;
+    const bool whole = c + V <= width;
     float acc[V] = {};
     uint32_t cur = keys[lo];
     bool head = lo > 0 && keys[lo - 1] == cur;  // the first row began in an earlier chunk
@@ -466,7 +466,7 @@ template <class TO>
 __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
     const uint32_t* __restrict__ keys, int64_t count, int clen, int64_t nchunks, float scale,
     int accumulate, TO* __restrict__ dtable, int64_t ldt, int64_t rows, int width,
-    const float* __restrict__ part, int ldpart, int vec) {
+    const float* __restrict__ part, int ldpart) {
     const int64_t chunk = blockIdx.x;
     const int64_t lo = chunk * clen, hi = lo + clen;
     if (hi >= count) return;
@@ -502,15 +502,7 @@ __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
                 }
         }
         const float r[4] = {s.x, s.y, s.z, s.w};
-        TO* dst = dtable + (int64_t)key * ldt;
-        if (vec) {
-            put_row<TO, 4>(dst, c, width, r, scale, accumulate);
-        } else {
-            for (int u = 0; u < 4; ++u) {
-                const float one[1] = {r[u]};
-                if (c + u < width) put_row<TO, 1>(dst, c + u, width, one, scale, accumulate);
-            }
-        }
+        put_row<TO, 4>(dtable + (int64_t)key * ldt, c, width, r, scale, accumulate);
     }
 }
 
@@ -519,12 +511,9 @@ inline int log2_up(int64_t v, int most) {
     while (l < most && (int64_t(1) << l) < v) ++l;
     return l;
 }
-inline bool vec_ok(const void* p, int64_t ld, int bytes, int v) {
-    return reinterpret_cast<uintptr_t>(p) % (size_t)(bytes * v) == 0 && ld % v == 0;
-}
-
-template <class TI, class TO, class ID, int V>
+template <class TI, class TO, class ID>
 hipError_t embed_run(const EmbedArgs& a, hipStream_t st) {
+    constexpr int V = sizeof(TI) == 4 || sizeof(TO) == 4 ? 4 : 8;
     const int lg = log2_up((a.width + V - 1) / V, 8);
     const int64_t per = 256 >> lg;
     hipLaunchKernelGGL((embed_kernel<TI, TO, ID, V>), dim3((unsigned)((a.count + per - 1) / per)),
@@ -532,17 +521,10 @@ hipError_t embed_run(const EmbedArgs& a, hipStream_t st) {
                        (const ID*)a.ids, a.count, a.scale, (TO*)a.out, a.ldo, lg);
     return hipGetLastError();
 }
-template <class TI, class TO, class ID>
-hipError_t embed_vec(const EmbedArgs& a, hipStream_t st) {
-    constexpr int V = sizeof(TI) == 4 || sizeof(TO) == 4 ? 4 : 8;
-    if (vec_ok(a.table, a.ldt, sizeof(TI), V) && vec_ok(a.out, a.ldo, sizeof(TO), V))
-        return embed_run<TI, TO, ID, V>(a, st);
-    return embed_run<TI, TO, ID, 1>(a, st);
-}
 template <class TI, class TO>
 hipError_t embed_id(const EmbedArgs& a, hipStream_t st) {
-    return a.id_type == kI32 ? embed_vec<TI, TO, int32_t>(a, st)
-                             : embed_vec<TI, TO, int64_t>(a, st);
+    return a.id_type == kI32 ? embed_run<TI, TO, int32_t>(a, st)
+                             : embed_run<TI, TO, int64_t>(a, st);
 }
 template <class TI>
 hipError_t embed_out(const EmbedArgs& a, hipStream_t st) {
@@ -658,9 +640,12 @@ hipError_t sort_ids(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
     return hipGetLastError();
 }
 
-template <class TD, class TO, int V>
+template <class TD, class TO>
 hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
                     const int32_t* pos, const AbsentFill& af, hipStream_t st) {
+    // float32 on either side: 4 elements a thread, so more threads share a row's
+    // reads (bf16 rows of 1024 into a float32 table: 125 us against 136 with 8)
+    constexpr int V = sizeof(TD) == 4 || sizeof(TO) == 4 ? 4 : 8;
     const int clen = chunk_len(a.count);
     const int64_t nchunks = (a.count + clen - 1) / clen;
     const int64_t nv = (a.width + V - 1) / V;
@@ -677,28 +662,17 @@ hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || nchunks < 2) return e;
     const unsigned fy = (unsigned)((a.width + 1023) / 1024);
-    const int vec = vec_ok(a.dtable, a.ldt, sizeof(TO), 4);
     hipLaunchKernelGGL((embed_grad_fold_kernel<TO>), dim3((unsigned)nchunks, fy), dim3(256), 0, st,
                        keys, a.count, clen, nchunks, a.scale, a.accumulate, (TO*)a.dtable, a.ldt,
-                       a.rows, (int)a.width, L.part, L.ldpart, vec);
+                       a.rows, (int)a.width, L.part, L.ldpart);
     return hipGetLastError();
-}
-template <class TD, class TO>
-hipError_t grad_vec(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
-                    const int32_t* pos, const AbsentFill& af, hipStream_t st) {
-    // float32 on either side: 4 elements a thread, so more threads share a row's
-    // reads (bf16 rows of 1024 into a float32 table: 125 us against 136 with 8)
-    constexpr int V = sizeof(TD) == 4 || sizeof(TO) == 4 ? 4 : 8;
-    if (vec_ok(a.dout, a.ldd, sizeof(TD), V) && vec_ok(a.dtable, a.ldt, sizeof(TO), V))
-        return grad_run<TD, TO, V>(a, L, keys, pos, af, st);
-    return grad_run<TD, TO, 1>(a, L, keys, pos, af, st);
 }
 template <class TD>
 hipError_t grad_out(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
                     const int32_t* pos, const AbsentFill& af, hipStream_t st) {
-    return a.dtable_type == kF32    ? grad_vec<TD, float>(a, L, keys, pos, af, st)
-           : a.dtable_type == kBF16 ? grad_vec<TD, bf16_t>(a, L, keys, pos, af, st)
-                                    : grad_vec<TD, f16_t>(a, L, keys, pos, af, st);
+    return a.dtable_type == kF32    ? grad_run<TD, float>(a, L, keys, pos, af, st)
+           : a.dtable_type == kBF16 ? grad_run<TD, bf16_t>(a, L, keys, pos, af, st)
+                                    : grad_run<TD, f16_t>(a, L, keys, pos, af, st);
 }
 
 // dtable = 0 where there are no tokens at all.

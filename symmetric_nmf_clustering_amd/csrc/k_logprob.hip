@@ -84,13 +84,15 @@ __device__ __forceinline__ Cand wave_best(Cand c, int& lane) {
     return r;
 }
 
-// How many of the candidates of lanes 0 .. n - 1 are better than this lane's.
-__device__ __forceinline__ int rank_among(Cand c, int n) {
+// How many of the candidates of lanes 0, step, 2 step, ... (n of them) are better
+// than this lane's.
+__device__ __forceinline__ int rank_among(Cand c, int n, int step = 1) {
+    const uint64_t key = (uint64_t)c.ord << 32 | (uint32_t)~c.idx;
     int r = 0;
-    for (int j = 0; j < n; ++j) {
-        const Cand o{(uint32_t)__builtin_amdgcn_readlane((int)c.ord, j),
-                     (uint32_t)__builtin_amdgcn_readlane((int)c.idx, j)};
-        r += better(o, c);
+    for (int j = 0; j < n * step; j += step) {
+        const uint32_t ord = (uint32_t)__builtin_amdgcn_readlane((int)c.ord, j);
+        const uint32_t idx = (uint32_t)__builtin_amdgcn_readlane((int)c.idx, j);
+        r += ((uint64_t)ord << 32 | (uint32_t)~idx) > key;
     }
     return r;
 }
@@ -102,12 +104,13 @@ __device__ __forceinline__ Cand of_rank(Cand c, int rank, int r) {
     return Cand{(uint32_t)__builtin_amdgcn_readlane((int)c.ord, l),
                 (uint32_t)__builtin_amdgcn_readlane((int)c.idx, l)};
 }
-// Appends the candidates of the lanes whose `on` is set to a list of 64 in LDS;
-// returns the list's new length (past 64: it did not fit).
+// Appends the candidates of the lanes whose `on` is set to a list of kFew in LDS;
+// returns the list's new length (past kFew: it did not fit).
+constexpr int kFew = 64;
 __device__ __forceinline__ int append(Cand* list, int n, bool on, Cand c) {
     const uint64_t m = __ballot(on);
     const int at = n + __popcll(m & ((1ull << (threadIdx.x & 63)) - 1ull));
-    if (on && at < 64) list[at] = c;
+    if (on && at < kFew) list[at] = c;
     return n + __popcll(m);
 }
 
@@ -183,33 +186,32 @@ __device__ __forceinline__ void put_top(const RowOut& o, const Stat& a, float sc
 
 // ---- long rows -------------------------------------------------------------------
 
-// A slice of a row per workgroup. Groups start at addresses that a vector load
-// can take: group q holds the columns [8 q - sh, 8 q - sh + 8), sh the row
-// start's distance (in elements) from the last such address; the first and
-// the last group may be partial and are read element by element.
-//
-// Each thread takes four groups (of a tile of 1024) at a time, the next four
-// already on their way. Group maxima are kept in the logits' own type (exact).
-template <class T>
+// WAVES waves per (row, slice): a workgroup has 4 / WAVES of them. Each thread
+// takes four groups (of a tile of 256 WAVES) at a time, the next four already
+// on their way; a row's last group may be partial and is read element by
+// element. Group maxima are kept in the logits' own type (exact).
+template <class T, int WAVES>
 __global__ __launch_bounds__(256) void logprob_slice_kernel(
-    const T* __restrict__ logits, int64_t vocab, int64_t ld, float scale, int groups_per_slice,
-    int nslice, int top, Stat* __restrict__ part, Cand* __restrict__ cand, RowOut out) {
+    const T* __restrict__ logits, int64_t items, int64_t vocab, int64_t ld, float scale,
+    int groups_per_slice, int nslice, int top, Stat* __restrict__ part, Cand* __restrict__ cand,
+    RowOut out) {
     extern __shared__ __align__(16) char smem[];
     __shared__ Stat wst[4];
-    __shared__ Cand lead[256];
-    constexpr int V = 16 / sizeof(T), NV = kGroup / V, Q = 4;
-    T* gmax = reinterpret_cast<T*>(smem);
-    const int t = threadIdx.x, lane = t & 63, w = t >> 6;
-    const int64_t row = blockIdx.x / nslice;
-    const int slice = blockIdx.x % nslice;
+    constexpr int V = 16 / sizeof(T), NV = kGroup / V, Q = 4, N = 64 * WAVES;
+    __shared__ Cand leads[4 / WAVES][N > 2 * kFew ? N : 2 * kFew];
+    const int slot = threadIdx.x / N, t = threadIdx.x % N, lane = t & 63, w = t >> 6;
+    const int64_t item = (int64_t)blockIdx.x * (4 / WAVES) + slot;
+    if (item >= items) return;  // whole waves, and with several to an item whole workgroups
+    T* gmax = reinterpret_cast<T*>(smem) + (int64_t)slot * groups_per_slice;
+    Cand* lead = leads[slot];
+    const int64_t row = item / nslice;
+    const int slice = (int)(item % nslice);
     const T* z = logits + row * ld;
-    const int sh = (int)((reinterpret_cast<uintptr_t>(z) % 16) / sizeof(T));
-    const int64_t all = (vocab + sh + kGroup - 1) / kGroup;
+    const int64_t all = (vocab + kGroup - 1) / kGroup;
     const int64_t g_lo = (int64_t)slice * groups_per_slice;
-    const int ng = (int)(all - g_lo < groups_per_slice ? all - g_lo : groups_per_slice);
-    const T* zs = z + g_lo * kGroup - sh;  // group g of the slice begins at zs + 8 g
-    const int g_first = slice == 0 && sh ? 1 : 0;
-    const int g_end = g_lo + ng == all && (vocab + sh) % kGroup ? ng - 1 : ng;
+    const int ng = (int)max((int64_t)0, min(all - g_lo, (int64_t)groups_per_slice));
+    const T* zs = z + g_lo * kGroup;  // group g of the slice begins at zs + 8 g
+    const int g_end = ng > 0 && g_lo + ng == all && vocab % kGroup ? ng - 1 : ng;
     const float k = scale * kLog2e;
     Stat a = stat_none();
     Cand mine{0, 0};
@@ -218,11 +220,10 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
     auto fetch = [&](Vec<T, V>(&to)[Q][NV], int g0) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const int g = g0 + q * 256;
-            const bool in = g >= g_first && g < g_end;
+            const int g = g0 + q * N;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                if (in) {
+                if (g < g_end) {
                     to[q][i] = load_vec<T, V>(zs + (int64_t)g * kGroup + i * V);
                 } else {
 #pragma unroll
@@ -245,8 +246,8 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
         mine = best_of(Cand{ordered(mx), (uint32_t)g}, mine);
     };
     fetch(cur, t);
-    for (int g0 = t; g0 - t < ng; g0 += 256 * Q) {
-        fetch(nxt, g0 + 256 * Q);
+    for (int g0 = t; g0 - t < g_end; g0 += N * Q) {
+        fetch(nxt, g0 + N * Q);
         float mx[Q], all_mx = -INFINITY;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -260,44 +261,47 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
         if (all_mx > a.m) stat_rescale(a, all_mx, k);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
+            const int g = g0 + q * N;
+            if (g - t >= g_end) break;  // nothing for the whole wave
             float v[kGroup];
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int u = 0; u < V; ++u) v[i * V + u] = to_f32(cur[q][i].e[u]);
             take(v);
-            const int g = g0 + q * 256;
-            if (top && g >= g_first && g < g_end) keep(g, mx[q]);
+            if (top && g < g_end) keep(g, mx[q]);
         }
 #pragma unroll
         for (int q = 0; q < Q; ++q)
 #pragma unroll
             for (int i = 0; i < NV; ++i) cur[q][i] = nxt[q][i];
     }
-    for (int e = 0; e < 2; ++e) {  // the partial groups
-        const int g = e ? g_end : 0;
-        if (!(e ? g_end < ng && g >= g_first : g_first == 1) || (g & 255) != t) continue;
+    if (g_end < ng && g_end % N == t) {  // the partial group
         float v[kGroup], mx = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kGroup; ++u) {
-            const int64_t c = (g_lo + g) * kGroup - sh + u;
-            v[u] = c >= 0 && c < vocab ? to_f32(z[c]) : -INFINITY;
+            const int64_t c = (g_lo + g_end) * kGroup + u;
+            v[u] = c < vocab ? to_f32(z[c]) : -INFINITY;
             mx = fmaxf(mx, v[u]);
         }
         if (mx > a.m) stat_rescale(a, mx, k);
         take(v);
-        if (top) keep(g, mx);
+        if (top) keep(g_end, mx);
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) a = stat_join(a, stat_shfl_xor(a, o), k);
-    if (lane == 0) wst[w] = a;
-    lead[t] = mine;
-    __syncthreads();
-    if (w != 0) return;
-    a = stat_join(stat_join(wst[0], wst[1], k), stat_join(wst[2], wst[3], k), k);
-    if (t == 0) {
+    if (WAVES > 1) {
+        if (lane == 0) wst[w] = a;
+        lead[t] = mine;
+        __syncthreads();
+        if (w != 0) return;
+        a = stat_join(stat_join(wst[0], wst[1], k), stat_join(wst[2], wst[3], k), k);
+        mine = best_of(best_of(lead[t], lead[t + 64]), best_of(lead[t + 128], lead[t + 192]));
+    }
+    wave_lds_sync();  // gmax is read below, and lead written
+    if (lane == 0) {
         if (nslice > 1)
-            part[row * nslice + slice] = a;
+            part[item] = a;
         else
             put_token<T>(out, a, scale, z, row, vocab);
     }
@@ -308,19 +312,38 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
     // all that is wanted. Mostly those are few enough for a lane each, and then
     // counting who is better ranks them at once (20 of 2048 columns: 13.1 us for
     // the kernel against 18.9 picking one by one).
-    mine = best_of(best_of(lead[t], lead[t + 64]), best_of(lead[t + 128], lead[t + 192]));
     {
-        const int lrank = rank_among(mine, 64);
-        const Cand low = of_rank(mine, lrank, top - 1);
-        Cand* list = lead;            // 64 groups
-        Cand* elems = lead + 64;      // 64 elements
+        Cand* list = lead;        // kFew groups
+        Cand* elems = lead + kFew;  // kFew elements
+        Cand low;
         int ngr = 0, nel = 0;
-        if (ng <= 64 * top) {
+        if (ng <= 64 * top) {  // look all groups over
+            if (top <= 8) {  // sixteen leaders of four lanes serve as well
+                auto quad = [&](int ctl) {
+                    Cand o;
+                    if (ctl == 0)
+                        o = Cand{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.ord, 0xB1, 0xf, 0xf, false),
+                                 (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.idx, 0xB1, 0xf, 0xf, false)};
+                    else
+                        o = Cand{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.ord, 0x4E, 0xf, 0xf, false),
+                                 (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.idx, 0x4E, 0xf, 0xf, false)};
+                    return best_of(mine, o);
+                };
+                const Cand own = mine;
+                mine = quad(0);
+                mine = quad(1);
+                low = of_rank(mine, (lane & 3) ? 64 : rank_among(mine, 16, 4), top - 1);
+                mine = own;
+            } else {
+                low = of_rank(mine, rank_among(mine, 64), top - 1);
+            }
             for (int g = lane; g - lane < ng; g += 64) {
                 const Cand c{g < ng ? ordered(to_f32(gmax[g])) : 0u, (uint32_t)g};
                 ngr = append(list, ngr, c.ord && !better(low, c), c);
             }
-        } else {
+        } else {  // look the winners' groups over
+            const int lrank = rank_among(mine, 64);
+            low = of_rank(mine, lrank, top - 1);
             for (int r = 0; r < top; ++r) {
                 const int owner = (int)(of_rank(mine, lrank, r).idx & 63);
                 for (int g = owner + 64 * lane; g - 64 * lane < ng; g += 4096) {
@@ -329,24 +352,24 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
                 }
             }
         }
-        if (ngr <= 64) {
+        if (ngr <= kFew) {
             wave_lds_sync();
             for (int e = lane; e - lane < ngr * kGroup; e += 64) {
                 Cand c{0, 0};
                 if (e < ngr * kGroup) {
-                    const int64_t col = (g_lo + list[e / kGroup].idx) * kGroup - sh + e % kGroup;
-                    if (col >= 0 && col < vocab) c = Cand{ordered(to_f32(z[col])), (uint32_t)col};
+                    const int64_t col = (g_lo + list[e / kGroup].idx) * kGroup + e % kGroup;
+                    if (col < vocab) c = Cand{ordered(to_f32(z[col])), (uint32_t)col};
                 }
                 nel = append(elems, nel, c.ord && c.ord >= low.ord, c);
             }
-            if (nel <= 64) {
+            if (nel <= kFew) {
                 wave_lds_sync();
                 const Cand c = lane < nel ? elems[lane] : Cand{0, 0};
                 int at = rank_among(c, nel);
                 if (lane >= nel) at = lane;  // fewer than `top` there are
                 if (at >= top) return;
                 if (nslice > 1)
-                    cand[(row * nslice + slice) * top + at] = c;
+                    cand[item * top + at] = c;
                 else
                     put_top(out, a, scale, row, top, at, c);
                 return;
@@ -378,8 +401,8 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         el[q] = Cand{0, 0};
-        const int64_t c = (g_lo + chosen[q].idx) * kGroup - sh + (lane & 7);
-        if (chosen[q].ord && c >= 0 && c < vocab) el[q] = Cand{ordered(to_f32(z[c])), (uint32_t)c};
+        const int64_t c = (g_lo + chosen[q].idx) * kGroup + (lane & 7);
+        if (chosen[q].ord && c < vocab) el[q] = Cand{ordered(to_f32(z[c])), (uint32_t)c};
     }
     Cand got{0, 0};  // lane r keeps the r-th
     for (int r = 0; r < top; ++r) {
@@ -393,7 +416,7 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
     }
     if (lane >= top) return;
     if (nslice > 1)
-        cand[(row * nslice + slice) * top + lane] = got;
+        cand[item * top + lane] = got;
     else
         put_top(out, a, scale, row, top, lane, got);
 }
@@ -451,7 +474,7 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T* __restrict__ 
 
 // ---- short rows ------------------------------------------------------------------
 
-constexpr int kShortCols = 512;  // 8 columns for each of a wave's lanes
+constexpr int kShortCols = 512;  // up to these, a row lies in the registers of a few lanes
 
 // Exchanges across a group of 2^lg lanes, one step per bit, for reductions that
 // leave every lane of the group with the result: within 16 lanes by lane
@@ -467,13 +490,14 @@ __device__ __forceinline__ void group_steps(int lg, F&& step) {
     if (lg > 5) step([](int v) { return __shfl_xor(v, 32, 64); });
 }
 
-// A row per group of 2^lg lanes; lane l holds the columns l, l + 2^lg, ... (NS
-// of them).
-template <class T, int NS>
+// A row per group of 2^lg lanes; lane l holds the column groups l, l + 2^lg, ...
+// (NG of them), all in registers.
+template <class T, int NG>
 __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict__ logits,
                                                             int64_t count, int vocab, int64_t ld,
                                                             float scale, int lg, int top,
                                                             RowOut out) {
+    constexpr int NS = NG * kGroup, V = 16 / sizeof(T);
     const int l = threadIdx.x & ((1 << lg) - 1);
     const int64_t row0 = (int64_t)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
     const bool on = row0 < count;
@@ -483,14 +507,24 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
     float v[NS];
     float m = -FLT_MAX;
 #pragma unroll
-    for (int u = 0; u < NS; ++u) {
-        const int c = l + (u << lg);
-        v[u] = c < vocab ? to_f32(z[c]) : -INFINITY;
-        m = fmaxf(m, v[u]);
+    for (int i = 0; i < NG; ++i) {
+        const int c = (l + (i << lg)) * kGroup;
+        if (c + kGroup <= vocab) {
+#pragma unroll
+            for (int q = 0; q < kGroup; q += V) {
+                const Vec<T, V> x = load_vec<T, V>(z + c + q);
+#pragma unroll
+                for (int u = 0; u < V; ++u) v[i * kGroup + q + u] = to_f32(x.e[u]);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kGroup; ++u)
+                v[i * kGroup + u] = c + u < vocab ? to_f32(z[c + u]) : -INFINITY;
+        }
     }
-    group_steps(lg, [&](auto x) {
-        m = fmaxf(m, __int_as_float(x(__float_as_int(m))));
-    });
+#pragma unroll
+    for (int u = 0; u < NS; ++u) m = fmaxf(m, v[u]);
+    group_steps(lg, [&](auto x) { m = fmaxf(m, __int_as_float(x(__float_as_int(m)))); });
     Stat a = {m, 0.f, 0.f};
 #pragma unroll
     for (int u = 0; u < NS; ++u) {
@@ -504,21 +538,31 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
         a.u += __int_as_float(x(__float_as_int(a.u)));
     });
     if (on && l == 0) put_token<T>(out, a, scale, z, row, vocab);
+    if (!top) return;
     uint32_t ord[NS];
 #pragma unroll
-    for (int u = 0; u < NS; ++u) ord[u] = l + (u << lg) < vocab ? ordered(v[u]) : 0u;
+    for (int u = 0; u < NS; ++u) {
+        const int c = (l + ((u / kGroup) << lg)) * kGroup + u % kGroup;
+        ord[u] = c < vocab ? ordered(v[u]) : 0u;
+    }
     for (int r = 0; r < top; ++r) {
-        Cand b{ord[0], (uint32_t)l};
+        uint32_t bo = ord[0];
+        int bu = 0;
 #pragma unroll
         for (int u = 1; u < NS; ++u)
-            if (ord[u] > b.ord) b = Cand{ord[u], (uint32_t)(l + (u << lg))};
+            if (ord[u] > bo) {
+                bo = ord[u];
+                bu = u;
+            }
+        Cand b{bo, (uint32_t)((l + ((bu / kGroup) << lg)) * kGroup + bu % kGroup)};
+        const uint32_t own = b.idx;
         group_steps(lg, [&](auto x) {
             b = best_of(b, Cand{(uint32_t)x((int)b.ord), (uint32_t)x((int)b.idx)});
         });
         if (on && l == 0) put_top(out, a, scale, row, top, r, b);
+        const int gone = own == b.idx ? bu : -1;  // the lane that held it
 #pragma unroll
-        for (int u = 0; u < NS; ++u)
-            if (l + (u << lg) == (int)b.idx) ord[u] = 0u;
+        for (int u = 0; u < NS; ++u) ord[u] = u == gone ? 0u : ord[u];
     }
 }
 
@@ -526,7 +570,9 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
 
 // dlogits_j = scale (w ([j = tok] - p_j) - q p_j (logp_j + H)), w = dlogp (0
 // without a token), q = dentropy. grid: (column tiles, groups of rows).
-// Rows of few columns share a workgroup, 2^lx lanes to each.
+// Rows of few columns share a workgroup, 2^lx lanes to each. Accesses start at
+// 16-byte boundaries where the rows of both arrays allow it (`aligned`; 2048 x
+// 100003 bf16: 153 us, from the rows' own starts 171).
 template <class T>
 __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int aligned, int lx) {
     constexpr int V = 16 / sizeof(T);
@@ -549,8 +595,9 @@ __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int al
         return empty ? 0.f : scale * g;
     };
     const int64_t step = ((int64_t)gridDim.x << lx) * V;
-    for (int64_t c = (((int64_t)blockIdx.x << lx) + (threadIdx.x & ((1 << lx) - 1))) * V - sh; c < p.vocab; c += step) {
-        if (aligned && c >= 0 && c + V <= p.vocab) {
+    for (int64_t c = (((int64_t)blockIdx.x << lx) + (threadIdx.x & ((1 << lx) - 1))) * V - sh;
+         c < p.vocab; c += step) {
+        if (c >= 0 && c + V <= p.vocab) {
             const Vec<T, V> v = load_vec<T, V>(z + c);
             Vec<T, V> o;
 #pragma unroll
@@ -569,10 +616,13 @@ __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int al
 struct SlicePlan {
     int groups, nslice;
 };
+// Up to these groups (16 a lane) a slice is one wave's, and four share a workgroup.
+constexpr int kWaveGroups = 1024;
+
 // As few slices as the LDS allows, more where there are few rows: about 1024
 // workgroups, each with at least one group per thread.
 SlicePlan slice_plan(int64_t vocab, int64_t count, int bytes) {
-    const int64_t all = (vocab + 7 + kGroup - 1) / kGroup;  // whatever the row's alignment
+    const int64_t all = (vocab + kGroup - 1) / kGroup;
     const int64_t fit = kMaxSlice / bytes / kGroup;
     int64_t n = (all + fit - 1) / fit;
     const int64_t want = (1024 + count - 1) / count;
@@ -589,16 +639,16 @@ template <class T>
 hipError_t logprobs_run(const LogprobArgs& a, hipStream_t st) {
     const RowOut o{a.tokens, a.token_type, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids};
     if (a.vocab <= kShortCols) {
-        // as few lanes a row as hold it with 8 columns each (24 columns: 4 lanes of 6)
+        // as few lanes a row as hold it with 32 columns each (24 columns: one lane)
         int lg = 0;
-        while ((int64_t)8 << lg < a.vocab) ++lg;
-        const int ns = (int)((a.vocab + (1 << lg) - 1) >> lg);
+        while ((int64_t)32 << lg < a.vocab) ++lg;
+        const int ng = (int)((a.vocab + (kGroup << lg) - 1) / (kGroup << lg));
         const int64_t per = 256 >> lg;
         const dim3 g((unsigned)((a.count + per - 1) / per)), b(256);
-        auto* kern = ns <= 2   ? logprob_short_kernel<T, 2>
-                     : ns <= 4 ? logprob_short_kernel<T, 4>
-                     : ns <= 6 ? logprob_short_kernel<T, 6>
-                               : logprob_short_kernel<T, 8>;
+        auto* kern = ng <= 1   ? logprob_short_kernel<T, 1>
+                     : ng <= 2 ? logprob_short_kernel<T, 2>
+                     : ng <= 3 ? logprob_short_kernel<T, 3>
+                               : logprob_short_kernel<T, 4>;
         hipLaunchKernelGGL(kern, g, b, 0, st, (const T*)a.logits, a.count, (int)a.vocab, a.ld,
                            a.scale, lg, a.top, o);
         return hipGetLastError();
@@ -607,9 +657,16 @@ hipError_t logprobs_run(const LogprobArgs& a, hipStream_t st) {
     Stat* part = (Stat*)a.ws;
     Cand* cand =
         (Cand*)((char*)a.ws + ((size_t)a.count * p.nslice * sizeof(Stat) + 255) / 256 * 256);
-    hipLaunchKernelGGL((logprob_slice_kernel<T>), dim3((unsigned)(a.count * p.nslice)), dim3(256),
-                       a.top ? (size_t)p.groups * sizeof(T) : 0, st, (const T*)a.logits, a.vocab, a.ld,
-                       a.scale, p.groups, p.nslice, a.top, part, cand, o);
+    const int64_t items = a.count * p.nslice;
+    const size_t lds = a.top ? (size_t)p.groups * sizeof(T) : 0;
+    if (p.groups <= kWaveGroups)
+        hipLaunchKernelGGL((logprob_slice_kernel<T, 1>), dim3((unsigned)((items + 3) / 4)),
+                           dim3(256), 4 * lds, st, (const T*)a.logits, items, a.vocab, a.ld,
+                           a.scale, p.groups, p.nslice, a.top, part, cand, o);
+    else
+        hipLaunchKernelGGL((logprob_slice_kernel<T, 4>), dim3((unsigned)items), dim3(256), lds, st,
+                           (const T*)a.logits, items, a.vocab, a.ld, a.scale, p.groups, p.nslice,
+                           a.top, part, cand, o);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.nslice == 1) return e;
     hipLaunchKernelGGL((logprob_join_kernel<T>), dim3((unsigned)a.count), dim3(64), 0, st,

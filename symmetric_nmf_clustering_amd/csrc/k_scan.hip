@@ -13,6 +13,8 @@
 // second starts each segment from the maps before it.
 //
 // Masked steps (t >= length) are the identity map; they are not read.
+#include <algorithm>
+
 #include "common.h"
 #include "seq.h"
 
@@ -165,7 +167,10 @@ __device__ __forceinline__ Place place(const ScanArgs& p, const Tile& tl, bool b
     q.b = item / tl.nct / tl.nseg;
     q.c0 = (ct * cl + (threadIdx.x & (cl - 1))) * V;
     q.grp = threadIdx.x >> tl.cl_log2;
-    q.on = q.c0 < p.width;  // V divides the width
+    q.on = q.c0 < p.width;
+    // a row's last lane ends with the row: the channels that it shares with the
+    // lane before it come out the same from both
+    q.c0 = min(q.c0, (int)p.width - V);
     q.t_lo = q.seg * tl.seg;
     q.t_hi = min((int)p.steps, q.t_lo + tl.seg);
     const int len = p.lengths ? min(max(p.lengths[q.b], 0), (int)p.steps) : (int)p.steps;
@@ -297,7 +302,7 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs p, Tile tl, float* _
 constexpr int kWalk = 4;
 template <class T, int V>
 __global__ __launch_bounds__(256) void scan_walk_kernel(ScanArgs p) {
-    const int64_t nv = p.width / V;
+    const int64_t nv = p.width / V;  // V divides the width: the state may be updated in place
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= p.batch * nv) return;
     const int64_t b = i / nv, c0 = (i - b * nv) * V, at = b * p.width + c0;
@@ -483,13 +488,13 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
     }
 }
 
-constexpr int kMaxSeg = 64;
+constexpr int kMaxSeg = 256;
 // Workgroups below which a scan is cut in time, and as many as it is cut into.
 // The forward is cut early: its uncut workgroups keep too little in flight. The
 // backward reads three arrays and writes two, so reading two of them twice only
 // pays where most of the chip would idle (8 x 2048 x 2048 bf16 as 256 workgroups:
 // 88 us, cut into 512: 116, into 1024: 118).
-constexpr int kFill = 2048, kFillGrad = 1024, kCutGrad = 256;
+constexpr int kCut = 256, kFill = 2048, kCutGrad = 256, kFillGrad = 1024;
 constexpr int kWalkSteps = 8;  // up to these, steps are walked one by one
 
 // Channels over threads: 64 channels to a tile, fewer where the width is smaller
@@ -523,7 +528,7 @@ static_assert(256 * kTileT / kTileCh % kScanChunk == 0, "tiles start at kept sta
 
 template <class T, int V, bool CG>
 hipError_t scan_run(const ScanArgs& a, hipStream_t st) {
-    const Tile tl = plan(a.batch, a.steps, a.width, V, kFill, kFill);
+    const Tile tl = plan(a.batch, a.steps, a.width, V, kCut, kFill);
     const dim3 g((unsigned)tl.items);
     if (tl.nseg > 1) {
         hipLaunchKernelGGL((scan_kernel<T, V, 1, CG>), g, dim3(256), 0, st, a, tl, (float*)a.ws);
@@ -553,48 +558,34 @@ hipError_t grad_run(const ScanArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-bool vec_ok(const void* p, int64_t sb, int64_t st, int bytes, int v) {
-    return reinterpret_cast<uintptr_t>(p) % (size_t)(bytes * v) == 0 && sb % v == 0 && st % v == 0;
-}
-template <class T>
-bool scan_fits(const ScanArgs& a, int v) {
-    return a.width % v == 0 && vec_ok(a.x, a.x_b, a.x_t, sizeof(T), v) &&
-           vec_ok(a.gate, a.g_b, a.g_t, sizeof(T), v) && vec_ok(a.h, 0, 0, sizeof(T), v);
-}
-
-// Channels to a lane, 8 bytes of them (one channel where the layout has odd
-// strides). 16 bytes put fewer steps into a thread and more maps into the scan
-// across lanes, 4 bytes take more loads: 2 x 32768 x 1024 bf16 in 153 us, with 16
-// bytes in 175, with 4 in 156; 250 x 100000 fp32 in 48.6, 48.8 and 80.8.
+// Channels to a lane, 8 bytes of them. 16 bytes put fewer steps into a thread and
+// more maps into the scan across lanes, 4 bytes take more loads: 2 x 32768 x 1024
+// bf16 in 153 us, with 16 bytes in 175, with 4 in 156; 250 x 100000 fp32 in 48.6,
+// 48.8 and 80.8. The backward holds more per element: 8 x 2048 x 2048 bf16 with 4
+// bytes in 88 us, with 8 in 97.
 template <class T>
 hipError_t scan_vec(const ScanArgs& a, hipStream_t st) {
     constexpr int W = 16 / sizeof(T), V = 8 / sizeof(T);
-    if (a.steps <= kWalkSteps)
-        return scan_fits<T>(a, W) ? walk_run<T, W>(a, st) : walk_run<T, 1>(a, st);
-    if (scan_fits<T>(a, V))
-        return a.g_t ? scan_run<T, V, false>(a, st) : scan_run<T, V, true>(a, st);
+    if (a.steps <= kWalkSteps) return a.width % W ? walk_run<T, 1>(a, st) : walk_run<T, W>(a, st);
+    if (a.width >= V) return a.g_t ? scan_run<T, V, false>(a, st) : scan_run<T, V, true>(a, st);
     return a.g_t ? scan_run<T, 1, false>(a, st) : scan_run<T, 1, true>(a, st);
 }
 template <class T>
 hipError_t grad_vec(const ScanArgs& a, hipStream_t st) {
-    constexpr int V = sizeof(T) == 2 ? 2 : 1;
-    if (a.width % V == 0 && vec_ok(a.x, a.x_b, a.x_t, sizeof(T), V) &&
-        vec_ok(a.gate, a.g_b, a.g_t, sizeof(T), V) && vec_ok(a.dh, a.d_b, a.d_t, sizeof(T), V) &&
-        vec_ok(a.dx, 0, 0, sizeof(T), V) && vec_ok(a.dgate, 0, 0, sizeof(T), V))
-        return grad_run<T, V>(a, st);
-    return grad_run<T, 1>(a, st);
+    constexpr int V = 4 / sizeof(T);
+    return a.width >= V ? grad_run<T, V>(a, st) : grad_run<T, 1>(a, st);
 }
 
 }  // namespace
 
-// Two numbers per channel and time segment, for as many segments as plan() can
-// make: each holds a unit or more, a unit of a cut scan kScanChunk steps or more,
-// and a scan of less than 4 units is not cut.
+// Two numbers per channel and time segment of the plan that has most.
 size_t scan_ws_bytes(int64_t batch, int64_t steps, int64_t width) {
-    int64_t nseg = (steps + kScanChunk - 1) / kScanChunk;
-    if (nseg < 4) return 256;
-    if (nseg > kMaxSeg) nseg = kMaxSeg;
-    return (size_t)(2 * nseg) * 4 * (size_t)batch * (size_t)width;
+    int64_t nseg = 1;
+    for (int v : {1, 2, 4}) {
+        nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, kCut, kFill).nseg);
+        nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, kCutGrad, kFillGrad).nseg);
+    }
+    return nseg > 1 ? 8 * (size_t)nseg * (size_t)batch * (size_t)width : 256;
 }
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t st) {

@@ -43,19 +43,23 @@ __device__ __forceinline__ f16_t from_f32<f16_t>(float v) {
     return f16_t{(_Float16)v};
 }
 
-// V consecutive elements, moved as one access (V * sizeof(T) <= 16 bytes, and
-// the address a multiple of it).
+// V consecutive elements, moved as one access of up to 16 bytes at any element's
+// address: global loads and stores need no more alignment than that here, so
+// rows of odd length keep their wide accesses (the compiler picks the widest
+// access the target allows for the copy).
 template <class T, int V>
 struct alignas(sizeof(T) * V) Vec {
     T e[V];
 };
 template <class T, int V>
 __device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
-    return *reinterpret_cast<const Vec<T, V>*>(p);
+    Vec<T, V> v;
+    __builtin_memcpy(&v, p, sizeof(T) * V);
+    return v;
 }
 template <class T, int V>
 __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
-    *reinterpret_cast<Vec<T, V>*>(p) = v;
+    __builtin_memcpy(p, &v, sizeof(T) * V);
 }
 
 // symnmf_workspace_bytes for the sequence operators; 0 for invalid sizes (seq.cpp).
