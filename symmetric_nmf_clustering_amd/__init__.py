@@ -8,11 +8,11 @@ synthetic inputs.
 """
 from . import _lib  # noqa: F401
 
-__all__ = ["api", "synth", "metrics", "rolling"]
+__all__ = ["api", "synth", "metrics", "rolling", "events"]
 
 
 def __getattr__(name):
-    if name in ("api", "synth", "metrics", "rolling"):
+    if name in __all__:
         import importlib
 
         return importlib.import_module(f".{name}", __name__)

@@ -351,9 +351,22 @@ __global__ __launch_bounds__(256) void sort_small_kernel(const ID* __restrict__ 
     }
 }
 
-// Sorted tokens per chunk of the sum. Short lists are cut finely, for enough
-// threads to hide the reads' latency; long ones coarsely, for few partials.
-int chunk_len(int64_t count) { return count <= kSmallCount ? 8 : count <= 131072 ? 32 : 128; }
+inline int log2_up(int64_t v, int most) {
+    int l = 0;
+    while (l < most && (int64_t(1) << l) < v) ++l;
+    return l;
+}
+
+// Sorted tokens per chunk of the sum: as few as leave the launch at about 4096
+// waves, 8 to 128. Finer chunks hide more latency but leave more partials
+// (32768 rows of 1024: 32 tokens 125 us, 16 tokens 137; 65536 rows of 24: 8 tokens
+// 48 us, 32 tokens 55).
+int chunk_len(int64_t count, int64_t width) {
+    const int64_t lanes = int64_t(1) << log2_up((width + 3) / 4, 8);
+    int c = 8;
+    while (c < 128 && count * lanes > (int64_t)c * 64 * 4096) c *= 2;
+    return c;
+}
 
 constexpr int kSumRows = 8;  // tokens whose rows a thread has in flight
 
@@ -466,7 +479,7 @@ template <class TO>
 __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
     const uint32_t* __restrict__ keys, int64_t count, int clen, int64_t nchunks, float scale,
     int accumulate, TO* __restrict__ dtable, int64_t ldt, int64_t rows, int width,
-    const float* __restrict__ part, int ldpart) {
+    const float* __restrict__ part, int ldpart, int lx) {
     const int64_t chunk = blockIdx.x;
     const int64_t lo = chunk * clen, hi = lo + clen;
     if (hi >= count) return;
@@ -481,36 +494,49 @@ __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
         more += n;
         if (n < 256) break;
     }
+    // The partials are shared out over groups of 2^lx lanes, each of which adds a
+    // run of them in order, 16 in flight; then the groups' sums in order. Rows of
+    // partials are padded to a multiple of 4 (what the padding holds is not stored).
+    __shared__ float4 sums[256];
+    const int lane = threadIdx.x & ((1 << lx) - 1), grp = threadIdx.x >> lx, groups = 256 >> lx;
+    const int64_t per = (more + groups) / groups, j0 = grp * per;  // the tail partial is the first
+    const int64_t j1 = j0 + per < more + 1 ? j0 + per : more + 1;
     const int64_t step = 2 * (int64_t)ldpart;
-    for (int c = (blockIdx.y * 256 + threadIdx.x) * 4; c < width; c += gridDim.y * 1024) {
-        // 16 partials in flight, added in order; rows of partials are padded to
-        // a multiple of 4 (what the padding holds is not stored)
-        const float* p = part + 2 * (chunk + 1) * (int64_t)ldpart + c;
-        float4 s = *reinterpret_cast<const float4*>(part + (2 * chunk + 1) * (int64_t)ldpart + c);
-        for (int64_t j = 0; j < more; j += 16) {
+    const int c = (int)((blockIdx.y << lx) + lane) * 4;
+    float4 s = {0.f, 0.f, 0.f, 0.f};
+    if (c < width) {
+        const float* p = part + 2 * chunk * (int64_t)ldpart + c;
+        for (int64_t j = j0; j < j1; j += 16) {
             float4 v[16];
 #pragma unroll
             for (int u = 0; u < 16; ++u)
-                if (j + u < more) v[u] = *reinterpret_cast<const float4*>(p + (j + u) * step);
+                if (j + u < j1)
+                    v[u] = *reinterpret_cast<const float4*>(p + (j + u) * step +
+                                                            (j + u == 0 ? ldpart : 0));
 #pragma unroll
             for (int u = 0; u < 16; ++u)
-                if (j + u < more) {
+                if (j + u < j1) {
                     s.x += v[u].x;
                     s.y += v[u].y;
                     s.z += v[u].z;
                     s.w += v[u].w;
                 }
         }
-        const float r[4] = {s.x, s.y, s.z, s.w};
-        put_row<TO, 4>(dtable + (int64_t)key * ldt, c, width, r, scale, accumulate);
     }
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    if (grp != 0 || c >= width) return;
+    for (int q = 1; q < groups; ++q) {
+        const float4 o = sums[(q << lx) + lane];
+        s.x += o.x;
+        s.y += o.y;
+        s.z += o.z;
+        s.w += o.w;
+    }
+    const float r[4] = {s.x, s.y, s.z, s.w};
+    put_row<TO, 4>(dtable + (int64_t)key * ldt, c, width, r, scale, accumulate);
 }
 
-inline int log2_up(int64_t v, int most) {
-    int l = 0;
-    while (l < most && (int64_t(1) << l) < v) ++l;
-    return l;
-}
 template <class TI, class TO, class ID>
 hipError_t embed_run(const EmbedArgs& a, hipStream_t st) {
     constexpr int V = sizeof(TI) == 4 || sizeof(TO) == 4 ? 4 : 8;
@@ -544,7 +570,7 @@ struct GradLayout {
 GradLayout grad_layout(void* ws, int64_t rows, int64_t width, int64_t count) {
     GradLayout L;
     const SortPlan p = sort_plan(rows, count);
-    const int64_t nchunks = (count + chunk_len(count) - 1) / chunk_len(count);
+    const int64_t nchunks = (count + chunk_len(count, width) - 1) / chunk_len(count, width);
     L.ldpart = (int)((width + 3) / 4 * 4);
     size_t off = 0;
     auto take = [&](size_t n) {
@@ -643,10 +669,11 @@ hipError_t sort_ids(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
 template <class TD, class TO>
 hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t* keys,
                     const int32_t* pos, const AbsentFill& af, hipStream_t st) {
-    // float32 on either side: 4 elements a thread, so more threads share a row's
-    // reads (bf16 rows of 1024 into a float32 table: 125 us against 136 with 8)
-    constexpr int V = sizeof(TD) == 4 || sizeof(TO) == 4 ? 4 : 8;
-    const int clen = chunk_len(a.count);
+    // 4 elements a thread, so many threads share a row's reads (bf16 rows of 1024
+    // into a float32 table: 125 us against 136 with 8; rows of 1000 into a bf16
+    // table: 45 against 60)
+    constexpr int V = 4;
+    const int clen = chunk_len(a.count, a.width);
     const int64_t nchunks = (a.count + clen - 1) / clen;
     const int64_t nv = (a.width + V - 1) / V;
     const int lg = log2_up(nv, 8);
@@ -661,10 +688,11 @@ hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
                        af, L.part, L.ldpart, lg);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || nchunks < 2) return e;
-    const unsigned fy = (unsigned)((a.width + 1023) / 1024);
+    const int fx = log2_up((a.width + 3) / 4, 8);
+    const unsigned fy = (unsigned)(((a.width + 3) / 4 + (1 << fx) - 1) >> fx);
     hipLaunchKernelGGL((embed_grad_fold_kernel<TO>), dim3((unsigned)nchunks, fy), dim3(256), 0, st,
                        keys, a.count, clen, nchunks, a.scale, a.accumulate, (TO*)a.dtable, a.ldt,
-                       a.rows, (int)a.width, L.part, L.ldpart);
+                       a.rows, (int)a.width, L.part, L.ldpart, fx);
     return hipGetLastError();
 }
 template <class TD>
