@@ -18,6 +18,8 @@
 // entropy 0. NaN or +inf in a row makes its results NaN.
 #include <float.h>
 
+#include <algorithm>
+
 #include "common.h"
 #include "seq.h"
 
@@ -186,21 +188,22 @@ __device__ __forceinline__ void put_top(const RowOut& o, const Stat& a, float sc
 
 // ---- long rows -------------------------------------------------------------------
 
-// WAVES waves per (row, slice): a workgroup has 4 / WAVES of them. Each thread
+// WAVES waves per (row, slice); a workgroup of at least 256 threads. Each thread
 // takes four groups (of a tile of 256 WAVES) at a time, the next four already
 // on their way; a row's last group may be partial and is read element by
 // element. Group maxima are kept in the logits' own type (exact).
 template <class T, int WAVES>
-__global__ __launch_bounds__(256) void logprob_slice_kernel(
+__global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_kernel(
     const T* __restrict__ logits, int64_t items, int64_t vocab, int64_t ld, float scale,
     int groups_per_slice, int nslice, int top, Stat* __restrict__ part, Cand* __restrict__ cand,
     RowOut out) {
     extern __shared__ __align__(16) char smem[];
-    __shared__ Stat wst[4];
     constexpr int V = 16 / sizeof(T), NV = kGroup / V, Q = 4, N = 64 * WAVES;
-    __shared__ Cand leads[4 / WAVES][N > 2 * kFew ? N : 2 * kFew];
+    constexpr int SLOTS = WAVES < 4 ? 4 / WAVES : 1;
+    __shared__ Stat wst[WAVES];
+    __shared__ Cand leads[SLOTS][N > 2 * kFew ? N : 2 * kFew];
     const int slot = threadIdx.x / N, t = threadIdx.x % N, lane = t & 63, w = t >> 6;
-    const int64_t item = (int64_t)blockIdx.x * (4 / WAVES) + slot;
+    const int64_t item = (int64_t)blockIdx.x * SLOTS + slot;
     if (item >= items) return;  // whole waves, and with several to an item whole workgroups
     T* gmax = reinterpret_cast<T*>(smem) + (int64_t)slot * groups_per_slice;
     Cand* lead = leads[slot];
@@ -295,8 +298,13 @@ __global__ __launch_bounds__(256) void logprob_slice_kernel(
         lead[t] = mine;
         __syncthreads();
         if (w != 0) return;
-        a = stat_join(stat_join(wst[0], wst[1], k), stat_join(wst[2], wst[3], k), k);
-        mine = best_of(best_of(lead[t], lead[t + 64]), best_of(lead[t + 128], lead[t + 192]));
+        a = lane < WAVES ? wst[lane] : stat_none();
+#pragma unroll
+        for (int o = WAVES / 2; o >= 1; o >>= 1) a = stat_join(a, stat_shfl_xor(a, o), k);
+        a = {__shfl(a.m, 0, 64), __shfl(a.s, 0, 64), __shfl(a.u, 0, 64)};
+        mine = lead[t];
+#pragma unroll
+        for (int i = 1; i < WAVES; ++i) mine = best_of(mine, lead[t + 64 * i]);
     }
     wave_lds_sync();  // gmax is read below, and lead written
     if (lane == 0) {
@@ -614,22 +622,29 @@ __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int al
 // ---- plans -------------------------------------------------------------------------
 
 struct SlicePlan {
-    int groups, nslice;
+    int waves, groups, nslice;
 };
-// Up to these groups (16 a lane) a slice is one wave's, and four share a workgroup.
+// A slice's waves: one up to these groups (16 a lane; four slices then share a
+// workgroup: 10000 x 4000 bf16 39 us against 52 with four waves), else four, or
+// sixteen where there are few rows (256 x 100000: 24.5 us against 28.9).
 constexpr int kWaveGroups = 1024;
+constexpr int64_t kFewRows = 256;
+// Rows are cut only where they are so few and so long that most of the chip would
+// idle: into about kItems slices altogether, joined by a second launch (16 x
+// 100000 bf16, top 20: 18.8 us, whole 31.3; 64 x 32768: 20.8 us, whole 18.7).
+constexpr int64_t kCutRows = 64, kCutBytes = 64 << 10, kItems = 1024;
 
-// As few slices as the LDS allows, more where there are few rows: about 1024
-// workgroups, each with at least one group per thread.
+// Whole rows fit a slice up to 256 KiB with four waves, 1 MiB with sixteen (the
+// maxima take an eighth of it in LDS).
 SlicePlan slice_plan(int64_t vocab, int64_t count, int bytes) {
     const int64_t all = (vocab + kGroup - 1) / kGroup;
-    const int64_t fit = kMaxSlice / bytes / kGroup;
-    int64_t n = (all + fit - 1) / fit;
-    const int64_t want = (1024 + count - 1) / count;
-    const int64_t most = (all + 255) / 256;
-    if (n < want) n = want < most ? want : most;
-    if (n > kMaxSlices) n = kMaxSlices;  // kMaxVocab columns fit that many
     SlicePlan p;
+    const bool cut = count <= kCutRows && vocab * bytes > kCutBytes && all > kWaveGroups;
+    p.waves = all <= kWaveGroups ? 1 : count <= kFewRows && !cut ? 16 : 4;
+    const int64_t fit = (p.waves == 16 ? 4 : 1) * (int64_t)kMaxSlice / bytes / kGroup;
+    int64_t n = (all + fit - 1) / fit;
+    if (cut) n = std::max(n, std::min((kItems + count - 1) / count, (all + 255) / 256));
+    if (n > kMaxSlices) n = kMaxSlices;  // kMaxVocab columns fit that many
     p.groups = (int)((all + n - 1) / n);
     p.nslice = (int)((all + p.groups - 1) / p.groups);
     return p;
@@ -659,14 +674,13 @@ hipError_t logprobs_run(const LogprobArgs& a, hipStream_t st) {
         (Cand*)((char*)a.ws + ((size_t)a.count * p.nslice * sizeof(Stat) + 255) / 256 * 256);
     const int64_t items = a.count * p.nslice;
     const size_t lds = a.top ? (size_t)p.groups * sizeof(T) : 0;
-    if (p.groups <= kWaveGroups)
-        hipLaunchKernelGGL((logprob_slice_kernel<T, 1>), dim3((unsigned)((items + 3) / 4)),
-                           dim3(256), 4 * lds, st, (const T*)a.logits, items, a.vocab, a.ld,
-                           a.scale, p.groups, p.nslice, a.top, part, cand, o);
-    else
-        hipLaunchKernelGGL((logprob_slice_kernel<T, 4>), dim3((unsigned)items), dim3(256), lds, st,
-                           (const T*)a.logits, items, a.vocab, a.ld, a.scale, p.groups, p.nslice,
-                           a.top, part, cand, o);
+    auto* kern = p.waves == 1   ? logprob_slice_kernel<T, 1>
+                 : p.waves == 4 ? logprob_slice_kernel<T, 4>
+                                : logprob_slice_kernel<T, 16>;
+    const int slots = p.waves == 1 ? 4 : 1, threads = p.waves == 16 ? 1024 : 256;
+    hipLaunchKernelGGL(kern, dim3((unsigned)((items + slots - 1) / slots)), dim3(threads),
+                       slots * lds, st, (const T*)a.logits, items, a.vocab, a.ld, a.scale,
+                       p.groups, p.nslice, a.top, part, cand, o);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.nslice == 1) return e;
     hipLaunchKernelGGL((logprob_join_kernel<T>), dim3((unsigned)a.count), dim3(64), 0, st,
@@ -709,10 +723,10 @@ hipError_t grad_run(const LogprobArgs& a, hipStream_t st) {
 
 size_t logprob_ws_bytes(int64_t vocab, int top, int64_t count) {
     if (vocab <= kShortCols || count == 0) return 256;
-    // float32 rows have the most slices
-    const SlicePlan p = slice_plan(vocab, count, 4);
-    return ((size_t)count * p.nslice * sizeof(Stat) + 255) / 256 * 256 +
-           (size_t)count * p.nslice * (size_t)top * 8 + 256;
+    const int64_t n = std::max(slice_plan(vocab, count, 2).nslice, slice_plan(vocab, count, 4).nslice);
+    if (n < 2) return 256;
+    return ((size_t)(count * n) * sizeof(Stat) + 255) / 256 * 256 +
+           (size_t)(count * n) * (size_t)top * sizeof(Cand) + 256;
 }
 
 hipError_t launch_logprobs(const LogprobArgs& a, hipStream_t st) {

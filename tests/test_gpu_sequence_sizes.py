@@ -1,0 +1,120 @@
+"""GPU tests of the sequence operators at the sizes where their plans change:
+how rows are shared out over waves, slices, chunks, tiles and segments."""
+import numpy as np
+import pytest
+
+from oracle import sequence_oracle as so
+from tests import test_gpu_sequence as base
+from tests.gpu_util import require_gpu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("count,vocab,top", [(70, 8192, 5), (66, 8193, 32), (64, 8200, 7), (3, 16390, 9),
+                                             (257, 9001, 4), (80, 70001, 3), (65, 300000, 2),
+                                             (3000, 32, 5), (999, 31, 31), (130, 65, 8), (5, 2049, 9)])
+def test_token_logprobs_plans(kind, count, vocab, top):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab * 3 + count)
+    z = (rng.standard_normal((count, vocab)) * 3).astype(np.float32)
+    z[1::4, ::3] = -np.inf
+    t, zv = base.dev(torch, z, kind)
+    tok = rng.integers(-1, vocab, size=count)
+    r = api.token_logprobs(t, torch.from_numpy(tok).cuda(), top=top)
+    logp, h, lse, tlp, ids = so.token_logprobs(zv, tok, top, 1.0)
+    bl, bh = base.logprob_bounds(zv, 1.0, lse)
+    base.close(r.logp, logp, bl)
+    base.close(r.entropy, h, bh)
+    base.close(r.lse, lse, bl)
+    assert np.array_equal(r.top_ids.cpu().numpy(), ids)
+    base.close(r.top_logp, tlp, bl[:, None])
+
+
+@pytest.mark.parametrize("count,vocab", [(6, 40), (6, 700), (6, 8000), (6, 20000), (6, 100003),
+                                         (100, 20000), (300, 20000)])
+def test_top_where_many_logits_are_equal_or_in_order(count, vocab):
+    """Constant rows, two values, rising, falling and sparse rows, all -inf: the
+    bounds that spare the search leave too many candidates or too few."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    i = np.arange(vocab)
+    rows = [np.zeros(vocab), np.where(i % 2, 1.0, 0.5), i / vocab, -i / vocab,
+            np.where(i % 977 == 5, 2.0, -np.inf), np.full(vocab, -np.inf)]
+    z = np.stack([rows[r % 6] for r in range(count)])
+    for kind in ("fp32", "bf16"):
+        t, zv = base.dev(torch, z, kind)
+        tok = torch.zeros(count, dtype=torch.int32, device="cuda")
+        for top in (1, 5, 32):
+            r = api.token_logprobs(t, tok, top=top)
+            ids = so.token_logprobs(zv, np.zeros(count, int), top, 1.0)[4]
+            assert np.array_equal(r.top_ids.cpu().numpy(), ids), (kind, top)
+
+
+@pytest.mark.parametrize("kind,out", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows,width,count", [(5, 6, 8191), (5, 6, 8192), (5, 6, 8193), (700, 1021, 8200),
+                                              (511, 40, 9000), (512, 40, 9000), (262143, 3, 9000),
+                                              (262144, 3, 9000), (90000, 3, 140000)])
+def test_embed_grad_plans(kind, out, rows, width, count):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(count + rows)
+    ids = base.skewed(rng, rows, count)
+    ids[rng.random(count) < 0.05] = -1
+    d, dv = base.dev(torch, rng.standard_normal((count, width)), kind)
+    ref, mag = np.zeros((rows, width)), np.zeros((rows, width))
+    ok = ids >= 0
+    np.add.at(ref, ids[ok], dv[ok])
+    np.add.at(mag, ids[ok], np.abs(dv[ok]))
+    n = np.bincount(ids[ok], minlength=rows)[:, None]
+    got = api.embed_grad(d, torch.from_numpy(ids).cuda(), rows, dtype=base.types(torch)[out])
+    base.close(got, ref, (n + 2) * base.U * mag, out)
+    assert torch.equal(got, api.embed_grad(d, torch.from_numpy(ids).int().cuda(), rows,
+                                           dtype=base.types(torch)[out]))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("batch,steps,width", [(2, 8, 5), (2, 9, 6), (3, 16, 300), (2, 32, 1000), (1, 33, 1000),
+                                               (5, 60, 257), (1, 70, 4), (2, 512, 67), (1, 640, 3),
+                                               (300, 130, 65)])
+def test_scan_plans(kind, batch, steps, width):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(steps + width)
+    x, xv = base.dev(torch, rng.standard_normal((batch, steps, width)), kind)
+    g, gv = base.dev(torch, rng.standard_normal((batch, steps, width)) + 2, kind)
+    c, cv = base.dev(torch, rng.standard_normal(width) + 2, kind)
+    h0, h0v = base.dev(torch, rng.standard_normal((batch, width)))
+    n = rng.integers(0, steps + 1, size=batch)
+    tn = torch.from_numpy(n).int().cuda()
+    for gate, gatev in ((g, gv), (c.expand(batch, steps, width), np.broadcast_to(cv, xv.shape))):
+        E, bx, bg, bm = base.scan_bounds(xv, gatev, h0v, n, xv, h0v)
+        h, last, st = api.gated_scan(x, gate, h0=h0, lengths=tn, return_states=True)
+        hr, lr, before = so.gated_scan(xv, gatev, h0v, n)
+        base.close(h, hr, E[:, 1:], kind)
+        base.close(last, lr, E[:, -1])
+        base.close(st, before[:, :-1:128], E[:, :-1:128])
+        dx, dg, dh0 = api.gated_scan_grad(x, gate, st, x, dh_last=h0, lengths=tn)
+        rx, rg, r0 = so.gated_scan_grad(xv, gatev, xv, h0v, h0v, n)
+        base.close(dx, rx, bx, kind)
+        base.close(dg, rg, bg, kind)
+        base.close(dh0, r0, bm)
+
+
+def test_live_state_in_place():
+    """h0 and h_last may be one buffer for a single step (C ABI)."""
+    import ctypes
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import _lib as L, api
+    for width in (33, 64):
+        x, g = (torch.randn(5, width, device="cuda").bfloat16() for _ in range(2))
+        s = torch.randn(5, width, device="cuda")
+        want = api.gated_step(x, g, s)[1]
+        h, ws = torch.empty_like(x), api.workspace(256)
+        st = L.load().symnmf_gated_scan(L.BF16, 5, 1, width, x.data_ptr(), width, 0, g.data_ptr(),
+                                        width, 0, None, s.data_ptr(), h.data_ptr(), s.data_ptr(),
+                                        None, ws.data_ptr(), ws.numel(),
+                                        ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        assert st == L.OK
+        assert torch.equal(s, want)
