@@ -14,6 +14,7 @@
 //
 // Masked steps (t >= length) are the identity map; they are not read.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 #include "seq.h"
@@ -23,9 +24,9 @@ namespace {
 
 // a = sigmoid(g) and c = sigmoid(-g), each with full relative accuracy
 // (1 - a would lose c's where a is near 1). exp(-g) is held below 2^100 so that
-// c stays 1 where a underflows.
+// c stays 1 where a underflows (by the minimum that keeps NaN).
 __device__ __forceinline__ void gates(float g, float& a, float& c) {
-    const float e = fminf(__expf(-g), 1.2676506e30f);
+    const float e = __builtin_elementwise_minimum(__expf(-g), 1.2676506e30f);
     a = __builtin_amdgcn_rcpf(1.f + e);
     c = e * a;
 }
@@ -149,6 +150,27 @@ __device__ __forceinline__ void segment_start(float (&h)[V], const float* __rest
     for (int u = 0; u < V; ++u) h[u] = next[u];
 }
 
+// p + stride, kept from being rewritten as one of R multiples of the stride,
+// which would take more scalar registers than there are.
+template <class T>
+__device__ __forceinline__ T* next_step(T* p, int64_t stride) {
+    asm("" : "+s"(stride));
+    return p + stride;
+}
+
+// R steps of V channels from `p` on, `stride` apart; ALL: every step is there,
+// else those at and past `lim` (the first step being ts) are zeros. The addresses
+// are one pointer per thread, moved on by a stride that the workgroup shares.
+template <class T, int V, int R, bool ALL>
+__device__ __forceinline__ void load_steps(Vec<T, V> (&v)[R], const T* p, int64_t stride, int ts,
+                                           int lim) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        v[r] = ALL ? load_vec<T, V>(p) : load_or_zero<T, V>(p, ts + r < lim);
+        p = next_step(p, stride);
+    }
+}
+
 // Where a workgroup works, for the kernels below. `back`: from the last item to
 // the first, so that the second launch of a scan cut in time begins with what
 // the first has just read (the last 256 MB of it may still be in the cache).
@@ -183,8 +205,12 @@ __device__ __forceinline__ Place place(const ScanArgs& p, const Tile& tl, bool b
 // MODE 0: the outputs; 1: only the segment's map, to agg (per segment A, then
 // B, batch x width each). CG: the gate does not change over time (stride 0), so
 // it is read, and its sigmoid taken, once.
+//
+// Four waves per SIMD are asked of the compiler where it misses them by a register
+// or two (250 x 100000 fp32, one decay a channel: 47.8 us against 50.7); elsewhere
+// that would spill.
 template <class T, int V, int MODE, bool CG>
-__global__ __launch_bounds__(256) void scan_kernel(ScanArgs p, Tile tl, float* __restrict__ agg) {
+__global__ __launch_bounds__(256, CG && sizeof(T) == 4 && V > 1 ? 4 : 1) void scan_kernel(ScanArgs p, Tile tl, float* __restrict__ agg) {
     constexpr int R = kTileT / V;
     __shared__ float tot[2][2 * 4 * 64 * V];
     const Place q = place<V>(p, tl, MODE == 0 && tl.nseg > 1);
@@ -207,17 +233,25 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs p, Tile tl, float* _
     if (MODE == 0 && q.seg > 0)
         segment_start<V, 1>(h, agg, q.lanes, q.at, on, q.seg, tl, q.grp, tot[1]);
 
+    // lanes past the width read what the last one reads, and write nothing
     Vec<T, V> xv[R], gv[CG ? 1 : R];
-    auto fetch = [&](int ts) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = on && ts + r < q.lim;
-            xv[r] = load_or_zero<T, V>(x + (int64_t)(ts + r) * p.x_t, in);
-            if (!CG) gv[CG ? 0 : r] = load_or_zero<T, V>(g + (int64_t)(ts + r) * p.g_t, in);
+    const T* px = x + (int64_t)(q.t_lo + q.grp * R) * p.x_t;
+    const T* pg = g + (int64_t)(q.t_lo + q.grp * R) * p.g_t;
+    T* po = (T*)p.h + (q.b * p.steps + q.t_lo + q.grp * R) * p.width + q.c0;
+    auto fetch = [&](int t0) {
+        const int ts = t0 + q.grp * R;
+        if (t0 + tt <= q.lim) {
+            load_steps<T, V, R, true>(xv, px, p.x_t, ts, q.lim);
+            if constexpr (!CG) load_steps<T, V, R, true>(gv, pg, p.g_t, ts, q.lim);
+        } else {
+            load_steps<T, V, R, false>(xv, px, p.x_t, ts, q.lim);
+            if constexpr (!CG) load_steps<T, V, R, false>(gv, pg, p.g_t, ts, q.lim);
         }
+        px += tt * p.x_t;
+        pg += tt * p.g_t;
     };
     int buf = 0;
-    fetch(q.t_lo + q.grp * R);
+    fetch(q.t_lo);
     for (int t0 = q.t_lo; t0 < q.t_hi; t0 += tt, buf ^= 1) {
         const int ts = t0 + q.grp * R;
         float a[R][V], bb[R][V], A[V], B[V];
@@ -235,7 +269,7 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs p, Tile tl, float* _
                 if (!CG) gates(to_f32(gv[CG ? 0 : r].e[u]), a[r][u], c);
                 bb[r][u] = c * to_f32(xv[r].e[u]);
             }
-        fetch(ts + tt);  // the next tile's, while this one is composed
+        fetch(t0 + tt);  // the next tile's, while this one is composed
         if (t0 + tt > q.lim) {
 #pragma unroll
             for (int r = 0; r < R; ++r)
@@ -269,17 +303,25 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanArgs p, Tile tl, float* _
 #pragma unroll
                 for (int u = 0; u < V; ++u) s[u] = in[u];
             }
-            T* o = (T*)p.h + (q.b * p.steps + ts) * p.width + q.c0;
+            auto put = [&](auto masked) {
+                T* o = po;
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                Vec<T, V> v;
+                for (int r = 0; r < R; ++r) {
+                    Vec<T, V> v;
 #pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    in[u] = fmaf(a[r][u], in[u], bb[r][u]);
-                    v.e[u] = from_f32<T>(ts + r < q.lim ? in[u] : 0.f);
+                    for (int u = 0; u < V; ++u) {
+                        in[u] = fmaf(a[r][u], in[u], bb[r][u]);
+                        v.e[u] = from_f32<T>(!masked || ts + r < q.lim ? in[u] : 0.f);
+                    }
+                    if (!masked || ts + r < q.t_hi) store_vec<T, V>(o, v);
+                    o = next_step(o, p.width);
                 }
-                if (ts + r < q.t_hi) store_vec<T, V>(o + (int64_t)r * p.width, v);
-            }
+            };
+            if (t0 + tt <= q.lim)
+                put(std::false_type{});
+            else
+                put(std::true_type{});
+            po += tt * p.width;
         }
 #pragma unroll
         for (int u = 0; u < V; ++u) h[u] = next[u];
@@ -376,23 +418,33 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
 
     Vec<T, V> xv[R], gv[R], dv[R];
     float hs[V];
+    const int ntile = (q.t_hi - q.t_lo + tt - 1) / tt;
+    const int64_t t_end = q.t_lo + (ntile - 1) * (int64_t)tt + q.grp * R;  // in the last tile
+    const T* px = x + t_end * p.x_t;
+    const T* pg = g + t_end * p.g_t;
+    const T* pd = d + t_end * p.d_t;
+    T* ox = (T*)p.dx + (q.b * p.steps + t_end) * p.width + q.c0;
+    T* og = (T*)p.dgate + (q.b * p.steps + t_end) * p.width + q.c0;
     auto fetch = [&](int t0) {
         const int ts = t0 + q.grp * R;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const bool in = on && t0 >= q.t_lo && ts + r < q.lim;
-            gv[r] = load_or_zero<T, V>(g + (int64_t)(ts + r) * p.g_t, in);
-            dv[r] = load_or_zero<T, V>(d + (int64_t)(ts + r) * p.d_t, in);
-            if (MODE == 0) xv[r] = load_or_zero<T, V>(x + (int64_t)(ts + r) * p.x_t, in);
+        if (t0 < q.t_lo) return;
+        if (t0 + tt <= q.lim) {
+            load_steps<T, V, R, true>(gv, pg, p.g_t, ts, q.lim);
+            load_steps<T, V, R, true>(dv, pd, p.d_t, ts, q.lim);
+            if (MODE == 0) load_steps<T, V, R, true>(xv, px, p.x_t, ts, q.lim);
+        } else {
+            load_steps<T, V, R, false>(gv, pg, p.g_t, ts, q.lim);
+            load_steps<T, V, R, false>(dv, pd, p.d_t, ts, q.lim);
+            if (MODE == 0) load_steps<T, V, R, false>(xv, px, p.x_t, ts, q.lim);
         }
         if (MODE == 0)
 #pragma unroll
             for (int u = 0; u < V; ++u)
-                hs[u] = on && t0 >= q.t_lo
-                            ? p.states[(q.b * nst + t0 / kScanChunk) * p.width + q.c0 + u]
-                            : 0.f;
+                hs[u] = p.states[(q.b * nst + t0 / kScanChunk) * p.width + q.c0 + u];
+        px -= tt * p.x_t;
+        pg -= tt * p.g_t;
+        pd -= tt * p.d_t;
     };
-    const int ntile = (q.t_hi - q.t_lo + tt - 1) / tt;
     int buf = 0;
     fetch(q.t_lo + (ntile - 1) * tt);
     for (int k = ntile - 1; k >= 0; --k, buf ^= 1) {
@@ -453,24 +505,34 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
                     hin[u] = fmaf(a[r][u], hin[u], c[r][u] * xf[r][u]);
                     xf[r][u] = before;
                 }
-            T* ox = (T*)p.dx + (q.b * p.steps + ts) * p.width + q.c0;
-            T* og = (T*)p.dgate + (q.b * p.steps + ts) * p.width + q.c0;
+            auto put = [&](auto masked) {
+                T* wx = ox + (R - 1) * p.width;
+                T* wg = og + (R - 1) * p.width;
 #pragma unroll
-            for (int r = R - 1; r >= 0; --r) {
-                Vec<T, V> vx, vg;
+                for (int r = R - 1; r >= 0; --r) {
+                    Vec<T, V> vx, vg;
 #pragma unroll
-                for (int u = 0; u < V; ++u) {
-                    const float lam = min_[u] + df[r][u];
-                    const float lc = lam * c[r][u];
-                    vx.e[u] = from_f32<T>(lc);
-                    vg.e[u] = from_f32<T>(lc * a[r][u] * xf[r][u]);
-                    min_[u] = a[r][u] * lam;
+                    for (int u = 0; u < V; ++u) {
+                        const float lam = min_[u] + df[r][u];
+                        const float lc = lam * c[r][u];
+                        vx.e[u] = from_f32<T>(lc);
+                        vg.e[u] = from_f32<T>(lc * a[r][u] * xf[r][u]);
+                        min_[u] = a[r][u] * lam;
+                    }
+                    if (!masked || ts + r < q.t_hi) {
+                        store_vec<T, V>(wx, vx);
+                        store_vec<T, V>(wg, vg);
+                    }
+                    wx = next_step(wx, -p.width);
+                    wg = next_step(wg, -p.width);
                 }
-                if (ts + r < q.t_hi) {
-                    store_vec<T, V>(ox + (int64_t)r * p.width, vx);
-                    store_vec<T, V>(og + (int64_t)r * p.width, vg);
-                }
-            }
+            };
+            if (t0 + tt <= q.t_hi)
+                put(std::false_type{});
+            else
+                put(std::true_type{});
+            ox -= tt * p.width;
+            og -= tt * p.width;
         }
 #pragma unroll
         for (int u = 0; u < V; ++u) m[u] = mn[u];

@@ -118,3 +118,19 @@ def test_live_state_in_place():
                                         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
         assert st == L.OK
         assert torch.equal(s, want)
+
+
+@pytest.mark.parametrize("steps", [5, 300])
+def test_scan_carries_nan_on(steps):
+    """A NaN gate or input makes its channel NaN from that step on, no other."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    for kind in ("fp32", "bf16"):
+        for which in (0, 1):
+            x, g = (torch.randn(2, steps, 20, device="cuda").to(base.types(torch)[kind]) for _ in range(2))
+            (x, g)[which][1, 3, 7] = float("nan")
+            h, last = api.gated_scan(x, g)
+            bad = torch.zeros(2, steps, 20, dtype=torch.bool, device="cuda")
+            bad[1, 3:, 7] = True
+            assert torch.equal(torch.isnan(h), bad)
+            assert torch.equal(torch.isnan(last), bad[:, -1])
