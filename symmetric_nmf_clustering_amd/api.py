@@ -8,6 +8,7 @@ only supplies device memory and the stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 from typing import Optional
@@ -365,7 +366,7 @@ def _here(device):
     """The stream to launch on: torch's current one, of the tensors' device. The
     raw handle (0.1 us) rather than a Stream object made for the call (2.7 us,
     a quarter of a small call)."""
-    index = torch.cuda.current_device()
+    index = torch._C._cuda_getDevice()
     if device.index != index:
         raise ValueError(f"the tensors are on {device}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(index)
@@ -376,14 +377,26 @@ def _rows_out(n: int, width: int, dtype, device) -> torch.Tensor:
     return torch.empty_strided((n, width), (width, 1), dtype=dtype, device=device)
 
 
+def _steps_out(batch: int, steps: int, width: int, dtype, device) -> torch.Tensor:
+    return torch.empty_strided((batch, steps, width), (steps * width, width, 1), dtype=dtype,
+                               device=device)
+
+
 _no_scratch: dict = {}
 
 
-def _scratch(nbytes: int, device) -> torch.Tensor:
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(op: int, n: int, k: int, T: int) -> int:
+    # the sizes decide alone, so a loop's calls ask once
+    return workspace_bytes(op, n, k, T)
+
+
+def _scratch(op: int, n: int, k: int, T: int, device) -> torch.Tensor:
     """Workspace of a call. One of the least size is never touched (the query's
     answer for "none"), so all such calls of a device share one."""
+    nbytes = _scratch_bytes(op, n, k, T)
     if nbytes > 256:
-        return workspace(nbytes, device)
+        return torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     ws = _no_scratch.get(device)
     if ws is None:
         ws = _no_scratch[device] = workspace(256, device)
@@ -439,7 +452,7 @@ def embed_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 
     if accumulate and out is None:
         raise ValueError("accumulate=True needs out")
     if out is None:
-        out = torch.empty((rows, width), dtype=dtype, device=dout.device)
+        out = _rows_out(rows, width, dtype, dout.device)
     ot = _seq_tensor(out, "out", shape=(rows, width), device=dout.device)
     ldo = _rows_ld(out, "out")
     flat = dout.reshape(-1, width)
@@ -447,7 +460,7 @@ def embed_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 
         flat = flat.contiguous()
     ldd = _rows_ld(flat, "dout") if flat.shape[0] else width
     ids = ids.contiguous()
-    ws = _scratch(workspace_bytes(L.OP_EMBED_GRAD, rows, width, ids.numel()), dout.device)
+    ws = _scratch(L.OP_EMBED_GRAD, rows, width, ids.numel(), dout.device)
     st = L.load().symnmf_embed_grad(flat.data_ptr(), dt, ids.numel(), width, ldd, ids.data_ptr(), it,
                                     scale, int(accumulate), out.data_ptr(), ot, rows, ldo,
                                     ws.data_ptr(), ws.numel(), _here(dout.device))
@@ -499,11 +512,10 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tensor] =
     x_b, x_t = _scan_view(x, "x")
     g_b, g_t = _scan_view(gate, "gate", x)
     batch, steps, width = x.shape
-    h = torch.empty((batch, steps, width), dtype=x.dtype, device=x.device)
+    h = _steps_out(batch, steps, width, x.dtype, x.device)
     states = None
     if return_states:
-        states = torch.empty((batch, -(-steps // L.SCAN_CHUNK), width), dtype=torch.float32,
-                             device=x.device)
+        states = _steps_out(batch, -(-steps // L.SCAN_CHUNK), width, torch.float32, x.device)
     last = _scan_call(x, gate, (batch, steps, width), (x_b, x_t, g_b, g_t), lengths, h0, h, states)
     return (h, last, states) if return_states else (h, last)
 
@@ -515,7 +527,7 @@ def _scan_call(x, gate, sizes, strides, lengths, h0, h, states):
     if batch < 1 or width < 1:
         raise ValueError("x must have at least one batch row and one channel")
     last = _rows_out(batch, width, torch.float32, dev)
-    ws = _scratch(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
+    ws = _scratch(L.OP_GATED_SCAN, width, batch, steps, dev)
     st = L.load().symnmf_gated_scan(
         _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
         _lengths_ptr(lengths, batch, dev), _state_ptr(h0, "h0", (batch, width), dev),
@@ -552,10 +564,10 @@ def gated_scan_grad(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, d
     dev = x.device
     if batch < 1 or width < 1:
         raise ValueError("x must have at least one batch row and one channel")
-    dx = torch.empty((batch, steps, width), dtype=x.dtype, device=dev)
+    dx = _steps_out(batch, steps, width, x.dtype, dev)
     dgate = torch.empty_like(dx)
-    dh0 = torch.empty((batch, width), dtype=torch.float32, device=dev)
-    ws = _scratch(workspace_bytes(L.OP_GATED_SCAN, width, batch, steps), dev)
+    dh0 = _rows_out(batch, width, torch.float32, dev)
+    ws = _scratch(L.OP_GATED_SCAN, width, batch, steps, dev)
     st = L.load().symnmf_gated_scan_grad(
         _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
         _lengths_ptr(lengths, batch, dev),
@@ -610,7 +622,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,
     if top:
         top_logp = _rows_out(n, top, torch.float32, dev)
         top_ids = _rows_out(n, top, torch.int32, dev)
-    ws = _scratch(workspace_bytes(L.OP_TOKEN_LOGPROBS, vocab, top, n), dev)
+    ws = _scratch(L.OP_TOKEN_LOGPROBS, vocab, top, n, dev)
     st = L.load().symnmf_token_logprobs(
         logits.data_ptr(), lt, n, vocab, ld, tokens.data_ptr(), it, scale, logp.data_ptr(),
         entropy.data_ptr(), lse.data_ptr(), top, top_logp.data_ptr() if top else None,
