@@ -300,7 +300,7 @@ __global__ __launch_bounds__(256) void sort_scatter_kernel(
 
 // Short lists: a token's place is the number of tokens that go before it, counted
 // directly: 16 tokens per workgroup, 16 threads to a token, every id in LDS.
-// One launch, quadratic but wide: 5000 tokens take 10.8 us, where one workgroup's
+// One launch, quadratic but wide: 5000 tokens take 9.6 us, where one workgroup's
 // passes in LDS took 16.3 and the four launches of the long lists' sort 23.6. The
 // launch's other workgroups clear the table.
 constexpr int64_t kSmallCount = 8192;
@@ -319,15 +319,26 @@ __global__ __launch_bounds__(256) void sort_small_kernel(const ID* __restrict__ 
         return;
     }
     const int padded = (count + 63) / 64 * 64;  // 16 threads x 4 ids
-    for (int i0 = t; i0 < padded; i0 += 256 * 8) {
-        uint32_t k[8];
+    // 16 bytes of ids a load, all of a thread's on their way together
+    constexpr int P = 16 / sizeof(ID), L = (int)kSmallCount / (256 * P);
+    Vec<ID, P> id[L];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            k[u] = i0 + 256 * u < count ? key_of(ids[i0 + 256 * u], rows) : 0xffffffffu;
+    for (int q = 0; q < L; ++q) {
+        const int i0 = (t + 256 * q) * P;
+        if (i0 + P <= count) {
+            id[q] = load_vec<ID, P>(ids + i0);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (i0 + 256 * u < padded) key[i0 + 256 * u] = k[u];
+            for (int u = 0; u < P; ++u) id[q].e[u] = i0 + u < count ? ids[i0 + u] : 0;
+        }
     }
+#pragma unroll
+    for (int q = 0; q < L; ++q)
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+            const int i0 = (t + 256 * q) * P + u;
+            if (i0 < padded) key[i0] = i0 < count ? key_of(id[q].e[u], rows) : 0xffffffffu;
+        }
     __syncthreads();
     const int i = min((int)blockIdx.x * kRankTokens + (t >> 4), count - 1);
     const bool on = (int)blockIdx.x * kRankTokens + (t >> 4) < count;
