@@ -548,6 +548,106 @@ __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
     put_row<TO, 4>(dtable + (int64_t)key * ldt, c, width, r, scale, accumulate);
 }
 
+// Short lists whose rows have few terms, in one launch: a workgroup takes the rows
+// whose terms begin in its window of the sorted tokens. Rows of up to kRowTokens
+// terms are added by one group of 2^lx lanes each, all terms on their way
+// together; longer ones after that by all groups, each a run of the terms, and
+// then the groups' sums in order. One workgroup per row is too little where a row
+// takes thousands of terms, which the sizes cannot tell but do suggest: 5000
+// tokens into 20000 x 24 take 17.4 us so, against 19.7 with partials and a fold;
+// 2000 into 5000 x 257 16.8 against 22.0; but 8192 into 50 x 24 29.6 against 23.5
+// and 8192 into 5000 x 1024 53 against 34.
+bool by_rows(int64_t rows, int64_t width, int64_t count) {
+    return count <= 1024 || (count <= kSmallCount && count <= rows && count * width <= 1 << 19);
+}
+constexpr int kRowTokens = 16;
+
+template <class TD, class TO>
+__global__ __launch_bounds__(256) void embed_grad_rows_kernel(
+    const TD* __restrict__ dout, int64_t ldd, int width, const uint32_t* __restrict__ keys,
+    const int32_t* __restrict__ pos, int count, int window, float scale, int accumulate,
+    TO* __restrict__ dtable, int64_t ldt, int64_t rows, int lx) {
+    constexpr int V = 4, K = kRowTokens;
+    __shared__ int longs[256];
+    __shared__ int nlong;
+    __shared__ float4 sums[256];
+    const int lane = threadIdx.x & ((1 << lx) - 1), grp = threadIdx.x >> lx, groups = 256 >> lx;
+    const int c = (int)((blockIdx.y << lx) + lane) * V;
+    const bool whole = c + V <= width;
+    // acc += the terms [p, p + n) of the sorted list, n <= K, in order
+    auto add = [&](float(&acc)[V], int p, int n) {
+        int32_t at[K];
+        Vec<TD, V> v[K];
+#pragma unroll
+        for (int q = 0; q < K; ++q) at[q] = q < n ? pos[p + q] : 0;
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[q].e[u] = from_f32<TD>(0.f);
+            if (q < n) {
+                const TD* src = dout + (int64_t)at[q] * ldd + c;
+                if (whole) {
+                    v[q] = load_vec<TD, V>(src);
+                } else {
+                    for (int u = 0; u < V; ++u)
+                        if (c + u < width) v[q].e[u] = src[u];
+                }
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < K; ++q)
+            if (q < n)
+#pragma unroll
+                for (int u = 0; u < V; ++u) acc[u] += to_f32(v[q].e[u]);
+    };
+    if (threadIdx.x == 0) nlong = 0;
+    __syncthreads();
+    const int w0 = (int)blockIdx.x * window;
+    for (int p = w0 + grp; p < min(w0 + window, count); p += groups) {
+        const uint32_t key = keys[p];
+        if ((int64_t)key >= rows || (p > 0 && keys[p - 1] == key)) continue;  // begins no row
+        int n = 1;
+#pragma unroll
+        for (int q = 1; q <= K; ++q) n += p + q < count && keys[p + q] == key ? 1 : 0;
+        if (n > K) {
+            if (lane == 0) longs[atomicAdd(&nlong, 1)] = p;  // rows, in any order
+        } else if (c < width) {
+            float acc[V] = {};
+            add(acc, p, n);
+            put_row<TO, V>(dtable + (int64_t)key * ldt, c, width, acc, scale, accumulate);
+        }
+    }
+    __syncthreads();
+    for (int i = 0; i < nlong; ++i) {
+        const int p = longs[i];
+        const uint32_t key = keys[p];
+        int n = 0;
+        for (;;) {
+            const int j = p + n + (int)threadIdx.x;
+            const int m = __syncthreads_count(j < count && keys[j] == key);
+            n += m;
+            if (m < 256) break;
+        }
+        const int per = (n + groups - 1) / groups, end = p + min(n, (grp + 1) * per);
+        float acc[V] = {};
+        if (c < width)
+            for (int q = p + grp * per; q < end; q += K) add(acc, q, min(K, end - q));
+        sums[threadIdx.x] = float4{acc[0], acc[1], acc[2], acc[3]};
+        __syncthreads();
+        if (grp == 0 && c < width) {
+            for (int g = 1; g < groups; ++g) {
+                const float4 o = sums[(g << lx) + lane];
+                acc[0] += o.x;
+                acc[1] += o.y;
+                acc[2] += o.z;
+                acc[3] += o.w;
+            }
+            put_row<TO, V>(dtable + (int64_t)key * ldt, c, width, acc, scale, accumulate);
+        }
+        __syncthreads();
+    }
+}
+
 template <class TI, class TO, class ID>
 hipError_t embed_run(const EmbedArgs& a, hipStream_t st) {
     constexpr int V = sizeof(TI) == 4 || sizeof(TO) == 4 ? 4 : 8;
@@ -596,7 +696,8 @@ GradLayout grad_layout(void* ws, int64_t rows, int64_t width, int64_t count) {
     const bool small = count <= kSmallCount;
     L.hist = (int32_t*)take(small ? 0 : 4 * (size_t)p.nblk << p.bits);
     L.present = (uint8_t*)take(small ? 0 : (size_t)rows);
-    L.part = (float*)take(8 * (size_t)nchunks * (size_t)L.ldpart);
+    L.part = (float*)take(by_rows(rows, width, count) ? 0
+                                                      : 8 * (size_t)nchunks * (size_t)L.ldpart);
     L.bytes = off;
     return L;
 }
@@ -684,6 +785,16 @@ hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
     // into a float32 table: 125 us against 136 with 8; rows of 1000 into a bf16
     // table: 45 against 60)
     constexpr int V = 4;
+    if (by_rows(a.rows, a.width, a.count)) {
+        // at most 32 lanes to a row: the groups share long rows between them
+        const int lx = log2_up((a.width + V - 1) / V, 5), window = 256 >> lx;
+        const dim3 g((unsigned)((a.count + window - 1) / window),
+                     (unsigned)(((a.width + V - 1) / V + (1 << lx) - 1) >> lx));
+        hipLaunchKernelGGL((embed_grad_rows_kernel<TD, TO>), g, dim3(256), 0, st,
+                           (const TD*)a.dout, a.ldd, (int)a.width, keys, pos, (int)a.count, window,
+                           a.scale, a.accumulate, (TO*)a.dtable, a.ldt, a.rows, lx);
+        return hipGetLastError();
+    }
     const int clen = chunk_len(a.count, a.width);
     const int64_t nchunks = (a.count + clen - 1) / clen;
     const int64_t nv = (a.width + V - 1) / V;

@@ -134,3 +134,28 @@ def test_scan_carries_nan_on(steps):
             bad[1, 3:, 7] = True
             assert torch.equal(torch.isnan(h), bad)
             assert torch.equal(torch.isnan(last), bad[:, -1])
+
+
+@pytest.mark.parametrize("count", [15, 16, 17, 18, 1024, 1025, 3000])
+@pytest.mark.parametrize("width", [1, 24, 130, 1025])
+def test_embed_grad_rows_of_every_length(count, width):
+    """Rows of 1, 15, 16, 17, ... terms and one of all of them, in short lists."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(count * 7 + width)
+    lengths = [1, 2, 15, 16, 17, 31, 33, 64, 200]
+    for ids in (np.zeros(count, np.int64),
+                np.repeat(np.arange(len(lengths) * 40), np.tile(lengths, 40))[:count]):
+        rows = 4000
+        ids = rng.permutation(ids * 3)
+        d, dv = base.dev(torch, rng.standard_normal((count, width)))
+        ref, mag = np.zeros((rows, width)), np.zeros((rows, width))
+        np.add.at(ref, ids, dv)
+        np.add.at(mag, ids, np.abs(dv))
+        n = np.bincount(ids, minlength=rows)[:, None]
+        tid = torch.from_numpy(ids).cuda()
+        got = api.embed_grad(d, tid, rows)
+        base.close(got, ref, (n + 2) * base.U * mag)
+        out = torch.ones(rows, width, device="cuda")
+        api.embed_grad(d, tid, rows, out=out, accumulate=True)
+        base.close(out, 1 + ref, (n + 2) * base.U * mag + 2 * base.U * (1 + mag))
