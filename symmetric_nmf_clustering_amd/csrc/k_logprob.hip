@@ -217,7 +217,8 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_ke
     const int g_end = ng > 0 && g_lo + ng == all && vocab % kGroup ? ng - 1 : ng;
     const float k = scale * kLog2e;
     Stat a = stat_none();
-    Cand mine{0, 0};
+    float best = -INFINITY;  // the thread's best group, compared as a float: its
+    int best_g = t;          // ordered key is made once, after the loop
 
     Vec<T, V> cur[Q][NV], nxt[Q][NV];
     auto fetch = [&](Vec<T, V>(&to)[Q][NV], int g0) {
@@ -246,7 +247,10 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_ke
     };
     auto keep = [&](int g, float mx) {
         gmax[g] = from_f32<T>(mx);
-        mine = best_of(Cand{ordered(mx), (uint32_t)g}, mine);
+        if (mx > best) {  // groups come in order: the first of equals stays
+            best = mx;
+            best_g = g;
+        }
     };
     fetch(cur, t);
     for (int g0 = t; g0 - t < g_end; g0 += N * Q) {
@@ -291,6 +295,8 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_ke
         take(v);
         if (top) keep(g_end, mx);
     }
+    // Groups of -inf alone are led by the first of them, so the leaders differ.
+    Cand mine{t < ng ? ordered(best) : 0u, (uint32_t)best_g};
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) a = stat_join(a, stat_shfl_xor(a, o), k);
     if (WAVES > 1) {

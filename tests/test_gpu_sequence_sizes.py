@@ -159,3 +159,29 @@ def test_embed_grad_rows_of_every_length(count, width):
         out = torch.ones(rows, width, device="cuda")
         api.embed_grad(d, tid, rows, out=out, accumulate=True)
         base.close(out, 1 + ref, (n + 2) * base.U * mag + 2 * base.U * (1 + mag))
+
+
+@pytest.mark.parametrize("vocab", [300, 2000, 8000, 20000, 100003])
+@pytest.mark.parametrize("left", [1, 2, 3, 9, 40])
+def test_top_where_few_columns_are_left(vocab, left):
+    """Rows of excluded columns but for a few, side by side, far apart or at either end."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab + left)
+    count = 40
+    zv = np.full((count, vocab), -np.inf, np.float32)
+    for i in range(count):
+        if i % 3 == 0:
+            at = rng.choice(vocab, left, replace=False)
+        elif i % 3 == 1:
+            at = int(rng.integers(0, vocab - left + 1)) + np.arange(left)
+        else:
+            at = np.arange(left) if i % 2 else vocab - 1 - np.arange(left)
+        zv[i, at] = rng.integers(-3, 4, left)
+    tok = np.zeros(count, int)
+    for dtype in (torch.float32, torch.bfloat16):
+        for top in (1, 2, 3, 7, 32):
+            r = api.token_logprobs(torch.from_numpy(zv).cuda().to(dtype), torch.from_numpy(tok).cuda(), top=top)
+            tlp, ids = so.token_logprobs(zv.astype(np.float64), tok, top, 1.0)[3:]
+            assert np.array_equal(r.top_ids.cpu().numpy(), ids), (dtype, top)
+            assert np.array_equal(np.isneginf(r.top_logp.cpu().numpy()), np.isneginf(tlp)), (dtype, top)
