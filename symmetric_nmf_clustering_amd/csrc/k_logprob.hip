@@ -128,14 +128,27 @@ __device__ __forceinline__ void stat_rescale(Stat& a, float m, float k) {
     a.s *= f;
     a.m = m;
 }
-__device__ __forceinline__ Stat stat_join(Stat a, Stat b, float k) {
-    const float m = fmaxf(a.m, b.m);
-    stat_rescale(a, m, k);
-    stat_rescale(b, m, k);
-    return {m, a.s + b.s, a.u + b.u};
+// v[op]... over the wave, in every lane (a scalar): row shifts inside each 16
+// lanes, then broadcasts across rows; lane 63 ends with it. `none` is what op
+// leaves unchanged.
+template <class F>
+__device__ __forceinline__ float wave_fold(float v, float none, F&& op) {
+    auto from = [&](auto x) { return __int_as_float(x(__float_as_int(none), __float_as_int(v))); };
+    v = op(v, from([](int o, int x) { return __builtin_amdgcn_update_dpp(o, x, 0x111, 0xf, 0xf, false); }));
+    v = op(v, from([](int o, int x) { return __builtin_amdgcn_update_dpp(o, x, 0x112, 0xf, 0xf, false); }));
+    v = op(v, from([](int o, int x) { return __builtin_amdgcn_update_dpp(o, x, 0x114, 0xf, 0xf, false); }));
+    v = op(v, from([](int o, int x) { return __builtin_amdgcn_update_dpp(o, x, 0x118, 0xf, 0xf, false); }));
+    v = op(v, from([](int o, int x) { return __builtin_amdgcn_update_dpp(o, x, 0x142, 0xf, 0xf, false); }));
+    v = op(v, from([](int o, int x) { return __builtin_amdgcn_update_dpp(o, x, 0x143, 0xf, 0xf, false); }));
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
-__device__ __forceinline__ Stat stat_shfl_xor(Stat a, int o) {
-    return {__shfl_xor(a.m, o, 64), __shfl_xor(a.s, o, 64), __shfl_xor(a.u, o, 64)};
+// The wave's statistics joined, in every lane: one rescaling to the common
+// maximum, then plain sums.
+__device__ __forceinline__ Stat stat_wave(Stat a, float k) {
+    stat_rescale(a, wave_fold(a.m, -FLT_MAX, [](float x, float y) { return fmaxf(x, y); }), k);
+    a.s = wave_fold(a.s, 0.f, [](float x, float y) { return x + y; });
+    a.u = wave_fold(a.u, 0.f, [](float x, float y) { return x + y; });
+    return a;
 }
 
 struct RowOut {
@@ -297,17 +310,13 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_ke
     }
     // Groups of -inf alone are led by the first of them, so the leaders differ.
     Cand mine{t < ng ? ordered(best) : 0u, (uint32_t)best_g};
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) a = stat_join(a, stat_shfl_xor(a, o), k);
+    a = stat_wave(a, k);
     if (WAVES > 1) {
         if (lane == 0) wst[w] = a;
         lead[t] = mine;
         __syncthreads();
         if (w != 0) return;
-        a = lane < WAVES ? wst[lane] : stat_none();
-#pragma unroll
-        for (int o = WAVES / 2; o >= 1; o >>= 1) a = stat_join(a, stat_shfl_xor(a, o), k);
-        a = {__shfl(a.m, 0, 64), __shfl(a.s, 0, 64), __shfl(a.u, 0, 64)};
+        a = stat_wave(lane < WAVES ? wst[lane] : stat_none(), k);
         mine = lead[t];
 #pragma unroll
         for (int i = 1; i < WAVES; ++i) mine = best_of(mine, lead[t + 64 * i]);
@@ -453,8 +462,7 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T* __restrict__ 
     const Cand* c = cand + (row * nslice + lane) * top;
     Stat a = on ? part[row * nslice + lane] : stat_none();
     for (int r = 0; r < top; ++r) list[r][lane] = on ? c[r] : Cand{0, 0};  // the lane's own
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) a = stat_join(a, stat_shfl_xor(a, o), k);
+    a = stat_wave(a, k);
     if (lane == 0) put_token<T>(out, a, scale, logits + row * ld, row, vocab);
     if (!top) return;
     Cand mine = list[0][lane], got{0, 0};
