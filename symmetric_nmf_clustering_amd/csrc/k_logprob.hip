@@ -561,6 +561,39 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
     });
     if (on && l == 0) put_token<T>(out, a, scale, z, row, vocab);
     if (!top) return;
+    // The lanes of the group hold one alternative each and write them together.
+    const int mask = (1 << lg) - 1;
+    Cand got{0, 0};
+    auto put = [&](int r, Cand b) {
+        if (l == (r & mask)) got = b;
+        const int first = r & ~mask;
+        if (((r & mask) == mask || r == top - 1) && on && first + l <= r)
+            put_top(out, a, scale, row, top, first + l, got);
+    };
+    if constexpr (sizeof(T) == 2) {
+        // Sixteen-bit logits: the order's upper 19 bits tell them apart (8 of exponent,
+        // 10 of mantissa at most), so value and column make one key, and the best key
+        // under the last one is last - 1 - min(last - 1 - key), where the keys from
+        // the last on wrap round to large numbers.
+        uint32_t key[NS], last = ~0u;
+#pragma unroll
+        for (int u = 0; u < NS; ++u) {
+            const int c = (l + ((u / kGroup) << lg)) * kGroup + u % kGroup;
+            key[u] = c < vocab ? (ordered(v[u]) >> 13 << 9 | (uint32_t)(kShortCols - 1 - c)) : 0u;
+        }
+        for (int r = 0; r < top; ++r) {
+            const uint32_t below = max(last, 1u) - 1;
+            uint32_t d = below;  // that of key 0: nothing
+#pragma unroll
+            for (int u = 0; u < NS; ++u) d = min(d, below - key[u]);
+            group_steps(lg, [&](auto x) { d = min(d, (uint32_t)x((int)d)); });
+            last = below - d;
+            uint32_t o = last >> 9 << 13;
+            if (last && !(o >> 31)) o |= 0x1fffu;  // negative numbers' lower bits
+            put(r, Cand{o, kShortCols - 1 - (last & (kShortCols - 1))});
+        }
+        return;
+    }
     uint32_t ord[NS];
 #pragma unroll
     for (int u = 0; u < NS; ++u) {
@@ -581,7 +614,7 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
         group_steps(lg, [&](auto x) {
             b = best_of(b, Cand{(uint32_t)x((int)b.ord), (uint32_t)x((int)b.idx)});
         });
-        if (on && l == 0) put_top(out, a, scale, row, top, r, b);
+        put(r, b);
         const int gone = own == b.idx ? bu : -1;  // the lane that held it
 #pragma unroll
         for (int u = 0; u < NS; ++u) ord[u] = u == gone ? 0u : ord[u];
