@@ -35,10 +35,8 @@ constexpr float kLn2 = 0.693147180559945309f;
 // Order of (value, column) as one number: larger is better. -0 equals 0; a NaN
 // counts as -inf.
 __device__ __forceinline__ uint32_t ordered(float v) {
-    if (!(v > -INFINITY)) v = -INFINITY;
-    v += 0.f;  // -0 -> 0
-    const uint32_t b = __float_as_uint(v);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+    const int b = __float_as_int(fmaxf(v, -INFINITY) + 0.f);  // -0 + 0 is 0
+    return (uint32_t)b ^ ((uint32_t)(b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
@@ -340,35 +338,29 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_ke
         Cand* elems = lead + kFew;  // kFew elements
         Cand low;
         int ngr = 0, nel = 0;
-        if (ng <= 64 * top) {  // look all groups over
-            if (top <= 8) {  // sixteen leaders of four lanes serve as well
-                auto quad = [&](int ctl) {
-                    Cand o;
-                    if (ctl == 0)
-                        o = Cand{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.ord, 0xB1, 0xf, 0xf, false),
-                                 (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.idx, 0xB1, 0xf, 0xf, false)};
-                    else
-                        o = Cand{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.ord, 0x4E, 0xf, 0xf, false),
-                                 (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine.idx, 0x4E, 0xf, 0xf, false)};
-                    return best_of(mine, o);
-                };
-                const Cand own = mine;
-                mine = quad(0);
-                mine = quad(1);
-                low = of_rank(mine, (lane & 3) ? 64 : rank_among(mine, 16, 4), top - 1);
-                mine = own;
+        // Sixteen leaders of four lanes serve for up to 8, 32 of two for up to 16.
+        const Cand own = mine;
+        if (top <= 16) {
+            Cand m = best_of(own, Cand{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)own.ord, 0xB1, 0xf, 0xf, false),
+                                       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)own.idx, 0xB1, 0xf, 0xf, false)});
+            if (top <= 8) {
+                m = best_of(m, Cand{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)m.ord, 0x4E, 0xf, 0xf, false),
+                                    (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m.idx, 0x4E, 0xf, 0xf, false)});
+                low = of_rank(m, (lane & 3) ? 64 : rank_among(m, 16, 4), top - 1);
             } else {
-                low = of_rank(mine, rank_among(mine, 64), top - 1);
+                low = of_rank(m, (lane & 1) ? 64 : rank_among(m, 32, 2), top - 1);
             }
+        } else {
+            low = of_rank(own, rank_among(own, 64), top - 1);
+        }
+        if (ng <= 64 * top) {  // look all groups over
             for (int g = lane; g - lane < ng; g += 64) {
                 const Cand c{g < ng ? ordered(to_f32(gmax[g])) : 0u, (uint32_t)g};
                 ngr = append(list, ngr, c.ord && !better(low, c), c);
             }
-        } else {  // look the winners' groups over
-            const int lrank = rank_among(mine, 64);
-            low = of_rank(mine, lrank, top - 1);
-            for (int r = 0; r < top; ++r) {
-                const int owner = (int)(of_rank(mine, lrank, r).idx & 63);
+        } else {  // look over the groups of the lanes whose best reaches the bound
+            for (uint64_t at = __ballot(!better(low, own)); at && ngr <= kFew; at &= at - 1) {
+                const int owner = __ffsll((unsigned long long)at) - 1;
                 for (int g = owner + 64 * lane; g - 64 * lane < ng; g += 4096) {
                     const Cand c{g < ng ? ordered(to_f32(gmax[g])) : 0u, (uint32_t)g};
                     ngr = append(list, ngr, c.ord && !better(low, c), c);
@@ -496,7 +488,14 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T* __restrict__ 
 
 // ---- short rows ------------------------------------------------------------------
 
-constexpr int kShortCols = 512;  // up to these, a row lies in the registers of a few lanes
+// Up to these columns, a row lies in the registers of a few lanes: 1024 (50000 x
+// 1000 bf16: 26.5 us, by the kernel for long rows 35.2; top 5: 47.4 and 54.0; 20000 x
+// 2000, top 5: 41.3 and 28.9). Alternatives of fp32 rows have no short key (below)
+// and stop at 512 (50000 x 1000, top 5: 74.0 us and 62.4).
+constexpr int kShortBits = 10, kShortCols = 1 << kShortBits;
+bool short_row(int64_t vocab, int top, int bytes) {
+    return vocab <= (bytes == 2 || top == 0 ? kShortCols : kShortCols / 2);
+}
 
 // Exchanges across a group of 2^lg lanes, one step per bit, for reductions that
 // leave every lane of the group with the result: within 16 lanes by lane
@@ -574,12 +573,13 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
         // Sixteen-bit logits: the order's upper 19 bits tell them apart (8 of exponent,
         // 10 of mantissa at most), so value and column make one key, and the best key
         // under the last one is last - 1 - min(last - 1 - key), where the keys from
-        // the last on wrap round to large numbers.
+        // the last on wrap round to large numbers. Places past the row count as -inf.
         uint32_t key[NS], last = ~0u;
 #pragma unroll
         for (int u = 0; u < NS; ++u) {
             const int c = (l + ((u / kGroup) << lg)) * kGroup + u % kGroup;
-            key[u] = c < vocab ? (ordered(v[u]) >> 13 << 9 | (uint32_t)(kShortCols - 1 - c)) : 0u;
+            const uint32_t o = ordered(v[u]) >> (13 - kShortBits);
+            key[u] = (o & -(1u << kShortBits)) | (uint32_t)(kShortCols - 1 - c);
         }
         for (int r = 0; r < top; ++r) {
             const uint32_t below = max(last, 1u) - 1;
@@ -588,7 +588,7 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
             for (int u = 0; u < NS; ++u) d = min(d, below - key[u]);
             group_steps(lg, [&](auto x) { d = min(d, (uint32_t)x((int)d)); });
             last = below - d;
-            uint32_t o = last >> 9 << 13;
+            uint32_t o = last >> kShortBits << 13;
             if (last && !(o >> 31)) o |= 0x1fffu;  // negative numbers' lower bits
             put(r, Cand{o, kShortCols - 1 - (last & (kShortCols - 1))});
         }
@@ -700,7 +700,7 @@ SlicePlan slice_plan(int64_t vocab, int64_t count, int bytes) {
 template <class T>
 hipError_t logprobs_run(const LogprobArgs& a, hipStream_t st) {
     const RowOut o{a.tokens, a.token_type, a.logp, a.entropy, a.lse, a.top_logp, a.top_ids};
-    if (a.vocab <= kShortCols) {
+    if (short_row(a.vocab, a.top, sizeof(T))) {
         // as few lanes a row as hold it with 32 columns each (24 columns: one lane)
         int lg = 0;
         while ((int64_t)32 << lg < a.vocab) ++lg;
@@ -769,7 +769,7 @@ hipError_t grad_run(const LogprobArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t logprob_ws_bytes(int64_t vocab, int top, int64_t count) {
-    if (vocab <= kShortCols || count == 0) return 256;
+    if (count == 0 || short_row(vocab, top, 4)) return 256;  // 4: any type
     const int64_t n = std::max(slice_plan(vocab, count, 2).nslice, slice_plan(vocab, count, 4).nslice);
     if (n < 2) return 256;
     return ((size_t)(count * n) * sizeof(Stat) + 255) / 256 * 256 +

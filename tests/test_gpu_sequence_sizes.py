@@ -185,3 +185,42 @@ def test_top_where_few_columns_are_left(vocab, left):
             tlp, ids = so.token_logprobs(zv.astype(np.float64), tok, top, 1.0)[3:]
             assert np.array_equal(r.top_ids.cpu().numpy(), ids), (dtype, top)
             assert np.array_equal(np.isneginf(r.top_logp.cpu().numpy()), np.isneginf(tlp)), (dtype, top)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("vocab", [511, 512, 513, 1000, 1023, 1024, 1025])
+@pytest.mark.parametrize("top", [0, 1, 32])
+def test_token_logprobs_around_the_register_plans(kind, vocab, top):
+    if top:
+        return test_token_logprobs_plans(kind, 37, vocab, top)
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab * 3 + 37)
+    z = (rng.standard_normal((37, vocab)) * 3).astype(np.float32)
+    z[1::4, ::3] = -np.inf
+    t, zv = base.dev(torch, z, kind)
+    tok = rng.integers(-1, vocab, size=37)
+    r = api.token_logprobs(t, torch.from_numpy(tok).cuda(), top=0)
+    logp, h, lse = so.token_logprobs(zv, tok, 0, 1.0)[:3]
+    bl, bh = base.logprob_bounds(zv, 1.0, lse)
+    base.close(r.logp, logp, bl)
+    base.close(r.entropy, h, bh)
+    base.close(r.lse, lse, bl)
+    assert r.top_ids is None and r.top_logp is None
+
+
+@pytest.mark.parametrize("vocab", [900, 4000, 40000])
+@pytest.mark.parametrize("top", [8, 9, 16, 17])
+def test_top_of_tied_rows_at_every_number_of_leaders(vocab, top):
+    """Small whole numbers: every value many times, ties taken in column order."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab + top)
+    zv = rng.integers(-30, 1, size=(9, vocab)).astype(np.float64)
+    zv[1::2] = np.where(rng.random((4, vocab)) < 20.0 / vocab, zv[1::2] + 50, zv[1::2])
+    zv[2, :] = np.where(rng.random(vocab) < 0.5, 0.0, -0.0)
+    tok = np.zeros(9, int)
+    ids = so.token_logprobs(zv, tok, top, 1.0)[4]
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        r = api.token_logprobs(torch.from_numpy(zv).cuda().to(dtype), torch.from_numpy(tok).cuda(), top=top)
+        assert np.array_equal(r.top_ids.cpu().numpy(), ids), dtype
