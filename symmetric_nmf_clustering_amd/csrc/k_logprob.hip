@@ -343,8 +343,8 @@ __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_ke
     // `top`-th best leader bounds the `top`-th best group and element from
     // below, so groups from it on, and their elements that reach its value, hold
     // all that is wanted. Mostly those are few enough for a lane each, and then
-    // counting who is better ranks them at once (20 of 2048 columns: 13.1 us for
-    // the kernel against 18.9 picking one by one).
+    // counting who is better ranks them at once (20000 x 2000, top 20:
+    // 46.7 us; picking one by one 88.9. 16 x 100000: 20.9 and 27.7).
     {
         Cand* list = lead;        // kFew groups
         Cand* elems = lead + kFew;  // kFew elements
@@ -686,13 +686,13 @@ struct SlicePlan {
     int waves, groups, nslice;
 };
 // A slice's waves: one up to these groups (16 a lane; four slices then share a
-// workgroup: 10000 x 4000 bf16 39 us against 52 with four waves), else four, or
-// sixteen where there are few rows (256 x 100000: 24.5 us against 28.9).
+// workgroup: 10000 x 4000 bf16 27.5 us against 34.0 with four waves), else four, or
+// sixteen where there are few rows (256 x 100000: 23.2 us against 28.1).
 constexpr int kWaveGroups = 1024;
 constexpr int64_t kFewRows = 256;
 // Rows are cut only where they are so few and so long that most of the chip would
 // idle: into about kItems slices altogether, joined by a second launch (16 x
-// 100000 bf16, top 20: 18.8 us, whole 31.3; 64 x 32768: 20.8 us, whole 18.7).
+// 100000 bf16, top 20: 20.9 us, whole 28.6; 64 x 32768: 21.8 us, whole 17.6).
 constexpr int64_t kCutRows = 64, kCutBytes = 64 << 10, kItems = 1024;
 
 // Whole rows fit a slice up to 256 KiB with four waves, 1 MiB with sixteen (the

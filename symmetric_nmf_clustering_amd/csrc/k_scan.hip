@@ -555,7 +555,7 @@ constexpr int kMaxSeg = 256;
 // The forward is cut early: its uncut workgroups keep too little in flight. The
 // backward reads three arrays and writes two, so reading two of them twice only
 // pays where most of the chip would idle (8 x 2048 x 2048 bf16 as 256 workgroups:
-// 88 us, cut into 512: 116, into 1024: 118).
+// 80.2 us, cut into 512: 86.0, into 1024: 88.6).
 constexpr int kCut = 256, kFill = 2048, kCutGrad = 256, kFillGrad = 1024;
 constexpr int kWalkSteps = 8;  // up to these, steps are walked one by one
 
@@ -621,10 +621,10 @@ hipError_t grad_run(const ScanArgs& a, hipStream_t st) {
 }
 
 // Channels to a lane, 8 bytes of them. 16 bytes put fewer steps into a thread and
-// more maps into the scan across lanes, 4 bytes take more loads: 2 x 32768 x 1024
-// bf16 in 153 us, with 16 bytes in 175, with 4 in 156; 250 x 100000 fp32 in 48.6,
-// 48.8 and 80.8. The backward holds more per element: 8 x 2048 x 2048 bf16 with 4
-// bytes in 88 us, with 8 in 97.
+// more maps into the scan across lanes, 4 bytes take more loads: 250 x 100000 fp32
+// in 47.7 us, with 16 bytes in 68.5, with 4 in 50.5; 2 x 32768 x 1024 bf16 in 141.6,
+// with 4 in 142.5. The backward holds more per element: 8 x 2048 x 2048 bf16 with 4
+// bytes in 80.2 us, with 8 in 93.0.
 template <class T>
 hipError_t scan_vec(const ScanArgs& a, hipStream_t st) {
     constexpr int W = 16 / sizeof(T), V = 8 / sizeof(T);
