@@ -224,3 +224,66 @@ def test_top_of_tied_rows_at_every_number_of_leaders(vocab, top):
     for dtype in (torch.float32, torch.bfloat16, torch.float16):
         r = api.token_logprobs(torch.from_numpy(zv).cuda().to(dtype), torch.from_numpy(tok).cuda(), top=top)
         assert np.array_equal(r.top_ids.cpu().numpy(), ids), dtype
+
+
+def test_offsets_past_32_bits():
+    """Rows, steps and outputs that lie more than 2^32 bytes and 2^31 elements apart
+    give the bits that packed ones give."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    room = torch.empty(2_500_000_000, dtype=torch.bfloat16, device="cuda")
+
+    def apart(packed, strides):
+        v = room.as_strided(packed.shape, strides)
+        v.copy_(packed)
+        return v
+
+    def noise(*shape):
+        return torch.randn(shape, generator=gen, device="cuda").bfloat16()
+
+    # logits and their gradient, three rows
+    for vocab in (700, 5000, 70001):
+        z = noise(3, vocab)
+        tok = torch.tensor([1, vocab - 1, 7], device="cuda")
+        w = torch.randn(3, generator=gen, device="cuda")
+        one = api.token_logprobs(z, tok, top=5)
+        d1 = api.token_logprobs_grad(z, tok, one.lse, one.entropy, w, dentropy=w)
+        far = apart(z, (1_200_000_000, 1))
+        two = api.token_logprobs(far, tok, top=5)
+        for a, b in ((one.logp, two.logp), (one.lse, two.lse), (one.top_ids, two.top_ids), (one.top_logp, two.top_logp)):
+            assert torch.equal(a, b)
+        api.token_logprobs_grad(far, tok, two.lse, two.entropy, w, dentropy=w, out=far)
+        assert torch.equal(far, d1)
+
+    # a table's rows, the rows of its gradient's terms
+    t = noise(3, 1000)
+    ids = torch.tensor([2, 0, 1, 2, 2], device="cuda")
+    assert torch.equal(api.embed(apart(t, (1_200_000_000, 1)), ids), api.embed(t, ids))
+    d = noise(5, 1000)
+    assert torch.equal(api.embed_grad(apart(d, (600_000_000, 1)), ids, 3), api.embed_grad(d, ids, 3))
+
+    # steps and batch rows
+    x, g = noise(2, 300, 64), noise(2, 300, 64)
+    h, last, st = api.gated_scan(x, g, return_states=True)
+    dx, dg, dh0 = api.gated_scan_grad(x, g, st, x)
+    for strides in ((64, 8_000_000, 1), (2_400_000_000, 64, 1)):
+        far = apart(x, strides)
+        h2, last2, st2 = api.gated_scan(far, g, return_states=True)
+        assert torch.equal(h, h2) and torch.equal(last, last2) and torch.equal(st, st2)
+        for a, b in zip((dx, dg, dh0), api.gated_scan_grad(far, g, st, far)):
+            assert torch.equal(a, b)
+        far = apart(g, strides)
+        assert torch.equal(api.gated_scan(x, far)[0], h)
+    del room, far
+
+    # outputs
+    table = noise(11, 2048)
+    many = torch.arange(1_100_000, device="cuda") % 11
+    out = api.embed(table, many)
+    assert torch.equal(out[-11:], table[many[-11:]])
+    del out
+    x = noise(1, 1000, 65536)
+    h = api.gated_scan(x.expand(34, -1, -1), x.expand(34, -1, -1))[0]
+    assert torch.equal(h[33], h[0])
+    assert torch.equal(h[0], api.gated_scan(x, x)[0][0])
