@@ -418,7 +418,19 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
 
     Vec<T, V> xv[R], gv[R], dv[R];
     float hs[V];
-    const int ntile = (q.t_hi - q.t_lo + tt - 1) / tt;
+    // The tiles that hold a step that counts; those after them are zeros, and m
+    // passes them (8 x 2048 x 2048 bf16, ragged: 72.5 us, walked like the others 82.0).
+    const int ntile = q.lim > q.t_lo ? (q.lim - q.t_lo + tt - 1) / tt : 0;
+    if (MODE == 0 && on) {
+        Vec<T, V> zero;
+#pragma unroll
+        for (int u = 0; u < V; ++u) zero.e[u] = from_f32<T>(0.f);
+        for (int t = q.t_lo + ntile * tt + q.grp; t < q.t_hi; t += 256 >> tl.cl_log2) {
+            const int64_t to = (q.b * p.steps + t) * p.width + q.c0;
+            store_vec<T, V>((T*)p.dx + to, zero);
+            store_vec<T, V>((T*)p.dgate + to, zero);
+        }
+    }
     const int64_t t_end = q.t_lo + (ntile - 1) * (int64_t)tt + q.grp * R;  // in the last tile
     const T* px = x + t_end * p.x_t;
     const T* pg = g + t_end * p.g_t;
@@ -515,8 +527,11 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
                     for (int u = 0; u < V; ++u) {
                         const float lam = min_[u] + df[r][u];
                         const float lc = lam * c[r][u];
-                        vx.e[u] = from_f32<T>(lc);
-                        vg.e[u] = from_f32<T>(lc * a[r][u] * xf[r][u]);
+                        // by the step, not by its c of 0: what passes a masked
+                        // step may be infinite or NaN
+                        const bool in = !masked || ts + r < q.lim;
+                        vx.e[u] = from_f32<T>(in ? lc : 0.f);
+                        vg.e[u] = from_f32<T>(in ? lc * a[r][u] * xf[r][u] : 0.f);
                         min_[u] = a[r][u] * lam;
                     }
                     if (!masked || ts + r < q.t_hi) {
@@ -527,7 +542,7 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
                     wg = next_step(wg, -p.width);
                 }
             };
-            if (t0 + tt <= q.t_hi)
+            if (t0 + tt <= q.lim)
                 put(std::false_type{});
             else
                 put(std::true_type{});
