@@ -399,7 +399,8 @@ int symnmf_embed_grad(const void* dout, int dout_type, int64_t count, int64_t wi
  *     state before the first step and after the last one.
  *   states (nullable): batch x ceil(steps / 128) x width float32, the state
  *     before every 128th step, which the gradient starts from.
- * A gate of -inf drops the state (h_t = x_t), one of +inf keeps it. One step
+ * A gate of -inf drops a finite state (h_t = x_t), one of +inf keeps it; a
+ * state that is infinite or NaN stays so or turns NaN (0 times inf). One step
  * of a live stream is steps = 1 with h0 and h_last; h0 and h_last may be the
  * same buffer then. Time is scanned in parallel with a fixed order of
  * operations. 1 <= batch <= 65535, steps >= 0.

@@ -22,13 +22,14 @@
 namespace symnmf {
 namespace {
 
-// a = sigmoid(g) and c = sigmoid(-g), each with full relative accuracy
-// (1 - a would lose c's where a is near 1). exp(-g) is held below 2^100 so that
-// c stays 1 where a underflows (by the minimum that keeps NaN).
+// a = sigmoid(g) and c = sigmoid(-g), each to (8 + 2 |g|) 2^-24 relative: the
+// exponential's argument is rounded once, its factor log2(e) is a float (1 - a
+// would lose c where a is near 1). Below 2^-126 either may be 0, and a is 0 at
+// g = -inf, where e is infinite and c is 1 by choice (NaN fails the comparison).
 __device__ __forceinline__ void gates(float g, float& a, float& c) {
-    const float e = __builtin_elementwise_minimum(__expf(-g), 1.2676506e30f);
+    const float e = __expf(-g);
     a = __builtin_amdgcn_rcpf(1.f + e);
-    c = e * a;
+    c = e > 1.2676506e30f ? 1.f : e * a;  // 2^100: 1 + e is e there
 }
 
 constexpr int kTileCh = 64;  // channels of a tile, unless the steps are few

@@ -47,3 +47,48 @@ def test_masked_steps_of_the_scan_gradient_are_zero_whatever_passes_them(batch, 
     assert torch.equal(got[2][:, 5:], want[2][:, 5:])
     assert torch.equal(got[2][0], pl[0]) or torch.isnan(pl[0, 2])  # row 0 has no step
     assert torch.equal(got[2][0, [0, 1, 3]], pl[0, [0, 1, 3]]) and torch.isnan(got[2][0, 2])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("steps", [1, 5, 9, 200, 2500])
+def test_a_gate_of_minus_infinity_drops_every_finite_state(steps, kind):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    gen = torch.Generator(device="cuda").manual_seed(steps)
+    x, dh = (torch.randn(2, steps, 12, generator=gen, device="cuda").to(base.types(torch)[kind]) for _ in range(2))
+    big = torch.full((2, 12), 3e38, device="cuda")
+    for gate in (torch.full_like(x, -INF), torch.full_like(x[0, 0], -INF).expand(2, steps, 12)):
+        h, last, st = api.gated_scan(x, gate, h0=big, return_states=True)
+        assert torch.equal(h, x) and torch.equal(last, x[:, -1].float())
+        # and nothing of later steps' gradients reaches earlier ones
+        dx, dgate, dh0 = api.gated_scan_grad(x, gate, st, dh, dh_last=big * 0)
+        assert torch.equal(dx, dh) and not dgate.any() and not dh0.any()
+        assert not torch.isnan(dgate).any()
+
+
+def test_gates_over_their_whole_range():
+    """a and c = 1 - a to (8 + 2 |g|) u each; below 2^-126 they may be 0."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    g = np.concatenate([np.linspace(-110, 110, 4401), [-3e38, 3e38, -1e4, 1e4, -88.8, 88.8, 0.0, -0.0]])
+    t, gv = base.dev(torch, g)
+    width = g.size
+    one, none = torch.full((1, width), 2.0 ** 96, device="cuda"), torch.zeros(1, width, device="cuda")
+    rel = (8 + 2 * np.minimum(np.abs(gv), 128)) * base.U  # the exponential's argument, and log2(e), to u each
+    for steps in (1, 9):  # walked, and as a tile of which one step counts
+        n = torch.ones(1, dtype=torch.int32, device="cuda")
+        gate = t.expand(1, steps, width)
+        ones = one.expand(1, steps, width)
+        for x, h0, ref in ((none.expand(1, steps, width), one, so.sigmoid(gv)), (ones, none, so.sigmoid(-gv))):
+            got = api.gated_scan(x, gate, h0=h0, lengths=n)[1][0].double().cpu().numpy() * 2.0 ** -96
+            assert (np.abs(got - ref) <= rel * ref + 2.0 ** -126).all()
+    # the gate's gradient falls off with a and c
+    x, h0 = torch.zeros(1, 9, width, device="cuda"), torch.full((1, width), 2.0 ** 60, device="cuda")
+    dh = torch.zeros(1, 9, width, device="cuda")
+    dh[:, 0] = 2.0 ** 60
+    gate = t.expand(1, 9, width)
+    n = torch.ones(1, dtype=torch.int32, device="cuda")
+    st = api.gated_scan(x, gate, h0=h0, lengths=n, return_states=True)[2]
+    dg = api.gated_scan_grad(x, gate, st, dh, lengths=n)[1][0, 0].double().cpu().numpy() * 2.0 ** -120
+    ref = so.sigmoid(gv) * so.sigmoid(-gv)
+    assert (np.abs(dg - ref) <= (2 * rel + 4 * base.U) * ref + 2.0 ** -126 + 2.0 ** -149).all()
