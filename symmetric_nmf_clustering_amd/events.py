@@ -106,11 +106,13 @@ class EventModel:
 
 
 def next_labels(ids, labels, lengths=None):
-    """Cluster label of each event's successor (-1 after a stream's last one)."""
+    """Cluster label of each event's successor (-1 after a stream's last one, and
+    where the successor is an empty slot)."""
     import torch
 
     nxt = torch.full_like(ids, -1)
-    nxt[:, :-1] = labels.long()[ids[:, 1:].clamp_min(0)]
+    after = ids[:, 1:]
+    nxt[:, :-1] = torch.where(after < 0, -1, labels.to(ids.dtype)[after.clamp_min(0).long()])
     if lengths is not None:
         t = torch.arange(ids.shape[1], device=ids.device)[None, :]
         nxt[t >= lengths[:, None] - 1] = -1

@@ -94,3 +94,17 @@ def test_training_learns_the_streams():
     assert 0.0 < r["after"]["entropy"] < np.log(4)
     again = events.run()
     assert again == r                                   # the same bits on every run
+
+
+def test_next_labels_of_empty_slots():
+    """No label follows where the next slot is empty, with lengths and without."""
+    import torch
+    lab = torch.tensor([5, 6, 7], dtype=torch.int32)
+    for dtype in (torch.int64, torch.int32):
+        ids = torch.tensor([[0, 1, 2], [2, -1, -1], [1, -1, 0], [-1, 2, 1], [-1, -1, -1]], dtype=dtype)
+        got = events.next_labels(ids, lab)
+        assert got.dtype == dtype
+        assert got.tolist() == [[6, 7, -1], [-1, -1, -1], [-1, 5, -1], [7, 6, -1], [-1, -1, -1]]
+        lengths = torch.tensor([2, 1, 3, 3, 0])
+        assert events.next_labels(ids, lab, lengths).tolist() == \
+            [[6, -1, -1], [-1, -1, -1], [-1, 5, -1], [7, 6, -1], [-1, -1, -1]]
