@@ -80,8 +80,10 @@ def log_softmax(logits, scale):
         m = z.max(axis=1, keepdims=True)
         m = np.where(np.isneginf(m), 0.0, m)
         e = np.exp(z - m)
-        lse = m[:, 0] + np.log(e.sum(axis=1))
-        lp = np.where(np.isneginf(z), -np.inf, z - lse[:, None])
+        ls = np.log(e.sum(axis=1))
+        lse = m[:, 0] + ls
+        # not z - lse, which loses ls where m is of the order of 1e16 and more
+        lp = np.where(np.isneginf(z), -np.inf, (z - m) - ls[:, None])
         p = np.exp(lp)
         h = -np.where(p > 0, p * lp, np.where(np.isnan(p), np.nan, 0.0)).sum(axis=1)
     return lp, lse, h

@@ -80,3 +80,10 @@ def test_logprobs_grad_matches_differences():
         logp, h, *_ = so.token_logprobs(z, tok, 0, 0.7)
         return (w * logp).sum() + (q * h).sum()
     assert np.abs(differences(f, z) - so.token_logprobs_grad(z, tok, w, q, 0.7)).max() < TOL
+
+
+def test_log_softmax_of_rows_of_the_lowest_value():
+    """Every column alike, however far from zero the row lies."""
+    for low in (np.finfo(np.float32).min, -65504.0, 0.0, 3e38):
+        lp, lse, h = so.log_softmax(np.full((2, 5), low), 1.0)
+        assert np.allclose(lp, -np.log(5), rtol=1e-12) and np.allclose(h, np.log(5), rtol=1e-12)
