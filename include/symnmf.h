@@ -450,7 +450,10 @@ int symnmf_token_logprobs(const void* logits, int type, int64_t count, int64_t v
  *   dlogits_j = scale (dlogp ([j = token] - p_j) - dentropy p_j (ln p_j + entropy)),
  * in the logits' type (count x vocab, ld ldd; it may be the logits' own
  * buffer with ldd = ld). Rows without a token have the entropy's part alone, rows with
- * no column left are zero. The alternatives carry no gradient.
+ * no column left are zero. The alternatives carry no gradient. lse's rounding
+ * costs ln p at most 2^-18 however far from zero the logits lie: where |lse| > 64
+ * the row is read again for what it took (but an lse that is not that of these
+ * columns is used as it is, and costs |lse| 2^-24).
  * Errors: E_INVALID, E_HIP. */
 int symnmf_token_logprobs_grad(const void* logits, int type, int64_t count, int64_t vocab,
                                int64_t ld, const void* tokens, int token_type, float scale,

@@ -637,7 +637,8 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.T
                         out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient at the logits from the gradients at ``token_logprobs``'s logp
     and (optionally) entropy, with its lse and entropy. In the logits' type;
-    ``out`` may be the logits themselves."""
+    ``out`` may be the logits themselves. Rows far from zero (|lse| > 64) are
+    read twice, for the bits that lse's rounding took."""
     lt = _seq_tensor(logits, "logits")
     ld = _rows_ld(logits, "logits")
     n, vocab = logits.shape

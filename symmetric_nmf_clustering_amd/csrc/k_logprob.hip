@@ -642,6 +642,61 @@ __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict_
 // Rows of few columns share a workgroup, 2^lx lanes to each. Accesses start at
 // 16-byte boundaries where the rows of both arrays allow it (`aligned`; 2048 x
 // 100003 bf16: 153 us, from the rows' own starts 171).
+//
+// ln p = scale z - lse takes lse's rounding into p: |lse| 2^-24 of it. Up to
+// kLseFar that is 4e-6 at most; past it the row is read again for its M and ln s,
+// which keep those bits as in the forward, in ln p = scale (z - M) - ln s. They
+// are taken where they round to the lse given (or, where scale M overflows, to
+// its infinity), so an lse of more columns than these stays what it was given
+// for. Such a row is one wave's or one workgroup's (the first of those that share
+// it), which has read it when it begins to write, since it may write in place
+// (bf16, near and far: 50000 x 500 25 and 45 us, 2048 x 100003 155 and 320, 16 x
+// 100000 11 and 43).
+constexpr float kLseFar = 64.f;
+
+// M and s of a row (u is not needed), by the n lanes of t = 0 ... n - 1 that share
+// it: up to 64 of one wave, or a workgroup's 256. All have read when it returns.
+template <class T>
+__device__ Stat row_again(const T* z, int64_t vocab, float k, int t, int n) {
+    __shared__ Stat wst[4];
+    constexpr int V = 16 / sizeof(T);
+    Stat a = stat_none();
+    for (int64_t c = (int64_t)t * V; c < vocab; c += (int64_t)n * V) {
+        float v[V], m = a.m;
+#pragma unroll
+        for (int u = 0; u < V; ++u) v[u] = -INFINITY;
+        if (c + V <= vocab) {
+            const Vec<T, V> x = load_vec<T, V>(z + c);
+#pragma unroll
+            for (int u = 0; u < V; ++u) v[u] = to_f32(x.e[u]);
+        } else {
+            for (int u = 0; u < V; ++u)
+                if (c + u < vocab) v[u] = to_f32(z[c + u]);
+        }
+#pragma unroll
+        for (int u = 0; u < V; ++u) m = fmaxf(m, v[u]);
+        if (m > a.m) stat_rescale(a, m, k);
+#pragma unroll
+        for (int u = 0; u < V; ++u) a.s += __builtin_amdgcn_exp2f(k * (v[u] - a.m));
+    }
+    auto join = [&](float m, float s) {
+        const float both = fmaxf(a.m, m);
+        stat_rescale(a, both, k);
+        a.s += s * __builtin_amdgcn_exp2f(k * (m - both));
+    };
+    for (int o = 1; o < min(n, 64); o <<= 1) {
+        const float m = __shfl_xor(a.m, o, 64), s = __shfl_xor(a.s, o, 64);
+        join(m, s);
+    }
+    if (n > 64) {
+        if ((t & 63) == 0) wst[t >> 6] = a;
+        __syncthreads();
+        a = wst[0];
+        for (int w = 1; w < 4; ++w) join(wst[w].m, wst[w].s);
+    }
+    return a;
+}
+
 template <class T>
 __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int aligned, int lx) {
     constexpr int V = 16 / sizeof(T);
@@ -654,18 +709,32 @@ __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int al
     const int64_t tok = p.token_type == kI32 ? (int64_t)((const int32_t*)p.tokens)[row]
                                              : ((const int64_t*)p.tokens)[row];
     const float w = tok < 0 ? 0.f : tok < p.vocab ? p.dlogp[row] : __builtin_nanf("");
-    const bool empty = lse == -INFINITY;
+    bool empty = lse == -INFINITY;
+    float ref = 0.f, off = lse;  // ln p = scale (z - ref) - off
+    // this lane among those that share the row, and how many they are
+    int t = (int)(threadIdx.x & ((1 << lx) - 1)) + ((int)blockIdx.x << lx);
+    int n = (int)gridDim.x << lx;
+    if (fabsf(lse) > kLseFar) {  // a row's lanes agree
+        n = lx == 7 ? 64 : 1 << lx;
+        if (t >= n) return;  // whole waves or whole workgroups
+        const Stat a = row_again<T>(z, p.vocab, scale * kLog2e, t, n);
+        const float ls = __logf(a.s), full = fmaf(scale, a.m, ls);
+        if (a.s > 0.f && (full == lse || fabsf(full - lse) <= fabsf(lse) * 4.7683716e-7f)) {  // 2^-21
+            ref = a.m;
+            off = ls;
+            empty = false;
+        }
+    }
     const int sh = aligned ? (int)((reinterpret_cast<uintptr_t>(z) % 16) / sizeof(T)) : 0;
     auto one = [&](float v, int64_t c) {
-        const float lp = fmaf(scale, v, -lse);
-        const float pr = __builtin_amdgcn_exp2f(lp * kLog2e);
+        const float lp = fmaf(scale, v - ref, -off);
+        // as a square: p below 2^-126, which ln p + H may lift above it, is not flushed
+        const float root = __builtin_amdgcn_exp2f(lp * (0.5f * kLog2e)), pr = root * root;
         float g = -pr * (w + q * (fmaxf(lp, -1e30f) + h));
         if (c == tok) g += w;
         return empty ? 0.f : scale * g;
     };
-    const int64_t step = ((int64_t)gridDim.x << lx) * V;
-    for (int64_t c = (((int64_t)blockIdx.x << lx) + (threadIdx.x & ((1 << lx) - 1))) * V - sh;
-         c < p.vocab; c += step) {
+    for (int64_t c = (int64_t)t * V - sh; c < p.vocab; c += (int64_t)n * V) {
         if (c >= 0 && c + V <= p.vocab) {
             const Vec<T, V> v = load_vec<T, V>(z + c);
             Vec<T, V> o;

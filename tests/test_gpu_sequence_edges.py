@@ -92,3 +92,85 @@ def test_gates_over_their_whole_range():
     dg = api.gated_scan_grad(x, gate, st, dh, lengths=n)[1][0, 0].double().cpu().numpy() * 2.0 ** -120
     ref = so.sigmoid(gv) * so.sigmoid(-gv)
     assert (np.abs(dg - ref) <= (2 * rel + 4 * base.U) * ref + 2.0 ** -126 + 2.0 ** -149).all()
+
+
+def check_grad_anywhere(zv, tok, w, q, scale, got, kind):
+    """As check_grad, with an error of ln p that knows no lse: (|ln p| + 8) 4 u for
+    its own rounding, at most 64 u where a small lse was rounded, and the sum's
+    (logprob_bounds)."""
+    lp, lse, h = so.log_softmax(zv, scale)
+    p = np.exp(lp)
+    wv, qv = w.double().cpu().numpy()[:, None], q.double().cpu().numpy()[:, None]
+    core, bh = (b[:, None] for b in np.broadcast_arrays(*base.logprob_bounds(0 * np.ones(zv.shape), 1.0, np.zeros(len(zv)))))
+    lp = np.where(np.isfinite(lp), lp, 0)
+    ep = (np.abs(lp) + 8 + 64) * 4 * base.U + core
+    bound = scale * (p * (np.abs(wv) + np.abs(qv) * (np.abs(lp) + h[:, None])) * (ep + 8 * base.U)
+                     + np.abs(qv) * p * (ep + bh)
+                     + 4 * base.U * np.abs(wv) * (np.arange(zv.shape[1])[None] == tok[:, None]))
+    base.close(got, so.token_logprobs_grad(zv, tok, wv[:, 0], qv[:, 0], scale), bound, kind)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("count,vocab", [(5, 2), (70, 24), (9, 512), (6, 1003), (5, 2600), (5, 8200), (3, 20011)])
+def test_logit_gradient_of_rows_far_from_zero(count, vocab, kind):
+    """A common offset of the logits changes nothing, and neither does a mask of
+    the type's lowest value (for a whole row: every column alike)."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab)
+    low = torch.finfo(base.types(torch)[kind]).min
+    z = rng.standard_normal((count, vocab)) * 3
+    z[::3, 1:][rng.random(z[::3, 1:].shape) < 0.5] = -np.inf
+    at = np.broadcast_to(np.arange(vocab), z.shape)
+    one, third = at == 1, at % 3 == 1
+    rows = {"offset 50": z + 50, "offset 3000": z + 3000, "offset -30000": z - 30000,
+            "confident": np.where(one, 3020.0, 3000.0),
+            "lowest": np.full_like(z, low), "lowest but one": np.where(one, 0.0, low),
+            "lowest and none": np.where(third, -np.inf, low),
+            "highest": np.where(one, 0.0, -low)}
+    tok = rng.integers(-1, vocab, size=count)
+    dtok = torch.from_numpy(tok).cuda()
+    w, q = (torch.from_numpy(rng.standard_normal(count).astype(np.float32)).cuda() for _ in range(2))
+    for name, r in rows.items():
+        t, zv = base.dev(torch, r, kind)
+        for scale in (1.0, 0.7, 4.0):
+            f = api.token_logprobs(t, dtok, scale=scale)
+            d = api.token_logprobs_grad(t, dtok, f.lse, f.entropy, w, dentropy=q, scale=scale)
+            check_grad_anywhere(zv, tok, w, q, np.float64(np.float32(scale)), d, kind)
+            own = t.clone()
+            api.token_logprobs_grad(own, dtok, f.lse, f.entropy, w, dentropy=q, scale=scale, out=own)
+            assert torch.equal(own, d), name
+
+
+def test_logit_gradient_takes_the_normaliser_it_is_given():
+    """The columns in two parts, each with the whole row's lse and entropy."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(9)
+    for offset in (0.0, 3000.0):
+        for vocab in (40, 700, 12000):
+            z, zv = base.dev(torch, rng.standard_normal((6, vocab)) + offset)
+            tok = np.array([0, 1, vocab - 1, vocab // 2, -1, 5])
+            dtok = torch.from_numpy(tok).cuda()
+            w, q = (torch.from_numpy(rng.standard_normal(6).astype(np.float32)).cuda() for _ in range(2))
+            f = api.token_logprobs(z, dtok)
+            half = vocab // 2
+            parts = []
+            for lo, hi in ((0, half), (half, vocab)):
+                at = torch.where((dtok >= lo) & (dtok < hi), dtok - lo, hi - lo - 1)
+                here = ((dtok >= lo) & (dtok < hi)).float()
+                d = api.token_logprobs_grad(z[:, lo:hi], at, f.lse, f.entropy, w, dentropy=q)
+                # rows whose token lies in the other part: its one-hot put back
+                fix = torch.zeros_like(d)
+                fix[torch.arange(6, device="cuda"), at] = torch.where(dtok < 0, 0.0, 1.0) * w * (here - 1)
+                fix[dtok < 0, at[dtok < 0]] = -w[dtok < 0]
+                parts.append((d + fix, at))
+            p = torch.softmax(z.double(), 1)
+            ref = so.token_logprobs_grad(zv, np.maximum(tok, -1), w.double().cpu().numpy(), q.double().cpu().numpy(), 1.0)
+            ref[4] -= (w[4].double() * p[4]).cpu().numpy()  # its parts were given a token
+            got = torch.cat([a for a, _ in parts], 1).double().cpu().numpy()
+            # p relative to 4 u (|lse| + |ln p| + 8), the one-hot's cancellation to 4 u
+            lp = np.log(np.exp(zv - zv.max(1, keepdims=True)).sum(1)).max() + np.ptp(zv)
+            ep = (offset + 2 * lp + 16) * 4 * base.U
+            wq = (w.abs() + q.abs() * 40).double().cpu().numpy()[:, None]
+            assert (np.abs(got - ref) <= wq * (p.cpu().numpy() * ep * 2 + 8 * base.U)).all()
