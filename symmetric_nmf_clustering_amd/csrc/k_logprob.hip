@@ -730,7 +730,7 @@ __global__ __launch_bounds__(256) void logprob_grad_kernel(LogprobArgs p, int al
         const float lp = fmaf(scale, v - ref, -off);
         // as a square: p below 2^-126, which ln p + H may lift above it, is not flushed
         const float root = __builtin_amdgcn_exp2f(lp * (0.5f * kLog2e)), pr = root * root;
-        float g = -pr * (w + q * (fmaxf(lp, -1e30f) + h));
+        float g = -pr * (w + q * (fmaxf(lp, -1000.f) + h));  // p is 0 there, for any q below 1e35
         if (c == tok) g += w;
         return empty ? 0.f : scale * g;
     };

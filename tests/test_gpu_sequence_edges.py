@@ -174,3 +174,23 @@ def test_logit_gradient_takes_the_normaliser_it_is_given():
             ep = (offset + 2 * lp + 16) * 4 * base.U
             wq = (w.abs() + q.abs() * 40).double().cpu().numpy()[:, None]
             assert (np.abs(got - ref) <= wq * (p.cpu().numpy() * ep * 2 + 8 * base.U)).all()
+
+
+@pytest.mark.parametrize("vocab", [24, 3001])
+def test_excluded_columns_stay_without_gradient_under_large_weights(vocab):
+    """p (ln p + H) is 0 at an excluded column for every finite weight."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab)
+    z = rng.standard_normal((6, vocab))
+    z[:, ::2] = -np.inf
+    t, zv = base.dev(torch, z)
+    tok = torch.ones(6, dtype=torch.int64, device="cuda")
+    f = api.token_logprobs(t, tok)
+    w = torch.zeros(6, device="cuda")
+    for weight in (1e9, -3e20, 1e34):
+        d = api.token_logprobs_grad(t, tok, f.lse, f.entropy, w, dentropy=torch.full_like(w, weight))
+        assert torch.isfinite(d).all() and not d[:, ::2].any()
+        unit = api.token_logprobs_grad(t, tok, f.lse, f.entropy, w, dentropy=torch.ones_like(w))
+        # one product more or less, each to u
+        assert ((d / weight - unit).abs() <= 4 * base.U * unit.abs() + 1e-37).all()
