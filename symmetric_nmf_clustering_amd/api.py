@@ -440,8 +440,9 @@ def embed_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 
                accumulate: bool = False) -> torch.Tensor:
     """Gradient of ``embed`` at its table: scale * the sum of dout's rows by id
     (dout of shape ids.shape + (width,)), a rows x width tensor of ``dtype`` or
-    ``out`` itself (accumulate=True adds to what ``out`` holds). Summed in
-    float32 in a fixed order. Ids outside the table give nothing."""
+    ``out`` itself (accumulate=True adds to what ``out`` holds). dout may be an
+    expanded view. Summed in float32 in a fixed order. Ids outside the table
+    give nothing."""
     dt = _seq_tensor(dout, "dout")
     it = _seq_tensor(ids, "ids", _INDEX, device=dout.device)
     if dout.dim() < 1 or tuple(dout.shape[:-1]) != tuple(ids.shape):
@@ -456,8 +457,8 @@ def embed_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, scale: float = 
     ot = _seq_tensor(out, "out", shape=(rows, width), device=dout.device)
     ldo = _rows_ld(out, "out")
     flat = dout.reshape(-1, width)
-    if width > 1 and flat.stride(1) != 1:
-        flat = flat.contiguous()
+    if (width > 1 and flat.stride(1) != 1) or (flat.shape[0] > 1 and flat.stride(0) < width):
+        flat = flat.contiguous()  # an expanded dout (a sum's gradient) among them
     ldd = _rows_ld(flat, "dout") if flat.shape[0] else width
     ids = ids.contiguous()
     ws = _scratch(L.OP_EMBED_GRAD, rows, width, ids.numel(), dout.device)

@@ -194,3 +194,22 @@ def test_excluded_columns_stay_without_gradient_under_large_weights(vocab):
         unit = api.token_logprobs_grad(t, tok, f.lse, f.entropy, w, dentropy=torch.ones_like(w))
         # one product more or less, each to u
         assert ((d / weight - unit).abs() <= 4 * base.U * unit.abs() + 1e-37).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_embedding_gradient_of_an_expanded_dout(kind):
+    """What a sum or a mean over events sends back: one row, or one number, for all."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(8)
+    for count, rows, width in ((1, 3, 5), (90, 20, 12), (9000, 70, 24)):
+        ids = torch.from_numpy(rng.integers(-1, rows, size=(count,))).cuda()
+        row, _ = base.dev(torch, rng.standard_normal(width), kind)
+        num, _ = base.dev(torch, rng.standard_normal(1), kind)
+        late, _ = base.dev(torch, rng.standard_normal(count + width), kind)
+        for d in (row.expand(count, width), num.expand(count, width), late.as_strided((count, width), (1, 1)),
+                  row[:1].expand(count, width)):
+            assert torch.equal(api.embed_grad(d, ids, rows), api.embed_grad(d.contiguous(), ids, rows))
+        two = ids.view(1, count).expand(2, count)
+        d = row.expand(2, count, width)
+        assert torch.equal(api.embed_grad(d, two, rows), api.embed_grad(d.contiguous(), two, rows))
