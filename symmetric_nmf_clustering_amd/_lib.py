@@ -30,6 +30,7 @@ OP_EMBED_GRAD, OP_GATED_SCAN, OP_TOKEN_LOGPROBS = 7, 8, 9
 F32, BF16, F16 = 0, 1, 2
 I32, I64 = 0, 1
 SCAN_CHUNK = 128  # steps between the states a gated scan keeps for its gradient
+MAX_BATCH = 65535 # most batch rows of one gated scan call (the binding makes several)
 MAX_TOP = 32      # most alternatives per row of token_logprobs
 (PROF_SH_FULL, PROF_SH_SAMPLED, PROF_SH_PROBE, PROF_BUILD_GRAM, PROF_UPDATE,
  PROF_SH_KMEANS, PROF_SH_SYM) = 0, 1, 2, 3, 4, 5, 6

@@ -509,7 +509,8 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tensor] =
     default zeros). ``gate`` has x's shape and type; an expanded view (one decay
     per channel, say) is read as it is. Steps at and past ``lengths[b]`` (int32)
     are masked: h is 0 there and the state passes. Returns (h, the last state in
-    float32), and with ``return_states`` the states ``gated_scan_grad`` needs."""
+    float32), and with ``return_states`` the states ``gated_scan_grad`` needs.
+    Batches past 65535 rows take a library call for each 65535."""
     x_b, x_t = _scan_view(x, "x")
     g_b, g_t = _scan_view(gate, "gate", x)
     batch, steps, width = x.shape
@@ -521,19 +522,32 @@ def gated_scan(x: torch.Tensor, gate: torch.Tensor, h0: Optional[torch.Tensor] =
     return (h, last, states) if return_states else (h, last)
 
 
-def _scan_call(x, gate, sizes, strides, lengths, h0, h, states):
+def _batch_rows(batch: int, *tensors):
+    """The batch rows of each tensor (None stays None), as many at a time as a
+    library call takes."""
+    for lo in range(0, batch, L.MAX_BATCH):
+        yield [None if t is None else t[lo:lo + L.MAX_BATCH] for t in tensors]
+
+
+def _scan_call(x, gate, sizes, strides, lengths, h0, h, states, last=None):
     batch, steps, width = sizes
     x_b, x_t, g_b, g_t = strides
     dev = x.device
     if batch < 1 or width < 1:
         raise ValueError("x must have at least one batch row and one channel")
-    last = _rows_out(batch, width, torch.float32, dev)
+    lengths_p = _lengths_ptr(lengths, batch, dev)
+    h0_p = _state_ptr(h0, "h0", (batch, width), dev)
+    if last is None:
+        last = _rows_out(batch, width, torch.float32, dev)
+    if batch > L.MAX_BATCH:
+        for xs, gs, ns, ss, hs, sts, ls in _batch_rows(batch, x, gate, lengths, h0, h, states, last):
+            _scan_call(xs, gs, (xs.shape[0], steps, width), strides, ns, ss, hs, sts, ls)
+        return last
     ws = _scratch(L.OP_GATED_SCAN, width, batch, steps, dev)
     st = L.load().symnmf_gated_scan(
         _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
-        _lengths_ptr(lengths, batch, dev), _state_ptr(h0, "h0", (batch, width), dev),
-        h.data_ptr(), last.data_ptr(), None if states is None else states.data_ptr(),
-        ws.data_ptr(), ws.numel(), _here(dev))
+        lengths_p, h0_p, h.data_ptr(), last.data_ptr(),
+        None if states is None else states.data_ptr(), ws.data_ptr(), ws.numel(), _here(dev))
     L.check(st, "symnmf_gated_scan")
     return last
 
@@ -558,6 +572,10 @@ def gated_scan_grad(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, d
     state), with the forward's ``states``. Returns (dx, dgate, dh0): dx and
     dgate per element in x's type, dh0 batch x width float32. The gradient of
     an expanded gate is dgate's sum over the expanded dimensions."""
+    return _scan_grad_call(x, gate, states, dh, dh_last, lengths)
+
+
+def _scan_grad_call(x, gate, states, dh, dh_last, lengths, dx=None, dgate=None, dh0=None):
     x_b, x_t = _scan_view(x, "x")
     g_b, g_t = _scan_view(gate, "gate", x)
     d_b, d_t = _scan_view(dh, "dh", x)
@@ -565,16 +583,22 @@ def gated_scan_grad(x: torch.Tensor, gate: torch.Tensor, states: torch.Tensor, d
     dev = x.device
     if batch < 1 or width < 1:
         raise ValueError("x must have at least one batch row and one channel")
-    dx = _steps_out(batch, steps, width, x.dtype, dev)
-    dgate = torch.empty_like(dx)
-    dh0 = _rows_out(batch, width, torch.float32, dev)
+    lengths_p = _lengths_ptr(lengths, batch, dev)
+    states_p = _state_ptr(states, "states", (batch, -(-steps // L.SCAN_CHUNK), width), dev)
+    last_p = _state_ptr(dh_last, "dh_last", (batch, width), dev)
+    if dx is None:
+        dx = _steps_out(batch, steps, width, x.dtype, dev)
+        dgate = torch.empty_like(dx)
+        dh0 = _rows_out(batch, width, torch.float32, dev)
+    if batch > L.MAX_BATCH:
+        for part in _batch_rows(batch, x, gate, states, dh, dh_last, lengths, dx, dgate, dh0):
+            _scan_grad_call(*part)
+        return dx, dgate, dh0
     ws = _scratch(L.OP_GATED_SCAN, width, batch, steps, dev)
     st = L.load().symnmf_gated_scan_grad(
         _DTYPES[x.dtype], batch, steps, width, x.data_ptr(), x_b, x_t, gate.data_ptr(), g_b, g_t,
-        _lengths_ptr(lengths, batch, dev),
-        _state_ptr(states, "states", (batch, -(-steps // L.SCAN_CHUNK), width), dev),
-        dh.data_ptr(), d_b, d_t, _state_ptr(dh_last, "dh_last", (batch, width), dev),
-        dx.data_ptr(), dgate.data_ptr(), dh0.data_ptr(), ws.data_ptr(), ws.numel(), _here(dev))
+        lengths_p, states_p, dh.data_ptr(), d_b, d_t, last_p, dx.data_ptr(), dgate.data_ptr(),
+        dh0.data_ptr(), ws.data_ptr(), ws.numel(), _here(dev))
     L.check(st, "symnmf_gated_scan_grad")
     return dx, dgate, dh0
 

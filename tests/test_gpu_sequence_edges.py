@@ -213,3 +213,38 @@ def test_embedding_gradient_of_an_expanded_dout(kind):
         two = ids.view(1, count).expand(2, count)
         d = row.expand(2, count, width)
         assert torch.equal(api.embed_grad(d, two, rows), api.embed_grad(d.contiguous(), two, rows))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("steps", [1, 20])
+def test_more_streams_than_a_call_of_the_library_takes(steps, kind):
+    """One stream per instrument: batch rows past 65535, with every optional input."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    gen = torch.Generator(device="cuda").manual_seed(steps)
+    batch, width = 65535 * 2 + 700, 6
+    x, g, dh = (torch.randn(batch, steps, width, generator=gen, device="cuda").to(base.types(torch)[kind])
+                for _ in range(3))
+    h0, dl = (torch.randn(batch, width, generator=gen, device="cuda") for _ in range(2))
+    n = torch.randint(0, steps + 1, (batch,), generator=gen, device="cuda").int()
+    one = g[0, 0].expand(batch, steps, width)
+    for gate in (g, one):
+        h, last, st = api.gated_scan(x, gate, h0=h0, lengths=n, return_states=True)
+        grads = api.gated_scan_grad(x, gate, st, dh, dh_last=dl, lengths=n)
+        for lo in range(0, batch, 40000):  # the same rows in smaller batches
+            s = slice(lo, min(lo + 40000, batch))
+            a = api.gated_scan(x[s], gate[s], h0=h0[s], lengths=n[s], return_states=True)
+            b = api.gated_scan_grad(x[s], gate[s], a[2], dh[s], dh_last=dl[s], lengths=n[s])
+            for whole, part in zip((h, last, st, *grads), (*a, *b)):
+                assert torch.equal(whole[s], part)
+        assert torch.equal(api.gated_scan(x, gate)[0], torch.cat([api.gated_scan(x[i:i + 60000], gate[i:i + 60000])[0]
+                                                                  for i in range(0, batch, 60000)]))
+    out, state = api.gated_step(x[:, 0], g[:, 0], h0)
+    for lo in range(0, batch, 40000):
+        s = slice(lo, min(lo + 40000, batch))
+        a, b = api.gated_step(x[s, 0], g[s, 0], h0[s])
+        assert torch.equal(out[s], a) and torch.equal(state[s], b)
+    with pytest.raises(ValueError):
+        api.gated_step(x[:, 0], g[:, 0], h0[:-1])
+    with pytest.raises(ValueError):
+        api.gated_scan(x, g, lengths=n[:-1])
