@@ -22,10 +22,10 @@ __global__ __launch_bounds__(256) void embed_kernel(const TI* __restrict__ table
                                                     int width, int64_t ldt,
                                                     const ID* __restrict__ ids, int64_t count,
                                                     float scale, TO* __restrict__ out, int64_t ldo,
-                                                    int lx_log2) {
+                                                    int lx_log2, int64_t first) {
     const int lx = 1 << lx_log2;
     const int lane = threadIdx.x & (lx - 1);
-    const int64_t i = (int64_t)blockIdx.x * (256 >> lx_log2) + (threadIdx.x >> lx_log2);
+    const int64_t i = (first + blockIdx.x) * (256 >> lx_log2) + (threadIdx.x >> lx_log2);
     if (i >= count) return;
     const int64_t id = (int64_t)ids[i];
     const bool in = id >= 0 && id < rows;
@@ -653,10 +653,11 @@ hipError_t embed_run(const EmbedArgs& a, hipStream_t st) {
     constexpr int V = sizeof(TI) == 4 || sizeof(TO) == 4 ? 4 : 8;
     const int lg = log2_up((a.width + V - 1) / V, 8);
     const int64_t per = 256 >> lg;
-    hipLaunchKernelGGL((embed_kernel<TI, TO, ID, V>), dim3((unsigned)((a.count + per - 1) / per)),
-                       dim3(256), 0, st, (const TI*)a.table, a.rows, (int)a.width, a.ldt,
-                       (const ID*)a.ids, a.count, a.scale, (TO*)a.out, a.ldo, lg);
-    return hipGetLastError();
+    return in_launches((a.count + per - 1) / per, [&](int64_t first, unsigned n) {
+        hipLaunchKernelGGL((embed_kernel<TI, TO, ID, V>), dim3(n), dim3(256), 0, st,
+                           (const TI*)a.table, a.rows, (int)a.width, a.ldt, (const ID*)a.ids,
+                           a.count, a.scale, (TO*)a.out, a.ldo, lg, first);
+    });
 }
 template <class TI, class TO>
 hipError_t embed_id(const EmbedArgs& a, hipStream_t st) {

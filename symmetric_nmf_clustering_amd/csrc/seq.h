@@ -62,6 +62,21 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
     __builtin_memcpy(p, &v, sizeof(T) * V);
 }
 
+// A launch takes fewer than 2^32 threads along a grid's first dimension. Work of
+// `blocks` workgroups goes out as launches of at most kMaxBlocks, which stay below
+// that with 1024 threads each; every one fills the chip for a millisecond or so.
+// launch(first, n): the workgroups first ... first + n - 1.
+constexpr int64_t kMaxBlocks = int64_t(1) << 20;
+template <class F>
+hipError_t in_launches(int64_t blocks, F&& launch) {
+    for (int64_t first = 0; first < blocks; first += kMaxBlocks) {
+        launch(first, (unsigned)(blocks - first < kMaxBlocks ? blocks - first : kMaxBlocks));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // symnmf_workspace_bytes for the sequence operators; 0 for invalid sizes (seq.cpp).
 size_t seq_workspace_bytes(int op, int64_t n, int32_t k, int64_t T);
 
