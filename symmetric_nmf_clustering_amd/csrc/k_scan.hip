@@ -41,6 +41,7 @@ struct Tile {       // how a workgroup's 256 threads lie over channels and time
     int nseg;       // time segments
     int seg;        // steps per segment (a multiple of the tile's and of kScanChunk)
     int64_t items;  // nct x nseg x batch
+    int64_t first;  // of this launch
 };
 
 template <class T, int V>
@@ -183,7 +184,8 @@ struct Place {
 template <int V>
 __device__ __forceinline__ Place place(const ScanArgs& p, const Tile& tl, bool back) {
     Place q;
-    const int64_t item = back ? tl.items - 1 - (int64_t)blockIdx.x : (int64_t)blockIdx.x;
+    const int64_t nth = tl.first + (int64_t)blockIdx.x;
+    const int64_t item = back ? tl.items - 1 - nth : nth;
     const int cl = 1 << tl.cl_log2;
     const int ct = (int)(item % tl.nct);
     q.seg = (int)(item / tl.nct % tl.nseg);
@@ -344,9 +346,9 @@ __global__ __launch_bounds__(256, CG && sizeof(T) == 4 && V > 1 ? 4 : 1) void sc
 // channels one after another, all reads of kWalk steps on their way first.
 constexpr int kWalk = 4;
 template <class T, int V>
-__global__ __launch_bounds__(256) void scan_walk_kernel(ScanArgs p) {
+__global__ __launch_bounds__(256) void scan_walk_kernel(ScanArgs p, int64_t first) {
     const int64_t nv = p.width / V;  // V divides the width: the state may be updated in place
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;
     if (i >= p.batch * nv) return;
     const int64_t b = i / nv, c0 = (i - b * nv) * V, at = b * p.width + c0;
     const T* x = (const T*)p.x + b * p.x_b + c0;
@@ -598,42 +600,44 @@ Tile plan(int64_t batch, int64_t steps, int64_t width, int V, int cut, int fill)
     t.nseg = (int)((units + per - 1) / per);
     t.seg = (int)(per * unit);
     t.items = batch * t.nct * t.nseg;
+    t.first = 0;
     return t;
 }
 // A tile has 256 x 32 elements. With 64 channels or fewer that is 128 steps or
 // more and a multiple of 128; wider tiles hold all steps there are.
 static_assert(256 * kTileT / kTileCh % kScanChunk == 0, "tiles start at kept states");
 
+// kernel<<<items>>> of the plan, in as many launches as it takes.
+template <class K>
+hipError_t run_plan(K* kernel, const ScanArgs& a, Tile tl, hipStream_t st) {
+    return in_launches(tl.items, [&](int64_t first, unsigned n) {
+        tl.first = first;
+        hipLaunchKernelGGL(kernel, dim3(n), dim3(256), 0, st, a, tl, (float*)a.ws);
+    });
+}
 template <class T, int V, bool CG>
 hipError_t scan_run(const ScanArgs& a, hipStream_t st) {
     const Tile tl = plan(a.batch, a.steps, a.width, V, kCut, kFill);
-    const dim3 g((unsigned)tl.items);
     if (tl.nseg > 1) {
-        hipLaunchKernelGGL((scan_kernel<T, V, 1, CG>), g, dim3(256), 0, st, a, tl, (float*)a.ws);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = run_plan(scan_kernel<T, V, 1, CG>, a, tl, st);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((scan_kernel<T, V, 0, CG>), g, dim3(256), 0, st, a, tl, (float*)a.ws);
-    return hipGetLastError();
+    return run_plan(scan_kernel<T, V, 0, CG>, a, tl, st);
 }
 template <class T, int V>
 hipError_t walk_run(const ScanArgs& a, hipStream_t st) {
-    const int64_t n = a.batch * (a.width / V);
-    hipLaunchKernelGGL((scan_walk_kernel<T, V>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
-                       st, a);
-    return hipGetLastError();
+    return in_launches((a.batch * (a.width / V) + 255) / 256, [&](int64_t first, unsigned n) {
+        hipLaunchKernelGGL((scan_walk_kernel<T, V>), dim3(n), dim3(256), 0, st, a, first);
+    });
 }
 template <class T, int V>
 hipError_t grad_run(const ScanArgs& a, hipStream_t st) {
     const Tile tl = plan(a.batch, a.steps, a.width, V, kCutGrad, kFillGrad);
-    const dim3 g((unsigned)tl.items);
     if (tl.nseg > 1) {
-        hipLaunchKernelGGL((scan_grad_kernel<T, V, 1>), g, dim3(256), 0, st, a, tl, (float*)a.ws);
-        const hipError_t e = hipGetLastError();
+        const hipError_t e = run_plan(scan_grad_kernel<T, V, 1>, a, tl, st);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((scan_grad_kernel<T, V, 0>), g, dim3(256), 0, st, a, tl, (float*)a.ws);
-    return hipGetLastError();
+    return run_plan(scan_grad_kernel<T, V, 0>, a, tl, st);
 }
 
 // Channels to a lane, 8 bytes of them. 16 bytes put fewer steps into a thread and

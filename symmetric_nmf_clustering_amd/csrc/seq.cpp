@@ -30,8 +30,9 @@ inline bool ws_fits(const void* ws, size_t got, size_t need) {
 }
 inline int done(hipError_t e) { return e == hipSuccess ? SYMNMF_OK : SYMNMF_E_HIP; }
 
-// Sizes the scan's kernels index with: 32-bit steps and channels, and a grid of
-// batch x channel tiles (of 64 channels, or all of them) in 32 bits.
+// Sizes the scan's kernels index with: steps and channels of a row in 32 bits. Its
+// workgroups (batch rows x channel tiles) are counted in 64 and sent out in several
+// launches where one does not take them.
 bool scan_sizes_ok(int64_t batch, int64_t steps, int64_t width) {
     return in(batch, 1, 65535) && in(steps, 0, kMaxCount) && in(width, 1, 1 << 24) &&
            batch * width <= int64_t(1) << 36;

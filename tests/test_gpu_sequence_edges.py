@@ -264,3 +264,41 @@ def test_embedding_of_more_rows_than_a_launch_takes():
         n = part.shape[0] // rows * rows
         assert (part[:n].view(-1, rows, width) == want).all()
         assert torch.equal(part[n:], want[:part.shape[0] - n])
+
+
+def test_scan_of_more_channels_than_a_launch_takes():
+    """Single steps of 2^32 channels of odd width, a thread each."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    batch, width = 65535, 65601
+    x, g = (torch.randn(width, device="cuda").bfloat16() for _ in range(2))
+    h, last = api.gated_scan(x.expand(batch, 1, width), g.expand(batch, 1, width))
+    one, one_last = api.gated_scan(x.expand(1, 1, width), g.expand(1, 1, width))
+    for lo in range(0, batch, 4096):
+        assert (h[lo:lo + 4096] == one).all() and (last[lo:lo + 4096] == one_last).all()
+
+
+def test_scan_of_more_tiles_than_a_launch_is_given():
+    """2^20 workgroups and more, forward and backward: several launches."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    batch, steps, width = 65535, 9, 512 * 17
+    x, g, d = (torch.randn(steps, width, device="cuda").bfloat16() for _ in range(3))
+    n = (torch.arange(batch, device="cuda") % 10).int()
+    big = [t.expand(batch, steps, width) for t in (x, g, d)]
+    few = [t.expand(10, steps, width) for t in (x, g, d)]
+    h, last, st = api.gated_scan(big[0], big[1], lengths=n, return_states=True)
+    want = api.gated_scan(few[0], few[1], lengths=n[:10], return_states=True)
+
+    def same(a, b):
+        for lo in range(0, batch, 5000):
+            part = a[lo:lo + 5000]
+            assert (part.view(-1, 10, *part.shape[1:]) == b).all() if len(part) == 5000 else \
+                torch.equal(part, b.repeat(-(-len(part) // 10), *[1] * (b.dim() - 1))[:len(part)])
+    for a, b in zip((h, last, st), want):
+        same(a, b)
+    del h, last
+    dx, dg, dh0 = api.gated_scan_grad(big[0], big[1], st, big[2], lengths=n)
+    want = api.gated_scan_grad(few[0], few[1], want[2], few[2], lengths=n[:10])
+    for a, b in zip((dx, dg, dh0), want):
+        same(a, b)
