@@ -219,14 +219,14 @@ template <class T, int WAVES>
 __global__ __launch_bounds__(WAVES < 4 ? 256 : 64 * WAVES) void logprob_slice_kernel(
     const T* __restrict__ logits, int64_t items, int64_t vocab, int64_t ld, float scale,
     int groups_per_slice, int nslice, int top, Stat* __restrict__ part, Cand* __restrict__ cand,
-    RowOut out) {
+    RowOut out, int64_t first) {
     extern __shared__ __align__(16) char smem[];
     constexpr int V = 16 / sizeof(T), NV = kGroup / V, Q = 4, N = 64 * WAVES;
     constexpr int SLOTS = WAVES < 4 ? 4 / WAVES : 1;
     __shared__ Stat wst[WAVES];
     __shared__ Cand leads[SLOTS][N > 2 * kFew ? N : 2 * kFew];
     const int slot = threadIdx.x / N, t = threadIdx.x % N, lane = t & 63, w = t >> 6;
-    const int64_t item = (int64_t)blockIdx.x * SLOTS + slot;
+    const int64_t item = (first + blockIdx.x) * SLOTS + slot;
     if (item >= items) return;  // whole waves, and with several to an item whole workgroups
     T* gmax = reinterpret_cast<T*>(smem) + (int64_t)slot * groups_per_slice;
     Cand* lead = leads[slot];
@@ -457,9 +457,9 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(const T* __restrict__ 
                                                           int nslice, int top,
                                                           const Stat* __restrict__ part,
                                                           const Cand* __restrict__ cand,
-                                                          RowOut out) {
+                                                          RowOut out, int64_t first) {
     __shared__ Cand list[kMaxTop][kMaxSlices];
-    const int64_t row = blockIdx.x;
+    const int64_t row = first + blockIdx.x;
     const int lane = threadIdx.x;
     const float k = scale * kLog2e;
     const bool on = lane < nslice;
@@ -530,10 +530,10 @@ template <class T, int NG>
 __global__ __launch_bounds__(256) void logprob_short_kernel(const T* __restrict__ logits,
                                                             int64_t count, int vocab, int64_t ld,
                                                             float scale, int lg, int top,
-                                                            RowOut out) {
+                                                            RowOut out, int64_t first) {
     constexpr int NS = NG * kGroup, V = 16 / sizeof(T);
     const int l = threadIdx.x & ((1 << lg) - 1);
-    const int64_t row0 = (int64_t)blockIdx.x * (256 >> lg) + (threadIdx.x >> lg);
+    const int64_t row0 = (first + blockIdx.x) * (256 >> lg) + (threadIdx.x >> lg);
     const bool on = row0 < count;
     const int64_t row = on ? row0 : count - 1;
     const T* z = logits + row * ld;
@@ -789,14 +789,14 @@ hipError_t logprobs_run(const LogprobArgs& a, hipStream_t st) {
         while ((int64_t)32 << lg < a.vocab) ++lg;
         const int ng = (int)((a.vocab + (kGroup << lg) - 1) / (kGroup << lg));
         const int64_t per = 256 >> lg;
-        const dim3 g((unsigned)((a.count + per - 1) / per)), b(256);
         auto* kern = ng <= 1   ? logprob_short_kernel<T, 1>
                      : ng <= 2 ? logprob_short_kernel<T, 2>
                      : ng <= 3 ? logprob_short_kernel<T, 3>
                                : logprob_short_kernel<T, 4>;
-        hipLaunchKernelGGL(kern, g, b, 0, st, (const T*)a.logits, a.count, (int)a.vocab, a.ld,
-                           a.scale, lg, a.top, o);
-        return hipGetLastError();
+        return in_launches((a.count + per - 1) / per, [&](int64_t first, unsigned n) {
+            hipLaunchKernelGGL(kern, dim3(n), dim3(256), 0, st, (const T*)a.logits, a.count,
+                               (int)a.vocab, a.ld, a.scale, lg, a.top, o, first);
+        });
     }
     const SlicePlan p = slice_plan(a.vocab, a.count, sizeof(T));
     Stat* part = (Stat*)a.ws;
@@ -808,14 +808,17 @@ hipError_t logprobs_run(const LogprobArgs& a, hipStream_t st) {
                  : p.waves == 4 ? logprob_slice_kernel<T, 4>
                                 : logprob_slice_kernel<T, 16>;
     const int slots = p.waves == 1 ? 4 : 1, threads = p.waves == 16 ? 1024 : 256;
-    hipLaunchKernelGGL(kern, dim3((unsigned)((items + slots - 1) / slots)), dim3(threads),
-                       slots * lds, st, (const T*)a.logits, items, a.vocab, a.ld, a.scale,
-                       p.groups, p.nslice, a.top, part, cand, o);
-    hipError_t e = hipGetLastError();
+    const hipError_t e =
+        in_launches((items + slots - 1) / slots, [&](int64_t first, unsigned n) {
+            hipLaunchKernelGGL(kern, dim3(n), dim3(threads), slots * lds, st, (const T*)a.logits,
+                               items, a.vocab, a.ld, a.scale, p.groups, p.nslice, a.top, part,
+                               cand, o, first);
+        });
     if (e != hipSuccess || p.nslice == 1) return e;
-    hipLaunchKernelGGL((logprob_join_kernel<T>), dim3((unsigned)a.count), dim3(64), 0, st,
-                       (const T*)a.logits, a.vocab, a.ld, a.scale, p.nslice, a.top, part, cand, o);
-    return hipGetLastError();
+    return in_launches(a.count, [&](int64_t first, unsigned n) {
+        hipLaunchKernelGGL((logprob_join_kernel<T>), dim3(n), dim3(64), 0, st, (const T*)a.logits,
+                           a.vocab, a.ld, a.scale, p.nslice, a.top, part, cand, o, first);
+    });
 }
 
 template <class T>

@@ -302,3 +302,24 @@ def test_scan_of_more_tiles_than_a_launch_is_given():
     want = api.gated_scan_grad(few[0], few[1], want[2], few[2], lengths=n[:10])
     for a, b in zip((dx, dg, dh0), want):
         same(a, b)
+
+
+@pytest.mark.parametrize("kind,vocab,count,top", [("bf16", 65, (1 << 26) + 2 * 999, 2), ("bf16", 1032, (1 << 22) + 2 * 999, 3),
+                                                  ("bf16", 8200, (1 << 20) + 2 * 999, 2)])
+def test_log_probabilities_of_more_rows_than_a_launch_is_given(kind, vocab, count, top):
+    """Rows by the register kernel, by a wave and by a workgroup: several launches."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    period = 1 << 12
+    z = torch.randn(period, vocab, device="cuda").to(base.types(torch)[kind])
+    tok = torch.randint(-1, vocab, (period,), device="cuda").int()
+    copies = -(-count // period)
+    many = torch.empty(copies, period, vocab, dtype=z.dtype, device="cuda")
+    many.copy_(z)
+    r = api.token_logprobs(many.view(-1, vocab)[:count], tok.repeat(copies)[:count], top=top)
+    want = api.token_logprobs(z, tok, top=top)
+    whole = count // period * period
+    for a, b in ((r.logp, want.logp), (r.entropy, want.entropy), (r.lse, want.lse), (r.top_ids, want.top_ids),
+                 (r.top_logp, want.top_logp)):
+        assert (a[:whole].view(-1, *b.shape) == b).all()
+        assert torch.equal(a[whole:], b[:count - whole])
