@@ -7,6 +7,8 @@
 // one chunk is written at once; the others leave one partial per chunk, which
 // a second kernel adds in chunk order. No floating-point atomics: the result
 // is the same on every run.
+#include <algorithm>
+
 #include "common.h"
 #include "seq.h"
 
@@ -172,13 +174,15 @@ struct AbsentFill {
                 for (int64_t c = lane; c < words; c += 1 << lx) q[c] = zero;
             }
     }
-    __device__ void run(int64_t part) const {
-        if (unit == 16)
-            put<uint4>(part);
-        else if (unit == 4)
-            put<uint32_t>(part);
-        else
-            put<uint16_t>(part);
+    __device__ void run(int64_t part, int64_t parts) const {
+        for (; part < blocks(); part += parts) {
+            if (unit == 16)
+                put<uint4>(part);
+            else if (unit == 4)
+                put<uint32_t>(part);
+            else
+                put<uint16_t>(part);
+        }
     }
 };
 
@@ -417,7 +421,7 @@ __global__ __launch_bounds__(256) void embed_grad_sum_kernel(
     const int lane = threadIdx.x & (lx - 1), grp = threadIdx.x >> lx_log2;
     const int c = ((int)blockIdx.y * lx + lane) * V;
     if ((int)blockIdx.x >= sum_blocks) {
-        if (blockIdx.y == 0) af.run((int)blockIdx.x - sum_blocks);
+        if (blockIdx.y == 0) af.run((int)blockIdx.x - sum_blocks, (int)gridDim.x - sum_blocks);
         return;
     }
     const int64_t chunk = (int64_t)blockIdx.x * groups + grp;
@@ -802,7 +806,9 @@ hipError_t grad_run(const EmbedGradArgs& a, const GradLayout& L, const uint32_t*
     const int lg = log2_up(nv, 8);
     const int64_t groups = 256 >> lg;
     const int64_t sum_blocks = (nchunks + groups - 1) / groups;
-    const int64_t fill = af.blocks();
+    // with at most 2^23 workgroups for the sum (128 tokens a chunk by then) the grid
+    // stays below 2^24
+    const int64_t fill = std::min<int64_t>(af.blocks(), 1 << 16);
     const unsigned cols = (unsigned)((nv + (1 << lg) - 1) >> lg);
     hipLaunchKernelGGL((embed_grad_sum_kernel<TD, TO, V>),
                        dim3((unsigned)(sum_blocks + fill), cols), dim3(256), 0, st,

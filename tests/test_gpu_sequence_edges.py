@@ -323,3 +323,25 @@ def test_log_probabilities_of_more_rows_than_a_launch_is_given(kind, vocab, coun
                  (r.top_logp, want.top_logp)):
         assert (a[:whole].view(-1, *b.shape) == b).all()
         assert torch.equal(a[whole:], b[:count - whole])
+
+
+@pytest.mark.parametrize("rows,width", [(540001, 257), ((1 << 29) + 1000, 33)])
+def test_embedding_gradient_clears_tables_of_many_rows(rows, width):
+    """More rows without tokens than the launch has workgroups for, and more than a
+    launch could have (2^24)."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    ids = torch.randint(0, rows, (9000,), generator=gen, device="cuda")
+    ids[:3] = torch.tensor([0, rows - 1, 70])
+    ids[100:200] = 70
+    d = torch.randint(-8, 9, (9000, width), generator=gen, device="cuda").bfloat16()  # sums are exact
+    out = torch.empty(rows, width, dtype=torch.bfloat16, device="cuda")
+    out.view(torch.int16).fill_(0x7fc0)  # NaN
+    api.embed_grad(d, ids, rows, out=out)
+    named, at = torch.unique(ids, return_inverse=True)
+    want = torch.zeros(len(named), width, device="cuda", dtype=torch.float64).index_add_(0, at, d.double())
+    assert torch.equal(out[named].double(), want.bfloat16().double())
+    out[named] = 0
+    for lo in range(0, rows, 1 << 24):
+        assert not out[lo:lo + (1 << 24)].view(torch.int16).any()
