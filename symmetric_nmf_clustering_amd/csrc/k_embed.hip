@@ -560,8 +560,10 @@ __global__ __launch_bounds__(256) void embed_grad_fold_kernel(
 // takes thousands of terms, which the sizes cannot tell but do suggest: 5000
 // tokens into 20000 x 24 take 17.4 us so, against 19.7 with partials and a fold;
 // 2000 into 5000 x 257 16.8 against 22.0; but 8192 into 50 x 24 29.6 against 23.5
-// and 8192 into 5000 x 1024 53 against 34.
+// and 8192 into 5000 x 1024 53 against 34. Column tiles (128 columns) are the grid's
+// second dimension, of at most 65535.
 bool by_rows(int64_t rows, int64_t width, int64_t count) {
+    if (width > 65535 * 128) return false;
     return count <= 1024 || (count <= kSmallCount && count <= rows && count * width <= 1 << 19);
 }
 constexpr int kRowTokens = 16;
