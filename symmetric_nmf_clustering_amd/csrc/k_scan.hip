@@ -569,12 +569,15 @@ __global__ __launch_bounds__(256) void scan_grad_kernel(ScanArgs p, Tile tl,
 }
 
 constexpr int kMaxSeg = 256;
-// Workgroups below which a scan is cut in time, and as many as it is cut into.
-// The forward is cut early: its uncut workgroups keep too little in flight. The
-// backward reads three arrays and writes two, so reading two of them twice only
-// pays where most of the chip would idle (8 x 2048 x 2048 bf16 as 256 workgroups:
-// 80.2 us, cut into 512: 86.0, into 1024: 88.6).
-constexpr int kCut = 256, kFill = 2048, kCutGrad = 256, kFillGrad = 1024;
+// Workgroups below which a scan is cut in time, and as many as it is cut into. Cut,
+// it reads its inputs twice but fills the chip (1 x 4096 steps, us uncut and cut:
+// bf16 128 workgroups 86.6 and 66.7, 192 106.6 and 93.6, 224 112 and 115, 255 108 and
+// 124; fp32 128 132 and 115, 192 142 and 184, 255 156 and 239). The backward reads
+// three arrays and writes two, in fp32 with half the waves (bf16 128 135 and 89, 192
+// 153 and 155, 255 141 and 175, fp32 64 154 and 91, 128 175 and 184, 255 252 and 344;
+// 8 x 2048 x 2048 bf16 as 256: 80.2 us, cut into 512 86.0, into 1024 88.6).
+constexpr int kCut = 192, kFill = 2048, kFillGrad = 1024;
+constexpr int cut_grad(int bytes) { return bytes == 4 ? 128 : 192; }
 constexpr int kWalkSteps = 8;  // up to these, steps are walked one by one
 
 // Channels over threads: 64 channels to a tile, fewer where the width is smaller
@@ -632,7 +635,7 @@ hipError_t walk_run(const ScanArgs& a, hipStream_t st) {
 }
 template <class T, int V>
 hipError_t grad_run(const ScanArgs& a, hipStream_t st) {
-    const Tile tl = plan(a.batch, a.steps, a.width, V, kCutGrad, kFillGrad);
+    const Tile tl = plan(a.batch, a.steps, a.width, V, cut_grad(sizeof(T)), kFillGrad);
     if (tl.nseg > 1) {
         const hipError_t e = run_plan(scan_grad_kernel<T, V, 1>, a, tl, st);
         if (e != hipSuccess) return e;
@@ -660,12 +663,13 @@ hipError_t grad_vec(const ScanArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// Two numbers per channel and time segment of the plan that has most.
+// Two numbers per channel and time segment of the plan that has most (a plan that is
+// cut has as many segments whatever it is cut below).
 size_t scan_ws_bytes(int64_t batch, int64_t steps, int64_t width) {
     int64_t nseg = 1;
     for (int v : {1, 2, 4}) {
         nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, kCut, kFill).nseg);
-        nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, kCutGrad, kFillGrad).nseg);
+        nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, cut_grad(2), kFillGrad).nseg);
     }
     return nseg > 1 ? 8 * (size_t)nseg * (size_t)batch * (size_t)width : 256;
 }

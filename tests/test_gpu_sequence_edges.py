@@ -359,3 +359,27 @@ def test_embedding_gradient_of_the_widest_tables():
     more = torch.ones(3, width, device="cuda")
     api.embed_grad(d, torch.tensor([1, -1, 1], device="cuda"), 3, out=more, accumulate=True)
     assert (more[0] == 1).all() and torch.equal(more[1], 1 + (d[0].float() + d[2].float()))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("batch,width", [(1, 64 * 127), (2, 64 * 64), (1, 64 * 191), (3, 64 * 64), (1, 64 * 255 - 1)])
+def test_scan_where_cutting_time_begins(batch, width, kind):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(width)
+    steps = 530
+    x, xv = base.dev(torch, rng.standard_normal((batch, steps, width)), kind)
+    g, gv = base.dev(torch, rng.standard_normal((batch, steps, width)) + 2, kind)
+    n = np.full(batch, 517)
+    tn = torch.from_numpy(n).int().cuda()
+    E, bx, bg, bm = base.scan_bounds(xv, gv, None, n, xv, None)
+    h, last, st = api.gated_scan(x, g, lengths=tn, return_states=True)
+    hr, lr, before = so.gated_scan(xv, gv, None, n)
+    base.close(h, hr, E[:, 1:], kind)
+    base.close(last, lr, E[:, -1])
+    base.close(st, before[:, :-1:128], E[:, :-1:128])
+    dx, dg, dh0 = api.gated_scan_grad(x, g, st, x, lengths=tn)
+    rx, rg, r0 = so.gated_scan_grad(xv, gv, xv, None, None, n)
+    base.close(dx, rx, bx, kind)
+    base.close(dg, rg, bg, kind)
+    base.close(dh0, r0, bm)
