@@ -383,3 +383,31 @@ def test_scan_where_cutting_time_begins(batch, width, kind):
     base.close(dx, rx, bx, kind)
     base.close(dg, rg, bg, kind)
     base.close(dh0, r0, bm)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("vocab", [2, 24, 40, 130, 520, 1003, 2600])
+def test_logit_gradient_of_near_and_far_rows_side_by_side(vocab, kind):
+    """Rows that share a wave or a workgroup, every fourth far from zero, of the
+    lowest value, empty or plain."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(vocab)
+    count = 45
+    z = rng.standard_normal((count, vocab)) * 3
+    z[1::4] += 2000
+    z[2::4] = torch.finfo(base.types(torch)[kind]).min
+    z[3::4] = -np.inf
+    t, zv = base.dev(torch, z, kind)
+    tok = rng.integers(-1, vocab, size=count)
+    dtok = torch.from_numpy(tok).cuda()
+    w, q = (torch.from_numpy(rng.standard_normal(count).astype(np.float32)).cuda() for _ in range(2))
+    f = api.token_logprobs(t, dtok)
+    d = api.token_logprobs_grad(t, dtok, f.lse, f.entropy, w, dentropy=q)
+    full = np.arange(count) % 4 != 3
+    check_grad_anywhere(zv[full], tok[full], w[full], q[full], 1.0, d[full], kind)
+    assert not d[3::4].any()
+    wide = torch.zeros(count, vocab + 3, dtype=t.dtype, device="cuda")[:, 1:-2]  # rows at every alignment
+    wide.copy_(t)
+    api.token_logprobs_grad(wide, dtok, f.lse, f.entropy, w, dentropy=q, out=wide)
+    check_grad_anywhere(zv[full], tok[full], w[full], q[full], 1.0, wide[full], kind)
