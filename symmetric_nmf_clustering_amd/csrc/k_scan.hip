@@ -209,9 +209,10 @@ __device__ __forceinline__ Place place(const ScanArgs& p, const Tile& tl, bool b
 // B, batch x width each). CG: the gate does not change over time (stride 0), so
 // it is read, and its sigmoid taken, once.
 //
-// Four waves per SIMD are asked of the compiler where it misses them by a register
-// or two (250 x 100000 fp32, one decay a channel: 47.8 us against 50.7); elsewhere
-// that would spill.
+// Four waves per SIMD are asked of the compiler where it misses them by little: it
+// then keeps two registers of the fp32 outputs' kernel in scratch, 12 bytes a lane
+// (250 x 100000 fp32, one decay a channel: 42.0 us against 43.9). Elsewhere it would
+// spill far more.
 template <class T, int V, int MODE, bool CG>
 __global__ __launch_bounds__(256, CG && sizeof(T) == 4 && V > 1 ? 4 : 1) void scan_kernel(ScanArgs p, Tile tl, float* __restrict__ agg) {
     constexpr int R = kTileT / V;
