@@ -461,6 +461,124 @@ int symnmf_token_logprobs_grad(const void* logits, int type, int64_t count, int6
                                const float* dentropy, void* dlogits, int64_t ldd,
                                void* hip_stream);
 
+/* ---- layers over event streams -----------------------------------------------
+ * What a model with a longer memory needs next to the operators above: linear
+ * attention (a matrix of memory for each head, where the gated scan keeps a
+ * number for each channel), rotary positions for its queries and keys, and the
+ * optimizer step of its tables and projections. Conventions as above:
+ * asynchronous, float32, bfloat16 or float16 elements, sums and states in
+ * float32, one rounding of each output, strides in elements and not negative,
+ * unit stride within a head's row, any element alignment. */
+
+/* Sizes of a linear attention: batch x steps x heads rows of dk (q) and dv (o,
+ * and its gradient), batch x steps x kv_heads rows of dk (k) and dv (v). Query
+ * head h reads key head h / (heads / kv_heads); kv_heads divides heads. dk and
+ * dv 1 to 256, heads up to 65536. *_stride: of a batch row, a step and a head
+ * (a stride of 0 broadcasts). do_stride is the gradient's alone. */
+typedef struct symnmf_attend_desc {
+    int32_t type; /* enum symnmf_dtype, of q, k, v, o and their gradients */
+    int32_t heads, kv_heads, dk, dv;
+    float scale;
+    int64_t batch, steps;
+    int64_t q_stride[3], k_stride[3], v_stride[3], do_stride[3];
+} symnmf_attend_desc;
+
+/* Workspace of symnmf_linear_attention (gradient 0) and its gradient (1); 0 for
+ * an invalid descriptor. */
+size_t symnmf_linear_attention_ws_bytes(const symnmf_attend_desc* d, int gradient);
+
+/* Linear attention with a decay for each head, per batch row and query head:
+ *   S_t = a S_{t-1} + k_t v_t^T  (dk x dv),  o_t = scale q_t^T S_t,  S_{-1} = state,
+ * a = exp(decay[head]). decay (heads float32) is the natural logarithm of what a
+ * step keeps, <= 0 in use; -inf keeps nothing (a = 0), 0 everything.
+ *   o (batch x steps x heads x dv, dense) receives o_t in the inputs' type.
+ *   lengths (nullable, batch int32): steps t >= lengths[b] are masked: not read,
+ *     o 0 there, and the state passes them. Values are clamped to [0, steps].
+ *   state (nullable: zeros), last (nullable): batch x heads x dk x dv float32,
+ *     dense, the state before the first step and after the last; they may not
+ *     overlap.
+ * Computed in chunks of steps as matrix products; the state to float32's
+ * precision whatever the type (for bfloat16, what o takes from within a chunk
+ * and from the state passes through one more rounding to bfloat16). Elements
+ * must be finite: an infinite or NaN one may make all of its chunk (64 steps)
+ * and what follows NaN. The same bits on every call.
+ * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
+int symnmf_linear_attention(const symnmf_attend_desc* d, const void* q, const void* k,
+                            const void* v, const float* decay, const int32_t* lengths,
+                            const float* state, void* o, float* last, void* ws, size_t ws_bytes,
+                            void* hip_stream);
+
+/* Its gradient from dout (at o) and dlast (nullable, at the last state):
+ *   dq_t = scale S_t dout_t,  R_t = a R_{t+1} + scale q_t dout_t^T  (dlast beyond),
+ *   dk_t = R_t v_t,  dv_t = R_t^T k_t,  dstate = a R_0,
+ * with the S_t made again from state. dq (batch x steps x heads x dk), dk and dv
+ * (batch x steps x kv_heads x dk, dv) are dense, in the inputs' type, 0 at masked
+ * steps; a shared key head's are summed over its query heads in float32, in
+ * order, before their rounding. dstate (nullable): batch x heads x dk x dv
+ * float32. The decays are constants: they have no gradient here.
+ * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
+int symnmf_linear_attention_grad(const symnmf_attend_desc* d, const void* q, const void* k,
+                                 const void* v, const float* decay, const int32_t* lengths,
+                                 const float* state, const void* dout, const float* dlast, void* dq,
+                                 void* dk, void* dv, float* dstate, void* ws, size_t ws_bytes,
+                                 void* hip_stream);
+
+/* One step of a live stream: steps = 1 in the descriptor (the strides of a step
+ * are not used); state -> new_state, which may be the same buffer; o (batch x
+ * heads x dv, dense). Every product and sum in float32.
+ * Errors: E_INVALID, E_HIP. */
+int symnmf_linear_attention_step(const symnmf_attend_desc* d, const void* q, const void* k,
+                                 const void* v, const float* decay, const float* state, void* o,
+                                 float* new_state, void* hip_stream);
+
+/* Rotary positions. The first `dims` (even) channels of each head's row of
+ * `width` are pairs, (i, i + dims / 2) or (interleaved) (2i, 2i + 1), turned by
+ * the angle positions[b, t] * freqs[i]:
+ *   (x1, x2) -> amplitude (x1 cos - x2 sin, x2 cos + x1 sin);
+ * the others are copied. inverse = 1 turns back, with the same amplitude: the
+ * gradient at x from that at out. positions: int32 or int64 (any value), element
+ * (b, t) at b * pos_batch + t * pos_step; freqs: dims / 2 float64, radians a
+ * position; the angle is taken in float64, so far positions lose nothing. out may
+ * be x itself, with the same strides.
+ * Errors: E_INVALID, E_HIP. */
+int symnmf_rotary(int type, int64_t batch, int64_t steps, int32_t heads, int32_t width,
+                  int32_t dims, int interleaved, int inverse, float amplitude, const void* x,
+                  int64_t x_batch, int64_t x_step, int64_t x_head, const void* positions,
+                  int position_type, int64_t pos_batch, int64_t pos_step, const double* freqs,
+                  void* out, int64_t out_batch, int64_t out_step, int64_t out_head,
+                  void* hip_stream);
+
+/* A tensor of symnmf_adamw: n dense elements of each. m and v: float32 (32-bit
+ * states), or float8 e4m3 with m_scale and v_scale (8-bit states: one float32
+ * for each 256 elements, ceil(n / 256)). master (nullable): the parameter in
+ * float32, which the update is made on; param then receives its rounding. */
+typedef struct symnmf_adamw_tensor {
+    void* param;
+    const void* grad;
+    void *m, *v;
+    float *m_scale, *v_scale;
+    float* master;
+    int64_t n;
+} symnmf_adamw_tensor;
+
+/* One AdamW step over `count` tensors (a host array, read during the call), in
+ * place, as few launches as 48 tensors each allow:
+ *   g = grad_scale grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps).
+ * state_bits 32 or 8. In 8 bits m is code * m_scale and sqrt(v) code * v_scale,
+ * codes rounded to nearest, a scale the largest finite magnitude of its block
+ * over 448; a root above zero is never held as zero; what is not finite is held
+ * as NaN. All zeros is a valid first state, scales included. step >= 1, or
+ * step_dev (nullable, one device int64) instead, lr_dev (nullable, one device
+ * float32) instead of lr, grad_scale_dev (nullable, one device float32) times
+ * grad_scale: read when the launch runs, so that a captured call can be replayed
+ * with other values. No two tensors may share memory.
+ * Errors: E_INVALID, E_HIP. */
+int symnmf_adamw(int param_type, int grad_type, int state_bits, const symnmf_adamw_tensor* tensors,
+                 int32_t count, double lr, double beta1, double beta2, double eps,
+                 double weight_decay, int64_t step, float grad_scale, const int64_t* step_dev,
+                 const float* lr_dev, const float* grad_scale_dev, void* hip_stream);
+
 const char* symnmf_status_string(int status);
 int symnmf_abi_version(void);
 

@@ -31,6 +31,8 @@ F32, BF16, F16 = 0, 1, 2
 I32, I64 = 0, 1
 SCAN_CHUNK = 128  # steps between the states a gated scan keeps for its gradient
 MAX_BATCH = 65535 # most batch rows of one gated scan call (the binding makes several)
+MAX_HEAD = 256    # most columns of a linear attention's head
+ADAM_BLOCK = 256  # elements of an 8-bit optimizer state that share a scale
 MAX_TOP = 32      # most alternatives per row of token_logprobs
 (PROF_SH_FULL, PROF_SH_SAMPLED, PROF_SH_PROBE, PROF_BUILD_GRAM, PROF_UPDATE,
  PROF_SH_KMEANS, PROF_SH_SYM) = 0, 1, 2, 3, 4, 5, 6
@@ -103,6 +105,38 @@ class FitReport(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class AttendDesc(ctypes.Structure):
+    """symnmf_attend_desc: sizes and strides of a linear attention."""
+    _fields_ = [
+        ("type", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("dk", ctypes.c_int32),
+        ("dv", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("batch", ctypes.c_int64),
+        ("steps", ctypes.c_int64),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("do_stride", ctypes.c_int64 * 3),
+    ]
+
+
+class AdamwTensor(ctypes.Structure):
+    """symnmf_adamw_tensor: one parameter with its gradient and states."""
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+    ]
+
+
 # (name, restype, argtypes) for every symbol include/symnmf.h declares
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -151,6 +185,18 @@ SIGNATURES = [
      [_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _I32, _P, _P, _P, _Z, _P]),
     ("symnmf_token_logprobs_grad", _I,
      [_P, _I, _I64, _I64, _I64, _P, _I, _F, _P, _P, _P, _P, _P, _I64, _P]),
+    ("symnmf_linear_attention_ws_bytes", _Z, [ctypes.POINTER(AttendDesc), _I]),
+    ("symnmf_linear_attention", _I,
+     [ctypes.POINTER(AttendDesc), _P, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    ("symnmf_linear_attention_grad", _I,
+     [ctypes.POINTER(AttendDesc), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    ("symnmf_linear_attention_step", _I,
+     [ctypes.POINTER(AttendDesc), _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("symnmf_rotary", _I,
+     [_I, _I64, _I64, _I32, _I32, _I32, _I, _I, _F, _P, _I64, _I64, _I64, _P, _I, _I64, _I64, _P, _P,
+      _I64, _I64, _I64, _P]),
+    ("symnmf_adamw", _I,
+     [_I, _I, _I, ctypes.POINTER(AdamwTensor), _I32, _D, _D, _D, _D, _D, _I64, _F, _P, _P, _P, _P]),
     ("symnmf_profile_enable", None, [ctypes.c_int]),
     ("symnmf_profile_reset", None, []),
     ("symnmf_profile_read", ctypes.c_int,

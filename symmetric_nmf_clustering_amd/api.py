@@ -695,6 +695,347 @@ def token_logprobs_grad(logits: torch.Tensor, tokens: torch.Tensor, lse: torch.T
     return out
 
 
+# ---- layers over event streams ------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _attend_desc(type_code, heads, kv_heads, dk, dv, scale, batch, steps, q, k, v, d):
+    """(descriptor, workspace bytes of the call, of its gradient) of these sizes and strides."""
+    desc = L.AttendDesc(type_code, heads, kv_heads, dk, dv, scale, batch, steps, q, k, v, d)
+    lib = L.load()
+    sizes = [lib.symnmf_linear_attention_ws_bytes(ctypes.byref(desc), grad) for grad in (0, 1)]
+    return desc, sizes[0], sizes[1]
+
+
+def _head_rows(t: torch.Tensor, name: str, dims: int, like: Optional[torch.Tensor] = None):
+    """(type code, strides of all but the last dimension) of rows of heads."""
+    code = _seq_tensor(t, name, dtype=None if like is None else like.dtype,
+                       device=None if like is None else like.device)
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+    if t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} needs unit stride within a head")
+    return code, t.stride()[:-1]
+
+
+def _attend_call(q, k, v, decay, scale, do=None):
+    """Checks of a linear attention's tensors (with a dimension of steps, or of one
+    step without); (descriptor, workspace bytes, workspace bytes of the gradient)."""
+    dims = q.dim() if isinstance(q, torch.Tensor) and q.dim() == 3 and do is None else 4
+    code, qs = _head_rows(q, "q", dims)
+    _, ks = _head_rows(k, "k", dims, q)
+    _, vs = _head_rows(v, "v", dims, q)
+    lead, heads, dk = q.shape[:-2], q.shape[-2], q.shape[-1]
+    kv_heads, dv = k.shape[-2], v.shape[-1]
+    if k.shape[:-2] != lead or v.shape[:-2] != lead or v.shape[-2] != kv_heads or k.shape[-1] != dk:
+        raise ValueError(f"q, k and v do not fit: {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    if heads < 1 or kv_heads < 1 or heads % kv_heads:
+        raise ValueError(f"{kv_heads} key heads do not divide {heads} query heads")
+    if not (1 <= dk <= L.MAX_HEAD and 1 <= dv <= L.MAX_HEAD):
+        raise ValueError(f"heads must have 1 to {L.MAX_HEAD} columns, not {dk} and {dv}")
+    if lead[0] < 1:
+        raise ValueError("q must have at least one batch row")
+    _seq_tensor(decay, "decay", dtype=torch.float32, shape=(heads,), device=q.device)
+    if not decay.is_contiguous():
+        raise ValueError("decay must be contiguous")
+    scale = dk ** -0.5 if scale is None else float(scale)
+    if not math.isfinite(scale):
+        raise ValueError("scale must be finite")
+    ds = (0, 0, 0)
+    if do is not None:
+        _, ds = _head_rows(do, "do", 4, q)
+        if do.shape != (*lead, heads, dv):
+            raise ValueError(f"do must have shape {(*lead, heads, dv)}, not {tuple(do.shape)}")
+    if dims == 3:
+        qs, ks, vs = ((x[0], 0, x[1]) for x in (qs, ks, vs))
+    steps = lead[1] if dims == 4 else 1
+    desc, ws, ws_grad = _attend_desc(code, heads, kv_heads, dk, dv, scale, lead[0], steps, tuple(qs),
+                                     tuple(ks), tuple(vs), tuple(ds))
+    if not ws:
+        raise ValueError(f"sizes out of range: {tuple(q.shape)}, {tuple(k.shape)}, {tuple(v.shape)}")
+    return desc, ws, ws_grad
+
+
+def _bytes_scratch(nbytes: int, device) -> torch.Tensor:
+    if nbytes > 256:
+        return torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
+    ws = _no_scratch.get(device)
+    if ws is None:
+        ws = _no_scratch[device] = workspace(256, device)
+    return ws
+
+
+def _dense(shape, dtype, device) -> torch.Tensor:
+    strides, n = [], 1
+    for size in reversed(shape):
+        strides.append(n)
+        n *= max(size, 1)
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                     state: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None):
+    """Linear attention with a decay for each head: S_t = a S_{t-1} + k_t v_t^T,
+    o_t = scale q_t^T S_t, a = exp(decay). q is batch x steps x heads x dk, k and v
+    batch x steps x kv_heads x dk or dv (dk, dv up to 256; query head h reads key head
+    h // (heads / kv_heads)), all of one type; views with strides are read as they are.
+    ``decay`` (heads, float32) is the logarithm of what a step keeps. ``state`` (batch x
+    heads x dk x dv float32; default zeros) is S before the first step, ``scale``
+    defaults to dk ** -0.5. Steps at and past ``lengths[b]`` (int32) are masked: o is 0
+    there and the state passes. Returns (o, the last state in float32)."""
+    desc, nbytes, _ = _attend_call(q, k, v, decay, scale)
+    if q.dim() != 4:
+        raise ValueError("q must be batch x steps x heads x dk")
+    dev = q.device
+    shape = (desc.batch, desc.heads, desc.dk, desc.dv)
+    lengths_p = _lengths_ptr(lengths, desc.batch, dev)
+    state_p = _state_ptr(state, "state", shape, dev)
+    o = _dense((desc.batch, desc.steps, desc.heads, desc.dv), q.dtype, dev)
+    last = _dense(shape, torch.float32, dev)
+    ws = _bytes_scratch(nbytes, dev)
+    st = L.load().symnmf_linear_attention(
+        ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), lengths_p,
+        state_p, o.data_ptr(), last.data_ptr(), ws.data_ptr(), ws.numel(), _here(dev))
+    L.check(st, "symnmf_linear_attention")
+    return o, last
+
+
+def linear_attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                          do: torch.Tensor, dlast: Optional[torch.Tensor] = None,
+                          state: Optional[torch.Tensor] = None,
+                          lengths: Optional[torch.Tensor] = None, scale: Optional[float] = None):
+    """Gradient of ``linear_attention`` from ``do`` (at o) and ``dlast`` (at the last
+    state), with the forward's other arguments. Returns (dq, dk, dv, dstate): in the
+    inputs' type and shapes, a shared key head's summed over its query heads; dstate
+    float32. The decays are constants and have none."""
+    if not isinstance(do, torch.Tensor):
+        raise ValueError("do must be a HIP device tensor")
+    desc, _, nbytes = _attend_call(q, k, v, decay, scale, do)
+    dev = q.device
+    shape = (desc.batch, desc.heads, desc.dk, desc.dv)
+    lengths_p = _lengths_ptr(lengths, desc.batch, dev)
+    state_p = _state_ptr(state, "state", shape, dev)
+    dlast_p = _state_ptr(dlast, "dlast", shape, dev)
+    dq, dk, dv = (_dense(tuple(x.shape), q.dtype, dev) for x in (q, k, v))
+    dstate = _dense(shape, torch.float32, dev)
+    ws = _bytes_scratch(nbytes, dev)
+    st = L.load().symnmf_linear_attention_grad(
+        ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), lengths_p,
+        state_p, do.data_ptr(), dlast_p, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+        dstate.data_ptr(), ws.data_ptr(), ws.numel(), _here(dev))
+    L.check(st, "symnmf_linear_attention_grad")
+    return dq, dk, dv, dstate
+
+
+def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                          state: torch.Tensor, scale: Optional[float] = None,
+                          out_state: Optional[torch.Tensor] = None):
+    """One step of ``linear_attention`` for live streams: q batch x heads x dk, k and v
+    batch x kv_heads x dk or dv, state batch x heads x dk x dv float32. Returns (o batch
+    x heads x dv, the new state), the state in ``out_state`` if given (``state`` itself
+    may be: it is then updated in place)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a HIP device tensor, batch x heads x dk")
+    desc, _, _ = _attend_call(q, k, v, decay, scale)
+    dev = q.device
+    shape = (desc.batch, desc.heads, desc.dk, desc.dv)
+    if state is None:
+        raise ValueError("state is needed")
+    state_p = _state_ptr(state, "state", shape, dev)
+    new = _dense(shape, torch.float32, dev) if out_state is None else out_state
+    new_p = _state_ptr(new, "out_state", shape, dev)
+    o = _dense((desc.batch, desc.heads, desc.dv), q.dtype, dev)
+    st = L.load().symnmf_linear_attention_step(
+        ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), state_p,
+        o.data_ptr(), new_p, _here(dev))
+    L.check(st, "symnmf_linear_attention_step")
+    return o, new
+
+
+def rotary_freqs(dims: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original: int = 4096, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """(frequencies, amplitude) for ``rotary``: base ** (-2 i / dims) radians a position,
+    i < dims / 2, in float64. Contexts ``factor`` times longer than the ``original`` one
+    are reached by ``scaling``: "linear" divides every frequency by factor; "base" raises
+    the base to base * factor ** (dims / (dims - 2)), which keeps the fastest pair and
+    divides the slowest by factor; "parts" keeps pairs that turn at least ``fast`` times
+    within the original context, divides those that turn at most ``slow`` times, goes
+    linearly between, and has the amplitude 1 + 0.1 ln(factor) (1 otherwise)."""
+    if dims < 2 or dims % 2:
+        raise ValueError("dims must be even and at least 2")
+    if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive and finite")
+    amplitude = 1.0
+    if scaling == "base":
+        if dims < 4:
+            raise ValueError('scaling "base" needs dims of at least 4')
+        base = base * factor ** (dims / (dims - 2))
+    f = base ** (-torch.arange(0, dims, 2, dtype=torch.float64) / dims)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        if not (original > 0 and fast > slow >= 0):
+            raise ValueError("original must be positive, and fast above slow")
+        keep = ((original * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+        amplitude = 1.0 + 0.1 * math.log(factor)
+    elif scaling not in ("none", "base"):
+        raise ValueError(f'scaling must be "none", "linear", "base" or "parts", not {scaling!r}')
+    return f.to(device), amplitude
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout: str = "half",
+           amplitude: float = 1.0, inverse: bool = False,
+           out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Turns the heads of x (tokens x heads x width, or batch x steps x heads x width; any
+    strides between rows, so q and k of one projection can go together) by their tokens'
+    ``positions`` (int32 or int64, of x's shape without heads and width; an expanded view
+    is read as it is). ``freqs`` (float64, see ``rotary_freqs``) turns the first 2 *
+    len(freqs) channels as pairs: (i, i + len(freqs)) for layout "half", (2i, 2i + 1) for
+    "interleaved"; the others stay. ``inverse`` turns back by the same ``amplitude``: the
+    gradient at x from the one at the result. ``out`` may be x."""
+    if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
+        raise ValueError("x must be a HIP device tensor, tokens x heads x width or batch x steps x "
+                         "heads x width")
+    code, xs = _head_rows(x, "x", x.dim())
+    dev = x.device
+    pt = _seq_tensor(positions, "positions", _INDEX, shape=x.shape[:-2], device=dev)
+    _seq_tensor(freqs, "freqs", {torch.float64: 0}, device=dev)
+    heads, width = x.shape[-2:]
+    if freqs.dim() != 1 or not freqs.is_contiguous() or 2 * freqs.numel() > width:
+        raise ValueError(f"freqs must be one dense row of at most {width // 2}")
+    if heads < 1 or width < 1:
+        raise ValueError("x must have a head and a column")
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f'layout must be "half" or "interleaved", not {layout!r}')
+    if not math.isfinite(amplitude):
+        raise ValueError("amplitude must be finite")
+    if out is None:
+        out = _dense(tuple(x.shape), x.dtype, dev)
+    elif out is not x:
+        _seq_tensor(out, "out", dtype=x.dtype, shape=x.shape, device=dev)
+    os_ = _head_rows(out, "out", x.dim())[1]
+    if out.data_ptr() == x.data_ptr() and os_ != xs and x.numel():
+        raise ValueError("out shares x's memory in another layout")
+    if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())) and x.numel():
+        raise ValueError("out has overlapping rows")
+    ps = positions.stride()
+    if x.dim() == 3:
+        batch, steps, xs, os_, ps = 1, x.shape[0], (0, *xs), (0, *os_), (0, *ps)
+    else:
+        batch, steps = x.shape[:2]
+    st = L.load().symnmf_rotary(
+        code, batch, steps, heads, width, 2 * freqs.numel(), int(layout == "interleaved"), int(inverse),
+        amplitude, x.data_ptr(), *xs, positions.data_ptr(), pt, *ps, freqs.data_ptr(), out.data_ptr(),
+        *os_, _here(dev))
+    L.check(st, "symnmf_rotary")
+    return out
+
+
+_CODES = {torch.float8_e4m3fn: 0}
+_FULL = {torch.float32: L.F32}
+
+
+def adamw_states(params, bits: int = 32):
+    """First states for ``adamw_step``: (m, v, m_scale, v_scale), lists of zeros like
+    ``params``; bits=32: m and v float32, no scales (None); bits=8: m and v float8 e4m3
+    with a float32 scale for each 256 elements."""
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    if bits == 32:
+        return ([torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params],
+                [torch.zeros(p.shape, dtype=torch.float32, device=p.device) for p in params],
+                None, None)
+
+    def codes(p):
+        return torch.zeros(p.shape, dtype=torch.uint8, device=p.device).view(torch.float8_e4m3fn)
+
+    def scales(p):
+        return torch.zeros(-(-p.numel() // L.ADAM_BLOCK), dtype=torch.float32, device=p.device)
+
+    return ([codes(p) for p in params], [codes(p) for p in params],
+            [scales(p) for p in params], [scales(p) for p in params])
+
+
+def _device_scalar(x, name: str, dtype, device):
+    """(value, pointer) of an argument that may be a number or one on the device."""
+    if isinstance(x, torch.Tensor):
+        _seq_tensor(x, name, {dtype: 0}, device=device)
+        if x.numel() != 1:
+            raise ValueError(f"{name} must hold one number")
+        return None, x.data_ptr()
+    return x, None
+
+
+def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999,
+               eps: float = 1e-8, weight_decay: float = 0.01, masters=None, m_scale=None,
+               v_scale=None, grad_scale=1.0) -> None:
+    """One AdamW step, in place, over lists of dense tensors of one device: params and
+    their gradients (float32, bfloat16 or float16; one launch for 48 tensors of the same
+    pair of types), states m and v (``adamw_states``; with m_scale and v_scale in 8 bits,
+    where v holds the root of the second moment), and, if given, ``masters`` (float32
+    copies that the update is made on; params receive their rounding):
+        g = grad_scale * grad, m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
+        p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+    ``step`` is 1 for the first one. step (int64), lr and grad_scale (float32) may be device
+    tensors of one element, read when the step runs: a captured step follows them. A
+    parameter whose gradient is None is left alone. No two tensors may share memory."""
+    lists = {"grads": grads, "m": m, "v": v, "masters": masters, "m_scale": m_scale, "v_scale": v_scale}
+    for name, x in lists.items():
+        if x is None and name in ("masters", "m_scale", "v_scale"):
+            continue
+        if len(x) != len(params):
+            raise ValueError(f"{name} must have an entry for each of {len(params)} params")
+    if (m_scale is None) != (v_scale is None):
+        raise ValueError("m_scale and v_scale go together")
+    low = m_scale is not None
+    used = [i for i in range(len(params)) if grads[i] is not None]
+    if not used:
+        return
+    dev = params[used[0]].device
+    held = []  # dense copies live until the launch is made
+    groups: dict = {}
+    seen = set()
+    for i in used:
+        p, g = params[i], grads[i]
+        key = (_seq_tensor(p, "params", device=dev), _seq_tensor(g, "grads", shape=p.shape, device=dev))
+        if not g.is_contiguous():
+            g = g.contiguous()
+            held.append(g)
+        written = [p, m[i], v[i]]
+        for name, x in (("m", m[i]), ("v", v[i])):
+            _seq_tensor(x, name, _CODES if low else _FULL, shape=p.shape, device=dev)
+        if masters is not None:
+            _seq_tensor(masters[i], "masters", _FULL, shape=p.shape, device=dev)
+            written.append(masters[i])
+        n = p.numel()
+        if low:
+            for name, x in (("m_scale", m_scale[i]), ("v_scale", v_scale[i])):
+                _seq_tensor(x, name, _FULL, shape=(-(-n // L.ADAM_BLOCK),), device=dev)
+            written += [m_scale[i], v_scale[i]]
+        if n == 0:
+            continue
+        at = [x.data_ptr() for x in written]
+        if not all(x.is_contiguous() for x in written):
+            raise ValueError("params and states must be contiguous")
+        if len(seen.union(at)) != len(seen) + len(at):
+            raise ValueError("two of the tensors share memory")
+        seen.update(at)
+        groups.setdefault(key, []).append(
+            (at[0], g.data_ptr(), at[1], at[2], at[-2] if low else None, at[-1] if low else None,
+             at[3] if masters is not None else None, n))
+    step, step_p = _device_scalar(step, "step", torch.int64, dev)
+    lr, lr_p = _device_scalar(lr, "lr", torch.float32, dev)
+    grad_scale, scale_p = _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
+    stream = _here(dev)
+    for (pt, gt), rows in groups.items():
+        table = (L.AdamwTensor * len(rows))(*rows)
+        st = L.load().symnmf_adamw(pt, gt, 8 if low else 32, table, len(rows), 0.0 if lr is None else lr,
+                                   beta1, beta2, eps, weight_decay, 1 if step is None else step,
+                                   1.0 if grad_scale is None else grad_scale, step_p, lr_p, scale_p,
+                                   stream)
+        L.check(st, "symnmf_adamw")
+
+
 # ---- kernel timing ---------------------------------------------------------
 def profile_enable(on: bool = True):
     L.load().symnmf_profile_enable(1 if on else 0)

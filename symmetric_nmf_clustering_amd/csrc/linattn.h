@@ -1,0 +1,493 @@
+// The walk of decayed linear attention over time (see AttendRun in layers.h),
+// instantiated for each element type by k_linattn_*.hip.
+//
+// Steps are taken in chunks of C. With W = a^(u - w) for w <= u inside a chunk,
+//   P = (X Y^T) . W,   out = P Z + diag(a^(u + in_pow)) X S,
+//   S <- a^n S + Y^T diag(a^(n - in_pow - w)) Z,
+// four matrix products a chunk. A workgroup of NW waves walks one head (and one
+// segment of its time) for 16 NW columns of z; wave i holds the dx x 16 block of
+// S of its own columns in accumulators, so S is never stored: as the product's
+// result a lane has S[4g + r][l % 16] (g = l / 16), which is also what the A
+// operand of the next product wants of S^T if the depth index runs through the
+// rows 4g + r and 16 + 4g + r. Every operand here takes its depth in that order.
+// Results come out transposed (a lane has 4 columns of one step): 8 or 16 bytes a
+// store. P alone passes through LDS, in the order its reader's lanes want it.
+//
+// bf16: products on the bf16 matrix cores. P and, in X S, the state are rounded to
+// bf16 (as the inputs and the output are: each costs the output at most what its
+// own rounding does). The state itself stays at float32's precision: the weights
+// go to z, and w z is split exactly into three bf16 parts, three products each.
+// fp32: 16x16x4 float32 products. fp16: widened to float32 as it is loaded.
+#pragma once
+
+#include "bf16split.h"
+#include "layers.h"
+
+namespace symnmf {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// LDS of one wave is in order; across waves: their LDS writes are done before the
+// barrier. Global loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <class T>
+struct InLds {  // how a tile is held
+    using type = float;
+};
+template <>
+struct InLds<bf16_t> {
+    using type = bf16_t;
+};
+
+// 32 deep operands of a product: 8 values a lane. rows(p): depth 8g + j, p at the
+// lane's own row; split(p): depth 4g + j and 16 + 4g + j (see above); column(t,
+// stride): the same depth order down the rows of a tile, lane l % 16's column.
+template <class LT>
+struct Op;
+
+template <>
+struct Op<bf16_t> {
+    using F = u32x4;
+    static __device__ __forceinline__ F rows(const bf16_t* p, int g) {
+        return *reinterpret_cast<const u32x4*>(p + 8 * g);
+    }
+    static __device__ __forceinline__ F split(const bf16_t* p, int g) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p + 4 * g);
+        const uint2 b = *reinterpret_cast<const uint2*>(p + 16 + 4 * g);
+        return F{a.x, a.y, b.x, b.y};
+    }
+    static __device__ __forceinline__ F column(const bf16_t* t, int stride, int lane) {
+        // a 4 x 16 block for each 16 lanes, read transposed: lane i asks for 4 elements of row
+        // i / 4 and receives column i
+        const bf16_t* p = t + (4 * (lane >> 4) + ((lane & 15) >> 2)) * stride + 4 * (lane & 3);
+        typedef __attribute__((address_space(3))) s16x4 lds4;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 16 * stride));
+        const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+        return F{ua.x, ua.y, ub.x, ub.y};
+    }
+    // the lane's values of two 16-deep blocks of a result
+    static __device__ __forceinline__ F of(const floatx4& a, const floatx4& b) {
+        return F{pack(a[0], a[1]), pack(a[2], a[3]), pack(b[0], b[1]), pack(b[2], b[3])};
+    }
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        const f32x2 v = {a, b};
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    }
+    static __device__ __forceinline__ floatx4 mma(const F& a, const F& b, floatx4 c) {
+        return mfma_bf16(a, b, c);
+    }
+    // a times (w . b) to float32's precision
+    struct W {
+        F p[3];
+    };
+    static __device__ __forceinline__ W weigh(const F& b, const float (&w)[8]) {
+        W o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t p1, p2, p3;
+            split3_pair(__uint_as_float(b[i] << 16) * w[2 * i],
+                        __uint_as_float(b[i] & 0xffff0000u) * w[2 * i + 1], p1, p2, p3);
+            o.p[0][i] = p1;
+            o.p[1][i] = p2;
+            o.p[2][i] = p3;
+        }
+        return o;
+    }
+    static __device__ __forceinline__ floatx4 mma(const F& a, const W& b, floatx4 c) {
+        c = mfma_bf16(a, b.p[2], c);
+        c = mfma_bf16(a, b.p[1], c);
+        return mfma_bf16(a, b.p[0], c);
+    }
+    static __device__ __forceinline__ void put4(bf16_t* p, const floatx4& v) {
+        *reinterpret_cast<uint2*>(p) = uint2{pack(v[0], v[1]), pack(v[2], v[3])};
+    }
+};
+
+template <>
+struct Op<float> {
+    struct F {
+        float v[8];
+    };
+    static __device__ __forceinline__ F two(const float* p, const float* q) {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
+        return F{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+    }
+    static __device__ __forceinline__ F rows(const float* p, int g) {
+        return two(p + 8 * g, p + 8 * g + 4);
+    }
+    static __device__ __forceinline__ F split(const float* p, int g) {
+        return two(p + 4 * g, p + 16 + 4 * g);
+    }
+    static __device__ __forceinline__ F column(const float* t, int stride, int lane) {
+        F o;
+        const float* p = t + 4 * (lane >> 4) * stride + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] = p[((j & 3) + (j >> 2) * 16) * stride];
+        return o;
+    }
+    static __device__ __forceinline__ F of(const floatx4& a, const floatx4& b) {
+        return F{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
+    }
+    static __device__ __forceinline__ floatx4 mma(const F& a, const F& b, floatx4 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = mfma16x16x4(a.v[j], b.v[j], c);
+        return c;
+    }
+    static __device__ __forceinline__ F weigh(const F& b, const float (&w)[8]) {
+        F o;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o.v[j] = b.v[j] * w[j];
+        return o;
+    }
+    static __device__ __forceinline__ void put4(float* p, const floatx4& v) {
+        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+    }
+};
+
+// The rows of one operand of a head.
+template <class T>
+struct Rows {
+    const T* p;       // of the batch row and head
+    int64_t stride;   // of a step, negative in reverse
+    int d;            // columns
+};
+
+// A chunk's C x COLS tile on its way from memory through registers to LDS, by NT
+// threads. Rows past `rows` and columns past d are zeros.
+template <class T, class LT, int C, int COLS, int NT>
+struct Tile {
+    static constexpr int V = 16 / sizeof(T), G = COLS / V, N = (C * G + NT - 1) / NT;
+    static constexpr int STRIDE = COLS + 16 / (int)sizeof(LT);
+    Vec<T, V> r[N];
+
+    __device__ __forceinline__ void load(const Rows<T>& m, int64_t u0, int rows, int c0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * NT, row = at / G, c = c0 + at % G * V;
+            r[i] = Vec<T, V>{};
+            if (row >= rows || c >= m.d) continue;  // rows <= C
+            const T* p = m.p + (u0 + row) * m.stride + c;
+            if (c + V <= m.d) {
+                r[i] = load_vec<T, V>(p);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (c + j < m.d) r[i].e[j] = p[j];
+            }
+        }
+    }
+    __device__ __forceinline__ void store(LT* t) const {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * NT, row = at / G, c = at % G * V;
+            if (C * G % NT && row >= C) continue;
+            if constexpr (sizeof(T) == sizeof(LT)) {
+                *reinterpret_cast<u32x4*>(t + row * STRIDE + c) = __builtin_bit_cast(u32x4, r[i]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) t[row * STRIDE + c + j] = to_f32(r[i].e[j]);
+            }
+        }
+    }
+};
+
+template <class T, int DX, int NW, bool OUT>
+struct WalkSizes {
+    using LT = typename InLds<T>::type;
+    static constexpr int C = sizeof(LT) == 2 ? 64 : 32;
+    static constexpr int NT = 64 * NW, ZC = 16 * NW;
+    using TX = Tile<T, LT, C, DX, NT>;
+    using TZ = Tile<T, LT, C, ZC, NT>;
+    struct Lds {
+        LT x[OUT ? C * TX::STRIDE : 8];
+        LT y[C * TX::STRIDE];
+        LT z[C * TZ::STRIDE];
+        LT p[OUT ? C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
+        float pw[C + 1];        // a^0 ... a^C
+    };
+};
+
+__device__ __forceinline__ double ln_decay(const float* decay, int head) {
+    const double g = decay[head];
+    return g < -200.0 ? -200.0 : g;  // exp(-200) is 0 in float32, and a^0 stays 1
+}
+
+// blockIdx.x (+ first): column tile, segment and head; blockIdx.y: the run.
+template <class T, int DX, int NW, bool OUT>
+__global__ __launch_bounds__(64 * NW) void attend_walk_kernel(AttendArgs a, int64_t first,
+                                                              int64_t items, int ztiles) {
+    using Z = WalkSizes<T, DX, NW, OUT>;
+    using LT = typename Z::LT;
+    using O = Op<LT>;
+    constexpr int C = Z::C, NX = DX / 16, NB = C / 16, XS = Z::TX::STRIDE, ZS = Z::TZ::STRIDE;
+    __shared__ alignas(16) typename Z::Lds lds;
+
+    // items go round the XCDs; the column tiles of one item to the same XCD, whose L2
+    // then has x and y for all of them
+    const int64_t id = first + blockIdx.x;
+    const int64_t grp = id >> 3;
+    const int zt = (int)(grp % ztiles);
+    const int64_t item = (grp / ztiles) + (id & 7) * ((items + 7) >> 3);
+    if (grp / ztiles >= ((items + 7) >> 3) || item >= items) return;
+    const AttendRun& R = a.run[blockIdx.y];
+    const int seg = (int)(item % a.nseg);
+    const int64_t bh = item / a.nseg;
+    const int64_t b = bh / a.heads;
+    const int head = (int)(bh % a.heads);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    const int z0 = zt * Z::ZC, zw = z0 + wave * 16;
+    if (z0 >= R.dz) return;  // the whole workgroup
+
+    int64_t len = a.steps;
+    if (a.lengths) {
+        const int64_t n = a.lengths[b];
+        len = n < 0 ? 0 : (n < len ? n : len);
+    }
+    const int64_t u_begin = seg * a.seg_len;
+    int64_t u_end = u_begin + a.seg_len;
+    if (u_end > a.steps) u_end = a.steps;
+    if (!OUT && (u_begin >= len || seg == a.nseg - 1)) return;  // the join does not read these
+
+    const double gd = ln_decay(a.decay, head);
+    for (int i = threadIdx.x; i <= C; i += Z::NT) lds.pw[i] = (float)exp(gd * i);
+    if constexpr (OUT) {  // blocks above the diagonal that a 32-deep step reads
+        for (int i = threadIdx.x; i < C * C; i += Z::NT) lds.p[i] = LT{};
+    }
+
+    const int64_t dir = R.reverse ? -1 : 1, from = R.reverse ? len - 1 : 0;
+    auto rows_of = [&](const void* p, int64_t sb, int64_t st, int64_t sh, int grp_, int d) {
+        return Rows<T>{static_cast<const T*>(p) + b * sb + from * st + (head / grp_) * sh, dir * st,
+                       d};
+    };
+    const Rows<T> mx = rows_of(R.x, R.xb, R.xt, R.xh, R.xg, R.dx);
+    const Rows<T> my = rows_of(R.y, R.yb, R.yt, R.yh, R.yg, R.dx);
+    const Rows<T> mz = rows_of(R.z, R.zb, R.zt, R.zh, R.zg, R.dz);
+
+    // the state at the segment's start
+    floatx4 S[NX];
+    {
+        const float* s = nullptr;
+        int64_t si = 0, sj = 0;
+        if (OUT && a.nseg > 1) {
+            s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
+            si = R.dz;
+            sj = 1;
+        } else if (OUT && R.s0) {
+            s = R.s0 + bh * ((int64_t)R.dx * R.dz);
+            si = R.s0_i;
+            sj = R.s0_j;
+        }
+        const int j = zw + l16;
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * g + r;
+                S[i][r] = s && row < R.dx && j < R.dz ? s[row * si + j * sj] : 0.f;
+            }
+    }
+
+    typename Z::TX rx, ry;
+    typename Z::TZ rz;
+    auto valid = [&](int64_t u0) {  // steps of the chunk at u0
+        const int64_t n = (len < u_end ? len : u_end) - u0;
+        return (int)(n < 0 ? 0 : (n < C ? n : C));
+    };
+    auto fetch = [&](int64_t u0) {
+        const int n = valid(u0);
+        if (OUT) rx.load(mx, u0, n, 0);
+        ry.load(my, u0, n, 0);
+        rz.load(mz, u0, n, z0);
+    };
+    if (u_begin < u_end) fetch(u_begin);
+    for (int64_t u0 = u_begin; u0 < u_end; u0 += C) {
+        const int n = valid(u0);
+        if (n == 0) break;
+        lds_barrier();  // the tiles of the last chunk are read
+        if (OUT) rx.store(lds.x);
+        ry.store(lds.y);
+        rz.store(lds.z);
+        lds_barrier();
+        if (u0 + C < u_end) fetch(u0 + C);
+
+        if constexpr (OUT) {
+            // P^T in 16 x 16 blocks on and below the diagonal, shared out among the waves
+            constexpr int BLOCKS = NB * (NB + 1) / 2;
+#pragma unroll
+            for (int q = 0; q < (BLOCKS + NW - 1) / NW; ++q) {
+                const int at = wave + q * NW;
+                if (at >= BLOCKS) break;
+                const int bu = (at >= 1) + (at >= 3) + (at >= 6), bw = at - bu * (bu + 1) / 2;
+                floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+                const LT* py = lds.y + (16 * bw + l16) * XS;
+                const LT* px = lds.x + (16 * bu + l16) * XS;
+#pragma unroll
+                for (int k = 0; k < DX / 32; ++k)
+                    acc = O::mma(O::rows(py + 32 * k, g), O::rows(px + 32 * k, g), acc);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int u = 16 * bu + l16, w = 16 * bw + 4 * g + r;
+                    acc[r] = w <= u ? acc[r] * (R.p_scale * lds.pw[u - w < 0 ? 0 : u - w]) : 0.f;
+                }
+                O::put4(lds.p + ((bu * NB + bw) * 64 + lane) * 4, acc);
+            }
+            lds_barrier();
+        }
+
+        typename O::F zf[C / 32];
+#pragma unroll
+        for (int k = 0; k < C / 32; ++k)
+            zf[k] = O::column(lds.z + 32 * k * ZS + 16 * wave, ZS, lane);
+
+        if constexpr (OUT) {
+            typename O::F sf[DX / 32];
+#pragma unroll
+            for (int k = 0; k < DX / 32; ++k) sf[k] = O::of(S[2 * k], S[2 * k + 1]);
+#pragma unroll
+            for (int bu = 0; bu < NB; ++bu) {
+                floatx4 acc = {0.f, 0.f, 0.f, 0.f};
+                const int u = 16 * bu + l16;
+                const LT* px = lds.x + u * XS;
+#pragma unroll
+                for (int k = 0; k < DX / 32; ++k)
+                    acc = O::mma(sf[k], O::split(px + 32 * k, g), acc);
+                acc *= R.in_scale * lds.pw[u + R.in_pow];
+#pragma unroll
+                for (int k = 0; k <= bu / 2; ++k) {
+                    typename O::F pf;
+                    const LT* pp = lds.p + ((bu * NB + 2 * k) * 64 + lane) * 4;
+                    if constexpr (sizeof(LT) == 2) {
+                        const uint2 p0 = *reinterpret_cast<const uint2*>(pp);
+                        const uint2 p1 = *reinterpret_cast<const uint2*>(pp + 256);
+                        pf = typename O::F{p0.x, p0.y, p1.x, p1.y};
+                    } else {
+                        pf = O::two(pp, pp + 256);
+                    }
+                    acc = O::mma(zf[k], pf, acc);
+                }
+                const int z = zw + 4 * g;
+                if (u < n && z < R.dz) {
+                    const int64_t t = from + dir * (u0 + u);
+                    const int64_t e = ((b * a.steps + t) * a.heads + head) * R.dz + z;
+                    const int cols = R.dz - z < 4 ? R.dz - z : 4;
+                    if (R.out32) {
+                        float* p = static_cast<float*>(R.out) + e;
+                        if (cols == 4) {
+                            store_vec<float, 4>(p, {{acc[0], acc[1], acc[2], acc[3]}});
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 3; ++r)
+                                if (r < cols) p[r] = acc[r];
+                        }
+                    } else {
+                        T* p = static_cast<T*>(R.out) + e;
+                        if (cols == 4) {
+                            store_vec<T, 4>(p, {{from_f32<T>(acc[0]), from_f32<T>(acc[1]),
+                                                 from_f32<T>(acc[2]), from_f32<T>(acc[3])}});
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < 3; ++r)
+                                if (r < cols) p[r] = from_f32<T>(acc[r]);
+                        }
+                    }
+                }
+            }
+        }
+
+        // S <- a^n S + Y^T (w Z); rows of z past n are zeros
+        const float an = lds.pw[n];
+#pragma unroll
+        for (int i = 0; i < NX; ++i) S[i] *= an;
+#pragma unroll
+        for (int k = 0; k < C / 32; ++k) {
+            float w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = n - R.in_pow - (32 * k + 4 * g + (j & 3) + (j >> 2) * 16);
+                w[j] = R.st_scale * lds.pw[at < 0 ? 0 : at];
+            }
+            const auto zw8 = O::weigh(zf[k], w);
+#pragma unroll
+            for (int i = 0; i < NX; ++i)
+                S[i] = O::mma(O::column(lds.y + 32 * k * XS + 16 * i, XS, lane), zw8, S[i]);
+        }
+    }
+
+    // steps past the length
+    if constexpr (OUT) {
+        const int64_t lo = u_begin > len ? u_begin : len;
+        const int64_t cells = u_end > lo ? (u_end - lo) * Z::ZC : 0;
+        for (int64_t i = threadIdx.x; i < cells; i += Z::NT) {
+            const int z = z0 + (int)(i % Z::ZC);
+            if (z >= R.dz) continue;
+            const int64_t e = ((b * a.steps + lo + i / Z::ZC) * a.heads + head) * R.dz + z;
+            if (R.out32)
+                static_cast<float*>(R.out)[e] = 0.f;
+            else
+                static_cast<T*>(R.out)[e] = from_f32<T>(0.f);
+        }
+    }
+
+    float* s = nullptr;
+    int64_t si = R.dz, sj = 1;
+    if (!OUT) {
+        s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
+    } else if (seg == a.nseg - 1 && R.s1) {
+        s = R.s1 + bh * ((int64_t)R.dx * R.dz);
+        si = R.s1_i;
+        sj = R.s1_j;
+    }
+    if (s) {
+        const int j = zw + l16;
+#pragma unroll
+        for (int i = 0; i < NX; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int row = 16 * i + 4 * g + r;
+                if (row < R.dx && j < R.dz) s[row * si + j * sj] = S[i][r];
+            }
+    }
+}
+
+template <class T, int DX, int NW>
+hipError_t attend_walk_as(const AttendArgs& a, bool maps, hipStream_t st) {
+    constexpr int ZC = 16 * NW;
+    int dz = 0;
+    for (int r = 0; r < a.nrun; ++r) dz = a.run[r].dz > dz ? a.run[r].dz : dz;
+    const int ztiles = (dz + ZC - 1) / ZC;
+    const int64_t items = a.batch * a.heads * a.nseg;
+    const int64_t blocks = (items + 7) / 8 * 8 * ztiles;
+    return in_launches(blocks, [&](int64_t first, unsigned n) {
+        const dim3 grid(n, (unsigned)a.nrun);
+        if (maps)
+            attend_walk_kernel<T, DX, NW, false><<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
+        else
+            attend_walk_kernel<T, DX, NW, true><<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
+    });
+}
+
+template <class T>
+hipError_t launch_attend_walk(const AttendArgs& a, bool maps, hipStream_t st) {
+    int dx = 0, dz = 0;
+    for (int r = 0; r < a.nrun; ++r) {
+        dx = a.run[r].dx > dx ? a.run[r].dx : dx;
+        dz = a.run[r].dz > dz ? a.run[r].dz : dz;
+    }
+    // two waves where they hold all columns of z, four otherwise
+#define SYMNMF_WALK(DX) \
+    return dz <= 32 ? attend_walk_as<T, DX, 2>(a, maps, st) : attend_walk_as<T, DX, 4>(a, maps, st)
+    if (dx <= 32) SYMNMF_WALK(32);
+    if (dx <= 64) SYMNMF_WALK(64);
+    if (dx <= 128) SYMNMF_WALK(128);
+    SYMNMF_WALK(256);
+#undef SYMNMF_WALK
+}
+
+}  // namespace symnmf

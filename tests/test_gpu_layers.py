@@ -1,0 +1,650 @@
+"""GPU tests of the layer operators against their float64 definitions.
+
+Tolerances are per element, from float32 arithmetic (u = 2^-24), the roundings
+that a type's kernel makes on the way (bfloat16: one of at most 2^-8 relative on
+every term) and the one rounding of the output: see each ``bound``.
+"""
+import numpy as np
+import pytest
+
+from oracle import layers_oracle as lo
+from tests.gpu_util import require_gpu
+from tests.test_gpu_sequence import U, close, dev, types
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- linear attention ---------------------------------------------------------
+
+def attend_bound(kind, steps, dk, dv):
+    """Relative to the sums of absolute values: a term meets at most dk + dv roundings of its
+    dot product, 64 of its chunk, 3 a chunk of 32 steps on the state's way (each product and sum
+    at most 2 u: the matrix cores may truncate), and in bfloat16 one rounding (P, or the state
+    as an operand) of at most 2^-8."""
+    return 2 * U * (dk + dv + 64 + 3 * (steps // 32 + 1) + 16) + (2.0 ** -8 if kind == "bf16" else 0.0)
+
+
+def make(torch, kind, B, T, H, G, dk, dv, seed, lengths=None, decay=None):
+    rng = np.random.default_rng(seed)
+    t, x = {}, {}
+    for name, shape in (("q", (B, T, H, dk)), ("k", (B, T, G, dk)), ("v", (B, T, G, dv)),
+                        ("do", (B, T, H, dv))):
+        t[name], x[name] = dev(torch, rng.standard_normal(shape), kind)
+    for name in ("state", "dlast"):
+        t[name], x[name] = dev(torch, rng.standard_normal((B, H, dk, dv)))
+    t["decay"], x["decay"] = dev(torch, -np.exp(rng.uniform(-7, 0.5, H)) if decay is None else decay)
+    t["lengths"] = x["lengths"] = None
+    if lengths is not None:
+        x["lengths"] = np.asarray(lengths)
+        t["lengths"] = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    return t, x
+
+
+def check_forward(got, x, kind, scale, state=True):
+    B, T, H, dk = x["q"].shape
+    dv = x["v"].shape[3]
+    s = x["state"] if state else None
+    ref = lo.linear_attention(x["q"], x["k"], x["v"], x["decay"], s, x["lengths"], scale)
+    mag = lo.linear_attention(*(abs(x[n]) for n in "qkv"), x["decay"], None if s is None else abs(s),
+                              x["lengths"], scale)
+    c = attend_bound(kind, T, dk, dv)
+    close(got[0], ref[0], c * mag[0], kind)
+    close(got[1], ref[1], attend_bound("fp32", T, dk, dv) * mag[1])
+
+
+def check_grad(got, x, kind, scale, state=True, dlast=True):
+    B, T, H, dk = x["q"].shape
+    dv = x["v"].shape[3]
+    s, d = x["state"] if state else None, x["dlast"] if dlast else None
+    ref = lo.linear_attention_grad(x["q"], x["k"], x["v"], x["decay"], x["do"], d, s, x["lengths"], scale)
+    mag = lo.linear_attention_grad(*(abs(x[n]) for n in "qkv"), x["decay"], abs(x["do"]),
+                                   None if d is None else abs(d), None if s is None else abs(s),
+                                   x["lengths"], scale)
+    # (a shared head's sum adds at most one u a term)
+    c = attend_bound(kind, T, dk, dv) + 2 * U * H
+    for i in range(3):
+        close(got[i], ref[i], c * mag[i], kind)
+    close(got[3], ref[3], attend_bound("fp32", T, dk, dv) * mag[3])
+
+
+SIZES = [(1, 1, 1, 1, 1, 1), (2, 5, 3, 3, 8, 8), (3, 31, 2, 1, 24, 24), (1, 64, 4, 2, 64, 64),
+         (2, 65, 2, 2, 33, 50), (1, 200, 6, 3, 128, 128), (2, 97, 2, 1, 80, 17), (1, 130, 1, 1, 256, 256),
+         (1, 70, 2, 2, 16, 256), (1, 129, 2, 2, 200, 40), (1, 33, 3, 1, 32, 32), (2, 96, 1, 1, 7, 129)]
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("B,T,H,G,dk,dv", SIZES)
+def test_linear_attention(kind, B, T, H, G, dk, dv):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, kind, B, T, H, G, dk, dv, T + dk)
+    scale = dk ** -0.5
+    got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+    check_forward(got, x, kind, scale)
+    again = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    got = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"],
+                                    state=t["state"])
+    check_grad(got, x, kind, scale)
+    again = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"],
+                                      state=t["state"])
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,lengths", [(70, [70, 0, 1, 64, 65]), (1100, [1100, 0, 500, 256, 1]),
+                                       (512, [512, 511, 257, 600, -3]), (33, [32, 33, 31, 0, 2])])
+def test_lengths(kind, T, lengths):
+    """Padded batches: masked steps hold NaN, which nothing reads; some are cut in time."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, kind, 5, T, 2, 1, 24, 40, T, lengths)
+    for b, n in enumerate(lengths):
+        for name in ("q", "k", "v", "do"):
+            t[name][b, max(0, n):] = float("nan")
+            x[name][b, max(0, n):] = 0.0
+    for state in (True, False):
+        s = t["state"] if state else None
+        got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=s, lengths=t["lengths"], scale=0.3)
+        check_forward(got, x, kind, 0.3, state)
+        got = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], state=s,
+                                        dlast=t["dlast"] if state else None, lengths=t["lengths"], scale=0.3)
+        check_grad(got, x, kind, 0.3, state, state)
+        for i, b in ((0, 1), (0, 3)):
+            n = min(max(lengths[b], 0), T)
+            assert not got[i][b, n:].any()
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("B,T,H,dk,dv", [(1, 3000, 2, 64, 64), (1, 2049, 1, 128, 96), (2, 1500, 1, 24, 24)])
+def test_long_histories_are_cut(kind, B, T, H, dk, dv):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, kind, B, T, H, H, dk, dv, 3)
+    got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"], scale=0.2)
+    check_forward(got, x, kind, 0.2)
+    got = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"],
+                                    state=t["state"], scale=0.2)
+    check_grad(got, x, kind, 0.2)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+def test_decays_at_their_ends(kind):
+    """Nothing kept (-inf, and far below), everything kept (0), and a growing memory."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    decay = [-np.inf, -1e30, -300.0, -90.0, -1e-6, 0.0, 0.01]
+    t, x = make(torch, kind, 2, 150, 7, 7, 16, 20, 5, lengths=[150, 77], decay=decay)
+    with np.errstate(invalid="ignore"):
+        got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"], lengths=t["lengths"])
+        check_forward(got, x, kind, 0.25)
+        got = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"],
+                                        state=t["state"], lengths=t["lengths"])
+        check_grad(got, x, kind, 0.25)
+    t["decay"][0] = float("nan")
+    o, last = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+    assert torch.isnan(o[:, :, 0]).all() and torch.isnan(last[:, 0]).all()
+    assert torch.isfinite(o[:, :, 1:]).all() and torch.isfinite(last[:, 1:]).all()
+
+
+def test_strides_alignment_and_broadcast():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    for kind in ("fp32", "bf16", "fp16"):
+        rng = np.random.default_rng(7)
+        B, T, H, G, dk, dv = 2, 67, 4, 2, 24, 33
+        # one projection's columns: q heads, k heads, v heads next to one another, from an odd start
+        wide, wv = dev(torch, rng.standard_normal((B, T, 1 + H * dk + G * dk + G * dv)), kind)
+        t, x = make(torch, kind, B, T, H, G, dk, dv, 8)
+
+        def heads(a, at, n, d):
+            return a[:, :, at:at + n * d].unflatten(2, (n, d)) if hasattr(a, "unflatten") else \
+                a[:, :, at:at + n * d].reshape(B, T, n, d)
+
+        for name, at, n, d in (("q", 1, H, dk), ("k", 1 + H * dk, G, dk), ("v", 1 + (H + G) * dk, G, dv)):
+            t[name], x[name] = heads(wide, at, n, d), heads(wv, at, n, d)
+        t["do"] = t["do"].transpose(0, 1).contiguous().transpose(0, 1)  # steps first
+        args = (t["q"], t["k"], t["v"], t["decay"])
+        check_forward(api.linear_attention(*args, state=t["state"]), x, kind, dk ** -0.5)
+        check_grad(api.linear_attention_grad(*args, t["do"], dlast=t["dlast"], state=t["state"]), x, kind,
+                   dk ** -0.5)
+        # one key row for the whole batch, one gradient row for all steps
+        t["k"], x["k"] = t["k"][:1].expand(B, -1, -1, -1), np.broadcast_to(x["k"][:1], x["k"].shape)
+        t["do"], x["do"] = t["do"][:, :1].expand(-1, T, -1, -1), np.broadcast_to(x["do"][:, :1], x["do"].shape)
+        args = (t["q"], t["k"], t["v"], t["decay"])
+        check_forward(api.linear_attention(*args, state=t["state"]), x, kind, dk ** -0.5)
+        check_grad(api.linear_attention_grad(*args, t["do"], dlast=t["dlast"], state=t["state"]), x, kind,
+                   dk ** -0.5)
+
+
+def test_no_steps():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, "bf16", 2, 0, 4, 2, 24, 33, 9)
+    o, last = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+    assert o.shape == (2, 0, 4, 33) and torch.equal(last, t["state"])
+    assert not api.linear_attention(t["q"], t["k"], t["v"], t["decay"])[1].any()
+    dq, dk, dv, ds = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"])
+    assert dq.shape == (2, 0, 4, 24) and dk.shape == (2, 0, 2, 24) and dv.shape == (2, 0, 2, 33)
+    assert torch.equal(ds, t["dlast"])
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("B,H,G,dk,dv", [(1, 1, 1, 1, 1), (64, 1, 1, 24, 24), (3, 4, 2, 128, 128), (2, 6, 2, 33, 50),
+                                         (1, 2, 1, 256, 256), (5, 2, 2, 7, 65), (2, 2, 1, 255, 4)])
+def test_step(kind, B, H, G, dk, dv):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, kind, B, 1, H, G, dk, dv, dk)
+    ref = lo.linear_attention(x["q"], x["k"], x["v"], x["decay"], x["state"], None, 0.5)
+    mag = lo.linear_attention(*(abs(x[n]) for n in "qkv"), x["decay"], abs(x["state"]), None, 0.5)
+    q, k, v = (t[n][:, 0] for n in "qkv")
+    state = t["state"].clone()
+    o, new = api.linear_attention_step(q, k, v, t["decay"], state, scale=0.5)
+    assert torch.equal(state, t["state"])
+    # the state: decay, product, sum; o: dk products summed
+    close(o, ref[0][:, 0], (dk + 5) * U * mag[0][:, 0], kind)
+    close(new, ref[1], 4 * U * mag[1])
+    o2, same = api.linear_attention_step(q, k, v, t["decay"], state, scale=0.5, out_state=state)
+    assert same is state and torch.equal(o, o2) and torch.equal(state, new)
+
+
+def test_steps_follow_the_sequence():
+    """A history read at once, then single steps, then the sequence that holds both."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, "fp32", 3, 90, 4, 2, 24, 24, 11)
+    cut = 70
+    _, s = api.linear_attention(*(t[n][:, :cut] for n in "qkv"), t["decay"], state=t["state"])
+    out = []
+    for i in range(cut, 90):
+        o, s = api.linear_attention_step(*(t[n][:, i] for n in "qkv"), t["decay"], s)
+        out.append(o)
+    ref = lo.linear_attention(x["q"], x["k"], x["v"], x["decay"], x["state"], None, 24 ** -0.5)
+    mag = lo.linear_attention(*(abs(x[n]) for n in "qkv"), x["decay"], abs(x["state"]), None, 24 ** -0.5)
+    c = attend_bound("fp32", 90, 24, 24) + 20 * 4 * U
+    close(torch.stack(out, 1), ref[0][:, cut:], c * mag[0][:, cut:])
+    close(s, ref[1], c * mag[1])
+
+
+def test_gradient_against_differences():
+    """The outputs are linear in q, in k and state, in v and state: <do, f(x + d) - f(x)> is <dx, d>."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, "fp32", 2, 300, 4, 2, 40, 24, 12, lengths=[300, 171])
+    kw = dict(lengths=t["lengths"], scale=0.2)
+    grads = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"],
+                                      state=t["state"], **kw)
+
+    def loss(q, k, v, s):
+        o, last = api.linear_attention(q, k, v, t["decay"], state=s, **kw)
+        a, b = t["do"].double() * o.double(), t["dlast"].double() * last.double()
+        return a.sum() + b.sum(), a.abs().sum() + b.abs().sum()
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    at = dict(q=t["q"], k=t["k"], v=t["v"], s=t["state"])
+    for name, grad in zip("qkvs", grads):
+        d = torch.randn(at[name].shape, generator=g, device="cuda")
+        hi, lo_ = dict(at), dict(at)
+        hi[name], lo_[name] = at[name] + d, at[name] - d
+        (a, ma), (b, mb) = loss(**hi), loss(**lo_)
+        want = (grad.double() * d.double()).sum()
+        # the inputs' sums round by u each, the kernels by attend_bound of the terms' magnitudes,
+        # which random signs make at most sqrt(dk T) ~ 100 times the terms seen here
+        assert abs((a - b) / 2 - want) <= 100 * attend_bound("fp32", 300, 40, 24) * (ma + mb)
+
+
+# ---- rotary --------------------------------------------------------------------
+
+def rotary_bound(xv, half, interleaved, amp, far=0.0):
+    """cos and sin to 8 u (the turn's rounding, 2 pi 2^-25, and the functions'), `far` on top,
+    two products and a sum."""
+    a = np.abs(xv)
+    b = np.zeros_like(a)
+    one, two = ((slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else
+                (slice(0, half), slice(half, 2 * half)))
+    b[..., one] = b[..., two] = (a[..., one] + a[..., two]) * (12 * U + far) * amp
+    return b
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("heads,width,half", [(1, 2, 1), (3, 24, 12), (2, 128, 64), (5, 80, 20), (2, 33, 16),
+                                              (1, 37, 3), (4, 96, 0), (20, 64, 30)])
+def test_rotary(kind, layout, heads, width, half):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(width + half)
+    for n in (1, 77):
+        x, xv = dev(torch, rng.standard_normal((n, heads, width)), kind)
+        pos = rng.integers(-1000, 1 << 20, size=n)
+        f = 10000.0 ** (-np.arange(half) / max(half, 1))
+        tf = torch.from_numpy(f).cuda()
+        for it in (torch.int32, torch.int64):
+            tp = torch.from_numpy(pos).to(it).cuda()
+            for inverse in (False, True):
+                got = api.rotary(x, tp, tf, layout=layout, amplitude=1.25, inverse=inverse)
+                ref = lo.rotary(xv, pos, f, layout == "interleaved", 1.25, inverse)
+                close(got, ref, rotary_bound(xv, half, layout == "interleaved", 1.25), kind)
+                if half * 2 < width:
+                    assert torch.equal(got[..., 2 * half:], x[..., 2 * half:])
+        mine = x.clone()
+        assert api.rotary(mine, tp, tf, layout=layout, out=mine) is mine  # in place
+        assert torch.equal(mine, api.rotary(x, tp, tf, layout=layout))
+        if kind == "fp32":  # turned there and back: twice the bound, on values at most sqrt 2 larger
+            back = api.rotary(mine, tp, tf, layout=layout, inverse=True)
+            close(back, xv, 4 * rotary_bound(xv, half, layout == "interleaved", 1.0))
+
+
+def test_rotary_strides_and_far_positions():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(3)
+    for kind in ("fp32", "bf16"):
+        B, T, width, half = 2, 9, 24, 12
+        wide, wv = dev(torch, rng.standard_normal((B, T, 1 + 5 * width)), kind)
+        f = 10000.0 ** (-np.arange(half) / half)
+        tf = torch.from_numpy(f).cuda()
+        x, xv = wide[:, :, 1:].unflatten(2, (5, width)), wv[:, :, 1:].reshape(B, T, 5, width)
+        # positions past 2^31 and 2^40, negative ones; one row for both batch rows
+        pos = np.array([0, 1, -5, 2 ** 20, 2 ** 31 - 1, 2 ** 31 + 7, 2 ** 33, -2 ** 33, 123456789])
+        tp = torch.from_numpy(pos).cuda().expand(B, T)
+        # 2^33 radians in float64: their turns round by 3 2^-53 relative, 2^33 3 2^-53 / (2 pi) 2 pi = 2.9e-6
+        bound = rotary_bound(xv, half, False, 1.0, far=3e-6)
+        ref = lo.rotary(xv, np.broadcast_to(pos, (B, T)), f)
+        close(api.rotary(x, tp, tf), ref, bound, kind)
+        out = torch.zeros_like(wide)  # into strides of its own
+        got = api.rotary(x, tp, tf, out=out[:, :, 1:].unflatten(2, (5, width)))
+        close(got, ref, bound, kind)
+        assert not out[:, :, 0].any()
+        xt = x.transpose(0, 1)  # steps first
+        close(api.rotary(xt, tp.t(), tf).transpose(0, 1), ref, bound, kind)
+        part = x[:, :, 1:4]  # some heads, in place: the others stay
+        mine = wide.clone()
+        api.rotary(mine[:, :, 1:].unflatten(2, (5, width))[:, :, 1:4], tp, tf,
+                   out=mine[:, :, 1:].unflatten(2, (5, width))[:, :, 1:4])
+        close(mine[:, :, 1:].unflatten(2, (5, width))[:, :, 1:4], ref[:, :, 1:4], bound[:, :, 1:4], kind)
+        assert torch.equal(mine[:, :, :1 + width], wide[:, :, :1 + width])
+        assert torch.equal(mine[:, :, 1 + 4 * width:], wide[:, :, 1 + 4 * width:]) and part.shape[2] == 3
+    for shape in ((0, 3, 24), (2, 0, 3, 24)):
+        e = api.rotary(torch.empty(shape, device="cuda"),
+                       torch.empty(shape[:-2], dtype=torch.int32, device="cuda"), tf)
+        assert e.shape == shape
+
+
+# ---- AdamW -----------------------------------------------------------------------
+
+HYPER = dict(lr=0.01, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.1)
+
+
+def adam_close(torch, got, x, kind, gs=1.0, step=3, hyper=HYPER):
+    """p, m, v (float32 tensors or decoded) against the definition: m and v three operations each,
+    the update about a dozen (root, quotient, product, the factors' own rounding)."""
+    g = x["g"] * gs
+    ref = lo.adamw(x["p"], g, x["m"], x["v"], step, **hyper)
+    mm = np.abs(hyper["beta1"] * x["m"]) + np.abs((1 - hyper["beta1"]) * g)
+    root = np.sqrt(ref[2] / (1 - hyper["beta2"] ** step)) + hyper["eps"]
+    upd = hyper["lr"] * mm / (1 - hyper["beta1"] ** step) / root
+    if "m" in got:
+        close(got["m"], ref[1], 4 * U * mm)
+        close(got["v"], ref[2], 6 * U * ref[2])
+    bound = 3 * U * np.abs(x["p"]) + 20 * U * upd
+    if "master" in got:
+        close(got["master"], ref[0], bound)
+    close(got["p"], ref[0], bound, kind)
+    return ref
+
+
+def adam_make(torch, shape, kind, gkind, seed):
+    rng = np.random.default_rng(seed)
+    t, x = {}, {}
+    t["p"], x["p"] = dev(torch, rng.standard_normal(shape), kind)
+    t["g"], x["g"] = dev(torch, rng.standard_normal(shape) * 10.0 ** rng.uniform(-3, 0, shape), gkind)
+    t["m"], x["m"] = dev(torch, rng.standard_normal(shape) * 0.1)
+    t["v"], x["v"] = dev(torch, rng.standard_normal(shape) ** 2 * 0.01)
+    return t, x
+
+
+@pytest.mark.parametrize("kind,gkind", [("fp32", "fp32"), ("bf16", "bf16"), ("fp16", "fp16"), ("fp32", "bf16"),
+                                        ("bf16", "fp32"), ("fp16", "fp32"), ("fp32", "fp16"), ("bf16", "fp16"),
+                                        ("fp16", "bf16")])
+@pytest.mark.parametrize("master", [False, True])
+def test_adamw_32(kind, gkind, master):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    shapes = [(1,), (7,), (8,), (2048,), (2049,), (33, 100), (5, 3, 411)]
+    made = [adam_make(torch, s, kind, gkind, i) for i, s in enumerate(shapes)]
+    ts, xs = [m[0] for m in made], [m[1] for m in made]
+    masters = None
+    if master:  # the masters hold what the params have rounded away
+        masters = []
+        for t, x in made:
+            mt, mv = dev(torch, x["p"] * (1 + 2.0 ** -12))
+            masters.append(mt)
+            x["p"] = mv
+    before = [t["g"].clone() for t in ts]
+    api.adamw_step([t["p"] for t in ts], [t["g"] for t in ts], [t["m"] for t in ts], [t["v"] for t in ts], 3,
+                   masters=masters, grad_scale=0.5, **HYPER)
+    for i, (t, x) in enumerate(zip(ts, xs)):
+        assert torch.equal(t["g"], before[i])
+        if master:
+            t["master"] = masters[i]
+        adam_close(torch, t, x, kind, gs=0.5)
+
+
+def decode(torch, code, scale):
+    n = code.numel()
+    return code.float().reshape(-1).double() * scale.double().repeat_interleave(256)[:n]
+
+
+@pytest.mark.parametrize("kind,gkind", [("fp32", "fp32"), ("bf16", "bf16"), ("fp16", "fp32")])
+@pytest.mark.parametrize("master", [False, True])
+def test_adamw_8(kind, gkind, master):
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    shapes = [(1,), (255,), (256,), (257,), (2048,), (4100,), (37, 111)]
+    made = [adam_make(torch, s, kind, gkind, 50 + i) for i, s in enumerate(shapes)]
+    params, grads = [t["p"] for t, _ in made], [t["g"] for t, _ in made]
+    masters = [t["p"].float().clone() for t, _ in made] if master else None
+    m, v, ms, vs = api.adamw_states(params, bits=8)
+    for step in (1, 2, 3):
+        olds = []
+        for i, (t, x) in enumerate(made):
+            olds.append(dict(p=(masters or params)[i].double().cpu().numpy(), g=x["g"],
+                             m=decode(torch, m[i], ms[i]).cpu().numpy().reshape(x["g"].shape),
+                             v=decode(torch, v[i], vs[i]).square().cpu().numpy().reshape(x["g"].shape)))
+        api.adamw_step(params, grads, m, v, step, masters=masters, m_scale=ms, v_scale=vs, **HYPER)
+        for i, x in enumerate(olds):
+            got = dict(p=params[i])
+            if master:
+                got["master"] = masters[i]
+            ref = adam_close(torch, got, x, kind, step=step)
+            for code, scale, want in ((m[i], ms[i], ref[1]), (v[i], vs[i], np.sqrt(ref[2]))):
+                want = want.reshape(-1)
+                top = np.array([np.abs(want[j:j + 256]).max() for j in range(0, want.size, 256)])
+                close(scale, top / 448, 8 * U * top / 448)
+                each = np.repeat(scale.double().cpu().numpy(), 256)[:want.size]
+                have = decode(torch, code, scale).cpu().numpy()
+                # half a step of 4 significant bits, half a step (2^-9) below the normal range; a root
+                # above zero that would be zero is one step: 2^-9
+                assert (np.abs(have - want) <= np.abs(want) * (2.0 ** -4 + 2.0 ** -20) + each * 2.0 ** -9).all()
+                if code is v[i]:
+                    assert ((have > 0) == (want > 0)).all()
+                assert not np.isnan(have).any()
+
+
+def test_adamw_8_extremes():
+    """Zeros, blocks of tiny and huge values, and what is not finite."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    n = 256 * 5
+    p = torch.zeros(n, device="cuda")
+    g = torch.zeros(n, device="cuda")
+    g[256:512] = 1e-30                      # roots near 1e-31, moments near 1e-31
+    g[512:768] = 1e15
+    g[768:1024] = torch.logspace(-18, 0, 256, device="cuda")   # more than the codes span
+    g[1024] = float("nan")
+    g[1030] = float("inf")
+    g[1031:] = 1.0
+    m, v, ms, vs = api.adamw_states([p], bits=8)
+    api.adamw_step([p], [g], m, v, 1, m_scale=ms, v_scale=vs, **HYPER)
+    md, vd = decode(torch, m[0], ms[0]), decode(torch, v[0], vs[0])
+    assert not md[:256].any() and not vd[:256].any() and not p[:256].any()
+    assert torch.isfinite(ms[0]).all() and torch.isfinite(vs[0]).all()
+    assert (vd[512:768] > 0).all() and (vd[768:1024] > 0).all()
+    assert torch.isfinite(p[256:1024]).all()
+    for x in (md, vd):
+        assert torch.isnan(x[1024]) and torch.isnan(x[1030])
+        assert torch.isfinite(x[1025:1030]).all() and torch.isfinite(x[1031:]).all()
+    assert abs(md[1100].item() - 0.1) <= 0.1 * 2.0 ** -4 and abs(vd[1100].item() - 0.1) <= 0.1 * 2.0 ** -4
+    # a second step without gradients moves nothing by more than the first could
+    before = p.clone()
+    api.adamw_step([p], [torch.zeros_like(g)], m, v, 2, m_scale=ms, v_scale=vs, **HYPER)
+    assert ((p - before)[256:1024].abs() <= 20 * HYPER["lr"]).all()
+
+
+def test_adamw_many_tensors_and_device_numbers():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    rng = np.random.default_rng(2)
+    made = [adam_make(torch, (int(n),), "fp32" if i % 3 else "bf16", "fp32" if i % 2 else "bf16", i)
+            for i, n in enumerate(rng.integers(0, 3000, size=131))]
+    cols = [[t[k] for t, _ in made] for k in "pgmv"]
+    cols[1][5] = None  # no gradient: left alone
+    keep = [made[5][0][k].clone() for k in "pmv"]
+    step = torch.tensor(3, dtype=torch.int64, device="cuda")
+    lr, gs = torch.tensor([0.01], device="cuda"), torch.tensor(0.5, device="cuda")
+    hyper = {k: v for k, v in HYPER.items() if k != "lr"}
+    api.adamw_step(*cols, step, lr=lr, grad_scale=gs, **hyper)
+    for i, (t, x) in enumerate(made):
+        if i == 5:
+            assert all(torch.equal(a, t[k]) for a, k in zip(keep, "pmv"))
+            continue
+        # (the rate arrives as float32: u more on every update, decay's product u more)
+        adam_close(torch, t, x, "fp32" if i % 3 else "bf16", gs=0.5)
+    api.adamw_step([], [], [], [], 1)
+
+
+# ---- streams, graphs, devices, refusals -------------------------------------------
+
+def test_on_another_stream():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, "bf16", 1, 2000, 2, 2, 64, 64, 21)
+    tf = torch.from_numpy(10000.0 ** (-np.arange(32) / 32)).cuda()
+    pos = torch.arange(2000, device="cuda").expand(1, -1)
+    want = api.linear_attention(api.rotary(t["q"], pos, tf), t["k"], t["v"], t["decay"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = api.linear_attention(api.rotary(t["q"], pos, tf), t["k"], t["v"], t["decay"])
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_captured_step():
+    """A training step of the layers as one graph, replayed between eager work; the optimizer's
+    step, rate and scale change from replay to replay."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, "fp32", 2, 700, 4, 2, 32, 24, 22, lengths=[700, 333])
+    tf = torch.from_numpy(10000.0 ** (-np.arange(16) / 16)).cuda()
+    pos = torch.arange(700, device="cuda").expand(2, -1)
+    live = {n: t[n].clone() for n in "qkv"}
+    states = {bits: api.adamw_states([live[n] for n in "qkv"], bits) for bits in (32, 8)}
+    step = torch.ones((), dtype=torch.int64, device="cuda")
+    lr = torch.full((), 0.01, device="cuda")
+
+    def run(p, states):
+        q = api.rotary(p["q"], pos, tf)
+        o, last = api.linear_attention(q, p["k"], p["v"], t["decay"], lengths=t["lengths"])
+        dq, dk, dv, _ = api.linear_attention_grad(q, p["k"], p["v"], t["decay"], o, dlast=last,
+                                                  lengths=t["lengths"])
+        g = [api.rotary(dq, pos, tf, inverse=True), dk, dv]
+        for bits in (32, 8):
+            m, v, ms, vs = states[bits]
+            api.adamw_step([p[n] for n in "qkv"], g, m, v, step, lr=lr, m_scale=ms, v_scale=vs)
+        return o, last
+
+    def copies(p, states):
+        return ({n: a.clone() for n, a in p.items()},
+                {b: tuple(None if l is None else [a.clone() for a in l] for l in s) for b, s in states.items()})
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run(*copies(live, states))
+    torch.cuda.current_stream().wait_stream(side)
+    eager, eager_states = copies(live, states)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(live, states)
+    for i in range(4):
+        step.fill_(i + 1)
+        lr.fill_(0.01 / (i + 1))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(eager, eager_states)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert all(torch.equal(live[n], eager[n]) for n in "qkv")
+        for b in (32, 8):
+            for mine, theirs in zip(states[b], eager_states[b]):
+                for p, q in zip(mine or [], theirs or []):
+                    assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
+def test_offsets_past_32_bits():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    far = (1 << 32) + 40  # elements between two batch rows of one buffer
+    buf = torch.zeros(far + 200 * 2 * 16, dtype=torch.bfloat16, device="cuda")
+    t, x = make(torch, "bf16", 2, 200, 2, 2, 16, 16, 30)
+
+    def spread(a):
+        v = torch.as_strided(buf, a.shape, (far, 2 * 16, 16, 1))
+        v.copy_(a)
+        return v
+
+    want = api.linear_attention(t["q"], t["k"], t["v"], t["decay"])
+    got = api.linear_attention(spread(t["q"]), t["k"], t["v"], t["decay"])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    tf = torch.ones(8, dtype=torch.float64, device="cuda")
+    pos = torch.arange(200, device="cuda").expand(2, -1)
+    want = api.rotary(t["q"], pos, tf)
+    assert torch.equal(api.rotary(spread(t["q"]), pos, tf), want)
+    mine = spread(t["q"])
+    assert torch.equal(api.rotary(mine, pos, tf, out=mine), want)
+    del buf, mine
+    n = (1 << 31) + 5  # one tensor of more than 2^31 elements
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[-3:] = 1.0
+    m, v, ms, vs = api.adamw_states([p], bits=8)
+    api.adamw_step([p], [g], m, v, 1, m_scale=ms, v_scale=vs, lr=0.5, weight_decay=0.0)
+    assert p[-3:].tolist() == [-0.5] * 3 and not p[:-3].any()
+    assert abs(ms[0][-1].item() * 448 - 0.1) < 1e-6
+
+
+def test_binding_refusals():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, _ = make(torch, "fp32", 2, 5, 4, 2, 8, 6, 1)
+    q, k, v, a, do = t["q"], t["k"], t["v"], t["decay"], t["do"]
+    z = lambda *s, **kw: torch.zeros(*s, device="cuda", **kw)  # noqa: E731
+    for args in ((q[0], k, v, a), (q, k[0], v, a), (q, k[:1], v, a), (q, k[..., :4], v, a), (q, k, v[:, :4], a),
+                 (q, k, v[:, :, :1], a), (q.bfloat16(), k, v, a), (q, k, v, a[:3]), (q, k, v, a.double()),
+                 (q, k, v, a.cpu()), (q[:, :, :3], k, v, a[:3]), (q, k, v, z(8)[::2]),
+                 (q.transpose(2, 3), k, v, a), (z(2, 5, 4, 257), z(2, 5, 2, 257), v, a), (q[:0], k[:0], v[:0], a),
+                 (z(2, 5, 4, 16)[..., ::2], k, v, a)):
+        with pytest.raises(ValueError):
+            api.linear_attention(*args)
+        with pytest.raises(ValueError):
+            api.linear_attention_grad(*args, do)
+    for kw in (dict(state=z(2, 4, 8, 5)), dict(state=z(2, 4, 8, 6).double()), dict(state=z(2, 4, 6, 8).transpose(2, 3)),
+               dict(lengths=z(3, dtype=torch.int32)), dict(lengths=z(2)), dict(scale=float("nan"))):
+        with pytest.raises(ValueError):
+            api.linear_attention(q, k, v, a, **kw)
+        with pytest.raises(ValueError):
+            api.linear_attention_grad(q, k, v, a, do, **kw)
+    for d in (do[:, :4], do.bfloat16(), do[0], None):
+        with pytest.raises(ValueError):
+            api.linear_attention_grad(q, k, v, a, d)
+    with pytest.raises(ValueError):
+        api.linear_attention_grad(q, k, v, a, do, dlast=z(1, 4, 8, 6))
+    s = z(2, 4, 8, 6)
+    for args in ((q, k, v, a, s), (q[:, 0], k[:, 0], v[:, 0], a, None), (q[:, 0], k[:, 0], v[:, 0], a, s[:1]),
+                 (q[:, 0], k, v, a, s)):
+        with pytest.raises(ValueError):
+            api.linear_attention_step(*args)
+    with pytest.raises(ValueError):
+        api.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], a, s, out_state=s.bfloat16())
+    pos, f = z(2, 5, dtype=torch.int32), z(4, dtype=torch.float64)
+    for args, kw in (((q[0, 0], pos, f), {}), ((q, pos[:, :4], f), {}), ((q, pos.float(), f), {}),
+                     ((q, pos, f.float()), {}), ((q, pos, z(5, dtype=torch.float64)), {}),
+                     ((q, pos, z(8, dtype=torch.float64)[::2]), {}), ((q, pos, f), dict(layout="other")),
+                     ((q, pos, f), dict(amplitude=float("inf"))), ((q, pos, f), dict(out=z(2, 5, 4, 7))),
+                     ((q, pos, f), dict(out=q.bfloat16())), ((q, pos, f), dict(out=q[:1, :1].expand_as(q))),
+                     ((q[:, :, :, ::2], pos, f[:2]), {})):
+        with pytest.raises(ValueError):
+            api.rotary(*args, **kw)
+    p, g = z(300), z(300)
+    m, v_, ms, vs = api.adamw_states([p], bits=8)
+    m32, v32, _, _ = api.adamw_states([p])
+    with pytest.raises(ValueError):
+        api.adamw_states([p], bits=16)
+    for args, kw in ((([p], [], m32, v32, 1), {}), (([p], [g[:9]], m32, v32, 1), {}), (([p], [g.double()], m32, v32, 1), {}),
+                     (([p], [g], m, v_, 1), {}), (([p], [g], m, v_, 1), dict(m_scale=ms)),
+                     (([p], [g], m, v_, 1), dict(m_scale=ms, v_scale=[z(1)])),
+                     (([p], [g], m32, v32, 1), dict(m_scale=ms, v_scale=vs)),
+                     (([p], [g], m32, m32, 1), {}), (([p, p], [g, g], m32 * 2, v32 * 2, 1), {}),
+                     (([p], [g], m32, v32, 1), dict(masters=[p])), (([p], [g], m32, v32, 1), dict(masters=[z(299)])),
+                     (([p[::2]], [g[::2]], [m32[0][:150]], [v32[0][:150]], 1), {}),
+                     (([p], [g], m32, v32, torch.ones(1, device="cuda")), {}),
+                     (([p], [g], m32, v32, 1), dict(lr=z(2)))):
+        with pytest.raises(ValueError):
+            api.adamw_step(*args, **kw)
+    from symmetric_nmf_clustering_amd import _lib as L
+    for kw in (dict(step=0), dict(lr=float("nan")), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1.0)):
+        with pytest.raises(L.SymNMFError):
+            api.adamw_step([p], [g], m32, v32, **{**dict(step=1), **kw})
