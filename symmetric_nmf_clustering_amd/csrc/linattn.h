@@ -159,40 +159,73 @@ struct Rows {
     int d;            // columns
 };
 
+// v's elements moved down by k (0 to V), zeros behind them.
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> moved_down(const Vec<T, V>& v, int k) {
+    constexpr int E = 8 * sizeof(T);
+    uint64_t w[2];
+    __builtin_memcpy(w, &v, 16);
+    const int s = k * E;
+    const uint64_t lo = s >= 64 ? (s >= 128 ? 0 : w[1] >> (s - 64))
+                                : (s ? (w[0] >> s) | (w[1] << (64 - s)) : w[0]);
+    const uint64_t hi = s >= 64 ? 0 : w[1] >> s;
+    w[0] = lo;
+    w[1] = hi;
+    Vec<T, V> r;
+    __builtin_memcpy(&r, w, 16);
+    return r;
+}
+
 // A chunk's C x COLS tile on its way from memory through registers to LDS, by NT
-// threads. Rows past `rows` and columns past d are zeros.
+// threads. Rows past n (at least 1) and columns past d are zeros. No access is
+// behind a lane's branch, so that all of them are in flight together: rows past n
+// read the last one, a row's last columns are read as the 16 bytes that end it, and
+// store() puts that right. (A branch around each costs a wait for each: 4 times the
+// time of the whole walk.)
 template <class T, class LT, int C, int COLS, int NT>
 struct Tile {
     static constexpr int V = 16 / sizeof(T), G = COLS / V, N = (C * G + NT - 1) / NT;
     static constexpr int STRIDE = COLS + 16 / (int)sizeof(LT);
     Vec<T, V> r[N];
 
-    __device__ __forceinline__ void load(const Rows<T>& m, int64_t u0, int rows, int c0) {
+    __device__ __forceinline__ void load(const Rows<T>& m, int64_t u0, int n, int c0) {
+        const T* p = m.p + u0 * m.stride;
+        if (m.d >= V) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = threadIdx.x + i * NT, row = at / G, c = c0 + at % G * V;
-            r[i] = Vec<T, V>{};
-            if (row >= rows || c >= m.d) continue;  // rows <= C
-            const T* p = m.p + (u0 + row) * m.stride + c;
-            if (c + V <= m.d) {
-                r[i] = load_vec<T, V>(p);
-            } else {
+            for (int i = 0; i < N; ++i) {
+                const int at = threadIdx.x + i * NT, row = min(at / G, n - 1);
+                r[i] = load_vec<T, V>(p + row * m.stride + min(c0 + at % G * V, m.d - V));
+            }
+        } else {  // rows of less than 16 bytes
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (c + j < m.d) r[i].e[j] = p[j];
+            for (int i = 0; i < N; ++i) {
+                const int at = threadIdx.x + i * NT, row = min(at / G, n - 1);
+#pragma unroll
+                for (int j = 0; j < V; ++j) r[i].e[j] = p[row * m.stride + min(j, m.d - 1)];
             }
         }
     }
-    __device__ __forceinline__ void store(LT* t) const {
+    __device__ __forceinline__ void store(LT* t, int d, int n, int c0) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = threadIdx.x + i * NT, row = at / G, c = at % G * V;
             if (C * G % NT && row >= C) continue;
+            Vec<T, V> v = r[i];
+            if (d % V) {
+                if (d < V) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (c0 + c + j >= d) v.e[j] = T{};
+                } else {
+                    v = moved_down(v, max(0, min(c0 + c - (d - V), V)));
+                }
+            }
+            if (row >= n || c0 + c >= d) v = Vec<T, V>{};
             if constexpr (sizeof(T) == sizeof(LT)) {
-                *reinterpret_cast<u32x4*>(t + row * STRIDE + c) = __builtin_bit_cast(u32x4, r[i]);
+                *reinterpret_cast<u32x4*>(t + row * STRIDE + c) = __builtin_bit_cast(u32x4, v);
             } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) t[row * STRIDE + c + j] = to_f32(r[i].e[j]);
+                for (int j = 0; j < V; ++j) t[row * STRIDE + c + j] = to_f32(v.e[j]);
             }
         }
     }
@@ -221,7 +254,7 @@ __device__ __forceinline__ double ln_decay(const float* decay, int head) {
 
 // blockIdx.x (+ first): column tile, segment and head; blockIdx.y: the run.
 template <class T, int DX, int NW, bool OUT>
-__global__ __launch_bounds__(64 * NW) void attend_walk_kernel(AttendArgs a, int64_t first,
+__global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(AttendArgs a, int64_t first,
                                                               int64_t items, int ztiles) {
     using Z = WalkSizes<T, DX, NW, OUT>;
     using LT = typename Z::LT;
@@ -302,6 +335,7 @@ __global__ __launch_bounds__(64 * NW) void attend_walk_kernel(AttendArgs a, int6
     };
     auto fetch = [&](int64_t u0) {
         const int n = valid(u0);
+        if (n == 0) return;
         if (OUT) rx.load(mx, u0, n, 0);
         ry.load(my, u0, n, 0);
         rz.load(mz, u0, n, z0);
@@ -311,9 +345,9 @@ __global__ __launch_bounds__(64 * NW) void attend_walk_kernel(AttendArgs a, int6
         const int n = valid(u0);
         if (n == 0) break;
         lds_barrier();  // the tiles of the last chunk are read
-        if (OUT) rx.store(lds.x);
-        ry.store(lds.y);
-        rz.store(lds.z);
+        if (OUT) rx.store(lds.x, R.dx, n, 0);
+        ry.store(lds.y, R.dx, n, 0);
+        rz.store(lds.z, R.dz, n, z0);
         lds_barrier();
         if (u0 + C < u_end) fetch(u0 + C);
 
