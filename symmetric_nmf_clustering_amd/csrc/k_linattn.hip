@@ -17,7 +17,8 @@ constexpr int kWant = 512;      // workgroups
 constexpr int64_t kLeast = 256;  // steps a segment has at least
 
 int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
-    const int ztiles = ((d.dk > d.dv ? d.dk : d.dv) + 63) / 64;
+    const int wide = d.dk > d.dv ? d.dk : d.dv, cols = wide > 64 && wide <= 128 ? 128 : 64;
+    const int ztiles = (wide + cols - 1) / cols;
     const int64_t items = d.batch * d.heads * ztiles * runs;
     int64_t n = (kWant + items - 1) / items;
     const int64_t most = d.steps / kLeast;

@@ -25,9 +25,9 @@ struct AttendRun {
     int32_t reverse, in_pow;
     float p_scale, in_scale, st_scale;
     const float* s0;      // nullable (zeros): batch x heads x (dx dz), element (i, j) at
-    int64_t s0_i, s0_j;   // i s0_i + j s0_j
+    int32_t s0_i, s0_j;   // i s0_i + j s0_j
     float* s1;            // nullable: the state after the last step
-    int64_t s1_i, s1_j;
+    int32_t s1_i, s1_j;
     void* out;            // batch x steps x heads x dz, dense
     int32_t out32;        // out is float32 whatever the type
     float* seg;           // nseg > 1: batch x heads x nseg x dx x dz

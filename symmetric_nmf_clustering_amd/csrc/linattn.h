@@ -20,6 +20,8 @@
 // fp32: 16x16x4 float32 products. fp16: widened to float32 as it is loaded.
 #pragma once
 
+#include <type_traits>
+
 #include "bf16split.h"
 #include "layers.h"
 
@@ -151,98 +153,80 @@ struct Op<float> {
     }
 };
 
-// The rows of one operand of a head.
+// The rows of one operand of a head, in the order of the walk.
 template <class T>
 struct Rows {
-    const T* p;       // of the batch row and head
-    int64_t stride;   // of a step, negative in reverse
-    int d;            // columns
+    const T* p;       // the first step's row
+    int64_t stride;   // of a step, not negative
+    int32_t reverse;
+    int32_t d;        // columns
 };
-
-// v's elements moved down by k (0 to V), zeros behind them.
-template <class T, int V>
-__device__ __forceinline__ Vec<T, V> moved_down(const Vec<T, V>& v, int k) {
-    constexpr int E = 8 * sizeof(T);
-    uint64_t w[2];
-    __builtin_memcpy(w, &v, 16);
-    const int s = k * E;
-    const uint64_t lo = s >= 64 ? (s >= 128 ? 0 : w[1] >> (s - 64))
-                                : (s ? (w[0] >> s) | (w[1] << (64 - s)) : w[0]);
-    const uint64_t hi = s >= 64 ? 0 : w[1] >> s;
-    w[0] = lo;
-    w[1] = hi;
-    Vec<T, V> r;
-    __builtin_memcpy(&r, w, 16);
-    return r;
-}
+// WIDE tiles count a chunk's elements from its lowest row in 32 bits.
+constexpr int64_t kNearStride = int64_t(1) << 24;
 
 // A chunk's C x COLS tile on its way from memory through registers to LDS, by NT
 // threads. Rows past n (at least 1) and columns past d are zeros. No access is
-// behind a lane's branch, so that all of them are in flight together: rows past n
-// read the last one, a row's last columns are read as the 16 bytes that end it, and
-// store() puts that right. (A branch around each costs a wait for each: 4 times the
-// time of the whole walk.)
-template <class T, class LT, int C, int COLS, int NT>
+// behind a lane's branch, so that all of them are in flight together: those past the
+// rows or columns read the last one, and store() clears them. (A branch around each
+// costs a wait for each: 2.4 times the time of the whole walk.) WIDE: 16 bytes a
+// lane, for d a multiple of that; otherwise one element a lane, neighbours together.
+template <class T, class LT, int C, int COLS, int NT, bool WIDE>
 struct Tile {
-    static constexpr int V = 16 / sizeof(T), G = COLS / V, N = (C * G + NT - 1) / NT;
+    static constexpr int V = WIDE ? 16 / sizeof(T) : 1, G = COLS / V, N = (C * G + NT - 1) / NT;
     static constexpr int STRIDE = COLS + 16 / (int)sizeof(LT);
     Vec<T, V> r[N];
 
     __device__ __forceinline__ void load(const Rows<T>& m, int64_t u0, int n, int c0) {
-        const T* p = m.p + u0 * m.stride;
-        if (m.d >= V) {
+        const T* low = m.p + (m.reverse ? -(u0 + n - 1) : u0) * m.stride;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = threadIdx.x + i * NT, row = min(at / G, n - 1);
-                r[i] = load_vec<T, V>(p + row * m.stride + min(c0 + at % G * V, m.d - V));
-            }
-        } else {  // rows of less than 16 bytes
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int at = threadIdx.x + i * NT, row = min(at / G, n - 1);
-#pragma unroll
-                for (int j = 0; j < V; ++j) r[i].e[j] = p[row * m.stride + min(j, m.d - 1)];
-            }
+        for (int i = 0; i < N; ++i) {
+            const int at = threadIdx.x + i * NT, c = min(c0 + at % G * V, m.d - V);
+            int row = min(at / G, n - 1);
+            if (m.reverse) row = n - 1 - row;
+            if constexpr (WIDE)
+                r[i] = load_vec<T, V>(low + (uint32_t)(__mul24(row, (int)m.stride) + c));
+            else
+                r[i] = load_vec<T, V>(low + row * m.stride + c);
         }
     }
-    __device__ __forceinline__ void store(LT* t, int d, int n, int c0) {
+    // n: rows that count (C: all); d: columns that count, from c0 on
+    template <bool FULL>
+    __device__ __forceinline__ void store(LT* t, int d, int n, int c0) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = threadIdx.x + i * NT, row = at / G, c = at % G * V;
             if (C * G % NT && row >= C) continue;
-            Vec<T, V> v = r[i];
-            if (d % V) {
-                if (d < V) {
+            const bool in = c0 + c < d && (FULL || row < n);
+            if constexpr (sizeof(T) == sizeof(LT) && WIDE) {
+                u32x4 v = __builtin_bit_cast(u32x4, r[i]);
 #pragma unroll
-                    for (int j = 0; j < V; ++j)
-                        if (c0 + c + j >= d) v.e[j] = T{};
-                } else {
-                    v = moved_down(v, max(0, min(c0 + c - (d - V), V)));
-                }
-            }
-            if (row >= n || c0 + c >= d) v = Vec<T, V>{};
-            if constexpr (sizeof(T) == sizeof(LT)) {
-                *reinterpret_cast<u32x4*>(t + row * STRIDE + c) = __builtin_bit_cast(u32x4, v);
+                for (int j = 0; j < 4; ++j) v[j] = in ? v[j] : 0u;
+                *reinterpret_cast<u32x4*>(t + row * STRIDE + c) = v;
+            } else if constexpr (sizeof(T) == sizeof(LT)) {
+                t[row * STRIDE + c] = in ? r[i].e[0] : LT{};
             } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) t[row * STRIDE + c + j] = to_f32(v.e[j]);
+                for (int j = 0; j < V; ++j) t[row * STRIDE + c + j] = in ? to_f32(r[i].e[j]) : 0.f;
             }
         }
     }
 };
 
-template <class T, int DX, int NW, bool OUT>
+template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
     using LT = typename InLds<T>::type;
     static constexpr int C = sizeof(LT) == 2 ? 64 : 32;
-    static constexpr int NT = 64 * NW, ZC = 16 * NW;
-    using TX = Tile<T, LT, C, DX, NT>;
-    using TZ = Tile<T, LT, C, ZC, NT>;
+    static constexpr int NT = 64 * NW, ZC = 16 * WN * NW;
+    using TX = Tile<T, LT, C, DX, NT, WIDE>;
+    using TZ = Tile<T, LT, C, ZC, NT, WIDE>;
     struct Lds {
         LT x[OUT ? C * TX::STRIDE : 8];
         LT y[C * TX::STRIDE];
         LT z[C * TZ::STRIDE];
         LT p[OUT ? C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
+        float wz[C];            // st_scale a^(C - in_pow - w): the weights of a whole chunk
+        float wx[OUT ? C : 4];  // in_scale a^(u + in_pow)
+        float wp[OUT ? C * 16 : 4];  // p_scale a^(u - w), as a lane holds a block, by bu - bw
         float pw[C + 1];        // a^0 ... a^C
     };
 };
@@ -252,11 +236,25 @@ __device__ __forceinline__ double ln_decay(const float* decay, int head) {
     return g < -200.0 ? -200.0 : g;  // exp(-200) is 0 in float32, and a^0 stays 1
 }
 
+// Four neighbouring columns of one step's result, of which `cols` are there (WIDE: all or
+// none).
+template <bool WIDE, class O>
+__device__ __forceinline__ void put_out(O* p, const floatx4& v, int cols) {
+    if (cols >= 4) {
+        store_vec<O, 4>(p, {{from_f32<O>(v[0]), from_f32<O>(v[1]), from_f32<O>(v[2]),
+                             from_f32<O>(v[3])}});
+    } else if (!WIDE) {
+#pragma unroll
+        for (int r = 0; r < 3; ++r)
+            if (r < cols) p[r] = from_f32<O>(v[r]);
+    }
+}
+
 // blockIdx.x (+ first): column tile, segment and head; blockIdx.y: the run.
-template <class T, int DX, int NW, bool OUT>
-__global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(AttendArgs a, int64_t first,
-                                                              int64_t items, int ztiles) {
-    using Z = WalkSizes<T, DX, NW, OUT>;
+template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
+__global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
+    AttendArgs a, int64_t first, int64_t items, int ztiles) {
+    using Z = WalkSizes<T, DX, NW, WN, OUT, WIDE>;
     using LT = typename Z::LT;
     using O = Op<LT>;
     constexpr int C = Z::C, NX = DX / 16, NB = C / 16, XS = Z::TX::STRIDE, ZS = Z::TZ::STRIDE;
@@ -269,13 +267,13 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     const int zt = (int)(grp % ztiles);
     const int64_t item = (grp / ztiles) + (id & 7) * ((items + 7) >> 3);
     if (grp / ztiles >= ((items + 7) >> 3) || item >= items) return;
-    const AttendRun& R = a.run[blockIdx.y];
+    const AttendRun R = a.run[blockIdx.y];
     const int seg = (int)(item % a.nseg);
     const int64_t bh = item / a.nseg;
     const int64_t b = bh / a.heads;
     const int head = (int)(bh % a.heads);
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
-    const int z0 = zt * Z::ZC, zw = z0 + wave * 16;
+    const int z0 = zt * Z::ZC, zw = z0 + wave * 16 * WN;
     if (z0 >= R.dz) return;  // the whole workgroup
 
     int64_t len = a.steps;
@@ -286,28 +284,31 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     const int64_t u_begin = seg * a.seg_len;
     int64_t u_end = u_begin + a.seg_len;
     if (u_end > a.steps) u_end = a.steps;
+    const int64_t u_stop = len < u_end ? len : u_end;  // of the segment's valid steps
     if (!OUT && (u_begin >= len || seg == a.nseg - 1)) return;  // the join does not read these
 
     const double gd = ln_decay(a.decay, head);
     for (int i = threadIdx.x; i <= C; i += Z::NT) lds.pw[i] = (float)exp(gd * i);
+    for (int i = threadIdx.x; i < C; i += Z::NT)
+        lds.wz[i] = R.st_scale * (float)exp(gd * (C - R.in_pow - i));
     if constexpr (OUT) {  // blocks above the diagonal that a 32-deep step reads
         for (int i = threadIdx.x; i < C * C; i += Z::NT) lds.p[i] = LT{};
     }
 
     const int64_t dir = R.reverse ? -1 : 1, from = R.reverse ? len - 1 : 0;
     auto rows_of = [&](const void* p, int64_t sb, int64_t st, int64_t sh, int grp_, int d) {
-        return Rows<T>{static_cast<const T*>(p) + b * sb + from * st + (head / grp_) * sh, dir * st,
-                       d};
+        return Rows<T>{static_cast<const T*>(p) + b * sb + from * st + (head / grp_) * sh, st,
+                       R.reverse, d};
     };
     const Rows<T> mx = rows_of(R.x, R.xb, R.xt, R.xh, R.xg, R.dx);
     const Rows<T> my = rows_of(R.y, R.yb, R.yt, R.yh, R.yg, R.dx);
     const Rows<T> mz = rows_of(R.z, R.zb, R.zt, R.zh, R.zg, R.dz);
 
     // the state at the segment's start
-    floatx4 S[NX];
+    floatx4 S[NX][WN];
     {
         const float* s = nullptr;
-        int64_t si = 0, sj = 0;
+        int si = 0, sj = 0;
         if (OUT && a.nseg > 1) {
             s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
             si = R.dz;
@@ -317,45 +318,49 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             si = R.s0_i;
             sj = R.s0_j;
         }
-        const int j = zw + l16;
 #pragma unroll
         for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * i + 4 * g + r;
-                S[i][r] = s && row < R.dx && j < R.dz ? s[row * si + j * sj] : 0.f;
-            }
+            for (int m = 0; m < WN; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * i + 4 * g + r, j = zw + 16 * m + l16;
+                    S[i][m][r] = s && row < R.dx && j < R.dz ? s[(uint32_t)(row * si + j * sj)] : 0.f;
+                }
+    }
+
+    if constexpr (OUT) {
+        for (int i = threadIdx.x; i < C; i += Z::NT)
+            lds.wx[i] = R.in_scale * (float)exp(gd * (i + R.in_pow));
+        for (int i = threadIdx.x; i < C * 16; i += Z::NT) {
+            const int gap = 16 * (i >> 8) + (i >> 2 & 15) - (4 * (i >> 6 & 3) + (i & 3));
+            lds.wp[i] = gap >= 0 ? R.p_scale * (float)exp(gd * gap) : 0.f;
+        }
     }
 
     typename Z::TX rx, ry;
     typename Z::TZ rz;
-    auto valid = [&](int64_t u0) {  // steps of the chunk at u0
-        const int64_t n = (len < u_end ? len : u_end) - u0;
-        return (int)(n < 0 ? 0 : (n < C ? n : C));
-    };
     auto fetch = [&](int64_t u0) {
-        const int n = valid(u0);
-        if (n == 0) return;
+        const int n = (int)min(u_stop - u0, (int64_t)C);
         if (OUT) rx.load(mx, u0, n, 0);
         ry.load(my, u0, n, 0);
         rz.load(mz, u0, n, z0);
     };
-    if (u_begin < u_end) fetch(u_begin);
-    for (int64_t u0 = u_begin; u0 < u_end; u0 += C) {
-        const int n = valid(u0);
-        if (n == 0) break;
-        lds_barrier();  // the tiles of the last chunk are read
-        if (OUT) rx.store(lds.x, R.dx, n, 0);
-        ry.store(lds.y, R.dx, n, 0);
-        rz.store(lds.z, R.dz, n, z0);
+    // A chunk of n steps from u0; FULL: n = C.
+    auto chunk = [&](auto full, int64_t u0, int n) {
+        constexpr bool FULL = decltype(full)::value;
+        if (!WIDE) fetch(u0);  // (many registers: not kept through a chunk)
+        lds_barrier();         // the tiles of the last chunk are read
+        if (OUT) rx.template store<FULL>(lds.x, R.dx, n, 0);
+        ry.template store<FULL>(lds.y, R.dx, n, 0);
+        rz.template store<FULL>(lds.z, R.dz, n, z0);
         lds_barrier();
-        if (u0 + C < u_end) fetch(u0 + C);
 
         if constexpr (OUT) {
             // P^T in 16 x 16 blocks on and below the diagonal, shared out among the waves
-            constexpr int BLOCKS = NB * (NB + 1) / 2;
+            constexpr int BLOCKS = NB * (NB + 1) / 2, MINE = (BLOCKS + NW - 1) / NW;
 #pragma unroll
-            for (int q = 0; q < (BLOCKS + NW - 1) / NW; ++q) {
+            for (int q = 0; q < MINE; ++q) {
                 const int at = wave + q * NW;
                 if (at >= BLOCKS) break;
                 const int bu = (at >= 1) + (at >= 3) + (at >= 6), bw = at - bu * (bu + 1) / 2;
@@ -365,34 +370,42 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
 #pragma unroll
                 for (int k = 0; k < DX / 32; ++k)
                     acc = O::mma(O::rows(py + 32 * k, g), O::rows(px + 32 * k, g), acc);
+                const f32x4 wp = *reinterpret_cast<const f32x4*>(lds.wp + ((bu - bw) * 64 + lane) * 4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int u = 16 * bu + l16, w = 16 * bw + 4 * g + r;
-                    acc[r] = w <= u ? acc[r] * (R.p_scale * lds.pw[u - w < 0 ? 0 : u - w]) : 0.f;
-                }
+                for (int r = 0; r < 4; ++r) acc[r] = wp[r] != 0.f ? acc[r] * wp[r] : 0.f;
                 O::put4(lds.p + ((bu * NB + bw) * 64 + lane) * 4, acc);
             }
             lds_barrier();
         }
 
-        typename O::F zf[C / 32];
+        typename O::F zf[C / 32][WN];
 #pragma unroll
         for (int k = 0; k < C / 32; ++k)
-            zf[k] = O::column(lds.z + 32 * k * ZS + 16 * wave, ZS, lane);
+#pragma unroll
+            for (int m = 0; m < WN; ++m)
+                zf[k][m] = O::column(lds.z + 32 * k * ZS + 16 * (WN * wave + m), ZS, lane);
 
         if constexpr (OUT) {
-            typename O::F sf[DX / 32];
+            typename O::F sf[DX / 32][WN];
 #pragma unroll
-            for (int k = 0; k < DX / 32; ++k) sf[k] = O::of(S[2 * k], S[2 * k + 1]);
+            for (int k = 0; k < DX / 32; ++k)
+#pragma unroll
+                for (int m = 0; m < WN; ++m) sf[k][m] = O::of(S[2 * k][m], S[2 * k + 1][m]);
+            const int64_t e0 = ((b * a.steps + from + dir * (u0 + l16)) * a.heads + head) * R.dz + zw + 4 * g;
+            const int64_t es = dir * 16 * a.heads * R.dz;
 #pragma unroll
             for (int bu = 0; bu < NB; ++bu) {
-                floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-                const int u = 16 * bu + l16;
-                const LT* px = lds.x + u * XS;
+                floatx4 acc[WN] = {};
+                const LT* px = lds.x + (16 * bu + l16) * XS;
 #pragma unroll
-                for (int k = 0; k < DX / 32; ++k)
-                    acc = O::mma(sf[k], O::split(px + 32 * k, g), acc);
-                acc *= R.in_scale * lds.pw[u + R.in_pow];
+                for (int k = 0; k < DX / 32; ++k) {
+                    const auto xf = O::split(px + 32 * k, g);
+#pragma unroll
+                    for (int m = 0; m < WN; ++m) acc[m] = O::mma(sf[k][m], xf, acc[m]);
+                }
+                const float wx = lds.wx[16 * bu + l16];
+#pragma unroll
+                for (int m = 0; m < WN; ++m) acc[m] *= wx;
 #pragma unroll
                 for (int k = 0; k <= bu / 2; ++k) {
                     typename O::F pf;
@@ -404,55 +417,66 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                     } else {
                         pf = O::two(pp, pp + 256);
                     }
-                    acc = O::mma(zf[k], pf, acc);
+#pragma unroll
+                    for (int m = 0; m < WN; ++m) acc[m] = O::mma(zf[k][m], pf, acc[m]);
                 }
-                const int z = zw + 4 * g;
-                if (u < n && z < R.dz) {
-                    const int64_t t = from + dir * (u0 + u);
-                    const int64_t e = ((b * a.steps + t) * a.heads + head) * R.dz + z;
-                    const int cols = R.dz - z < 4 ? R.dz - z : 4;
+                if (FULL || 16 * bu + l16 < n) {
+                    const int64_t e = e0 + bu * es;
                     if (R.out32) {
-                        float* p = static_cast<float*>(R.out) + e;
-                        if (cols == 4) {
-                            store_vec<float, 4>(p, {{acc[0], acc[1], acc[2], acc[3]}});
-                        } else {
 #pragma unroll
-                            for (int r = 0; r < 3; ++r)
-                                if (r < cols) p[r] = acc[r];
-                        }
+                        for (int m = 0; m < WN; ++m)
+                            put_out<WIDE>(static_cast<float*>(R.out) + e + 16 * m, acc[m],
+                                          R.dz - zw - 16 * m - 4 * g);
                     } else {
-                        T* p = static_cast<T*>(R.out) + e;
-                        if (cols == 4) {
-                            store_vec<T, 4>(p, {{from_f32<T>(acc[0]), from_f32<T>(acc[1]),
-                                                 from_f32<T>(acc[2]), from_f32<T>(acc[3])}});
-                        } else {
 #pragma unroll
-                            for (int r = 0; r < 3; ++r)
-                                if (r < cols) p[r] = from_f32<T>(acc[r]);
-                        }
+                        for (int m = 0; m < WN; ++m)
+                            put_out<WIDE>(static_cast<T*>(R.out) + e + 16 * m, acc[m],
+                                          R.dz - zw - 16 * m - 4 * g);
                     }
                 }
             }
         }
 
+        if (WIDE && u0 + C < u_stop) fetch(u0 + C);  // (earlier, its registers are wanted above)
         // S <- a^n S + Y^T (w Z); rows of z past n are zeros
-        const float an = lds.pw[n];
+        const float an = FULL ? lds.pw[C] : lds.pw[n];
 #pragma unroll
-        for (int i = 0; i < NX; ++i) S[i] *= an;
+        for (int i = 0; i < NX; ++i)
+#pragma unroll
+            for (int m = 0; m < WN; ++m) S[i][m] *= an;
 #pragma unroll
         for (int k = 0; k < C / 32; ++k) {
             float w[8];
+            if constexpr (FULL) {
+                const f32x4 a0 = *reinterpret_cast<const f32x4*>(lds.wz + 32 * k + 4 * g);
+                const f32x4 a1 = *reinterpret_cast<const f32x4*>(lds.wz + 32 * k + 16 + 4 * g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int at = n - R.in_pow - (32 * k + 4 * g + (j & 3) + (j >> 2) * 16);
-                w[j] = R.st_scale * lds.pw[at < 0 ? 0 : at];
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = a0[j];
+                    w[4 + j] = a1[j];
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int at = n - R.in_pow - (32 * k + 4 * g + (j & 3) + (j >> 2) * 16);
+                    w[j] = R.st_scale * lds.pw[at < 0 ? 0 : at];
+                }
             }
-            const auto zw8 = O::weigh(zf[k], w);
+            decltype(O::weigh(zf[0][0], w)) zw8[WN];
 #pragma unroll
-            for (int i = 0; i < NX; ++i)
-                S[i] = O::mma(O::column(lds.y + 32 * k * XS + 16 * i, XS, lane), zw8, S[i]);
+            for (int m = 0; m < WN; ++m) zw8[m] = O::weigh(zf[k][m], w);
+#pragma unroll
+            for (int i = 0; i < NX; ++i) {
+                const auto yf = O::column(lds.y + 32 * k * XS + 16 * i, XS, lane);
+#pragma unroll
+                for (int m = 0; m < WN; ++m) S[i][m] = O::mma(yf, zw8[m], S[i][m]);
+            }
         }
-    }
+    };
+    if (WIDE && u_begin < u_stop) fetch(u_begin);
+    int64_t u0 = u_begin;
+    for (; u0 + C <= u_stop; u0 += C) chunk(std::true_type{}, u0, C);
+    if (u0 < u_stop) chunk(std::false_type{}, u0, (int)(u_stop - u0));
 
     // steps past the length
     if constexpr (OUT) {
@@ -470,7 +494,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     }
 
     float* s = nullptr;
-    int64_t si = R.dz, sj = 1;
+    int si = R.dz, sj = 1;
     if (!OUT) {
         s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
     } else if (seg == a.nseg - 1 && R.s1) {
@@ -479,31 +503,40 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
         sj = R.s1_j;
     }
     if (s) {
-        const int j = zw + l16;
 #pragma unroll
         for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 16 * i + 4 * g + r;
-                if (row < R.dx && j < R.dz) s[row * si + j * sj] = S[i][r];
-            }
+            for (int m = 0; m < WN; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 16 * i + 4 * g + r, j = zw + 16 * m + l16;
+                    if (row < R.dx && j < R.dz) s[(uint32_t)(row * si + j * sj)] = S[i][m][r];
+                }
     }
 }
 
-template <class T, int DX, int NW>
-hipError_t attend_walk_as(const AttendArgs& a, bool maps, hipStream_t st) {
-    constexpr int ZC = 16 * NW;
+template <class T, int DX, int NW, int WN, bool OUT>
+hipError_t attend_walk_as(const AttendArgs& a, hipStream_t st) {
+    constexpr int ZC = 16 * NW * WN, V = 16 / sizeof(T);
     int dz = 0;
-    for (int r = 0; r < a.nrun; ++r) dz = a.run[r].dz > dz ? a.run[r].dz : dz;
+    bool wide = true;
+    for (int r = 0; r < a.nrun; ++r) {
+        dz = a.run[r].dz > dz ? a.run[r].dz : dz;
+        const AttendRun& q = a.run[r];
+        wide = wide && q.dx % V == 0 && q.dz % V == 0 && q.xt < kNearStride && q.yt < kNearStride &&
+               q.zt < kNearStride;
+    }
     const int ztiles = (dz + ZC - 1) / ZC;
     const int64_t items = a.batch * a.heads * a.nseg;
     const int64_t blocks = (items + 7) / 8 * 8 * ztiles;
     return in_launches(blocks, [&](int64_t first, unsigned n) {
         const dim3 grid(n, (unsigned)a.nrun);
-        if (maps)
-            attend_walk_kernel<T, DX, NW, false><<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
+        if (wide)
+            attend_walk_kernel<T, DX, NW, WN, OUT, true>
+                <<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
         else
-            attend_walk_kernel<T, DX, NW, true><<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
+            attend_walk_kernel<T, DX, NW, WN, OUT, false>
+                <<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
     });
 }
 
@@ -514,13 +547,18 @@ hipError_t launch_attend_walk(const AttendArgs& a, bool maps, hipStream_t st) {
         dx = a.run[r].dx > dx ? a.run[r].dx : dx;
         dz = a.run[r].dz > dz ? a.run[r].dz : dz;
     }
-    // two waves where they hold all columns of z, four otherwise
-#define SYMNMF_WALK(DX) \
-    return dz <= 32 ? attend_walk_as<T, DX, 2>(a, maps, st) : attend_walk_as<T, DX, 4>(a, maps, st)
-    if (dx <= 32) SYMNMF_WALK(32);
-    if (dx <= 64) SYMNMF_WALK(64);
-    if (dx <= 128) SYMNMF_WALK(128);
-    SYMNMF_WALK(256);
+    // small heads: two waves hold all columns of z; wide ones: two column tiles a wave, which
+    // share what it reads of x and y
+#define SYMNMF_WALK(DX, NW, WN) \
+    return maps ? attend_walk_as<T, DX, NW, WN, false>(a, st) \
+                : attend_walk_as<T, DX, NW, WN, true>(a, st)
+    if (dx <= 32 && dz <= 32) SYMNMF_WALK(32, 2, 1);
+    if (dx <= 32) SYMNMF_WALK(32, 4, 1);
+    if (dx <= 64 && dz <= 32) SYMNMF_WALK(64, 2, 1);
+    if (dx <= 64) SYMNMF_WALK(64, 4, 1);
+    if (dx <= 128 && dz <= 64) SYMNMF_WALK(128, 4, 1);
+    if (dx <= 128) SYMNMF_WALK(128, 4, 2);
+    SYMNMF_WALK(256, 4, 1);
 #undef SYMNMF_WALK
 }
 
