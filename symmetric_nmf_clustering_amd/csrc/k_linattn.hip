@@ -33,13 +33,14 @@ int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
 }
 
 // Slot i of a head's segments holds the state that segment i makes from nothing, and
-// receives the state it starts from: X_0 = s0, X_{i+1} = a^n_i X_i + L_i.
+// receives the state it starts from: X_0 = s0, X_{i+1} = a^n_i X_i + L_i. A thread
+// takes V neighbouring elements; eight segments' are asked for together.
+template <int V>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int64_t first,
                                                           int tiles) {
     const AttendRun& R = a.run[blockIdx.y];
     const int64_t id = first + blockIdx.x, bh = id / tiles, b = bh / a.heads;
-    const int64_t D = (int64_t)R.dx * R.dz;
-    const int64_t e = (id % tiles) * 256 + threadIdx.x;
+    const int D = R.dx * R.dz, e = ((int)(id % tiles) * 256 + threadIdx.x) * V;
     if (e >= D) return;
     int64_t len = a.steps;
     if (a.lengths) {
@@ -51,21 +52,27 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int64_t 
     const float af = (float)exp(gd * (double)a.seg_len);
     const float ap = (float)exp(gd * (double)(len - whole * a.seg_len));
     float* p = R.seg + bh * a.nseg * D + e;
-    float X = R.s0 ? R.s0[bh * D + (e / R.dz) * R.s0_i + (e % R.dz) * R.s0_j] : 0.f;
+    Vec<float, V> X{};
+    if (R.s0) {
+        const float* s = R.s0 + bh * D;
+#pragma unroll
+        for (int j = 0; j < V; ++j)  // the slots' order is i dz + j
+            X.e[j] = s[(e + j) / R.dz * R.s0_i + (e + j) % R.dz * R.s0_j];
+    }
     for (int i0 = 0; i0 < a.nseg; i0 += 8) {
-        float L[8];  // asked for together
+        Vec<float, V> L[8] = {};
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-            L[k] = i0 + k < a.nseg - 1 && (i0 + k) * a.seg_len < len ? p[(i0 + k) * D] : 0.f;
+            if (i0 + k < a.nseg - 1 && (i0 + k) * a.seg_len < len)
+                L[k] = load_vec<float, V>(p + (int64_t)(i0 + k) * D);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const int i = i0 + k;
             if (i >= a.nseg) break;
-            p[i * D] = X;
-            if (i < whole)
-                X = af * X + L[k];
-            else if (i * a.seg_len < len)
-                X = ap * X + L[k];
+            store_vec<float, V>(p + (int64_t)i * D, X);
+            const float keep = i < whole ? af : (i * a.seg_len < len ? ap : 1.f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) X.e[j] = keep * X.e[j] + L[k].e[j];
         }
     }
 }
@@ -101,17 +108,31 @@ hipError_t walk(const AttendArgs& a, bool maps, hipStream_t st) {
     }
 }
 
-hipError_t run_all(const AttendArgs& a, hipStream_t st) {
+// Up to this many segments, each adds up those before it as it starts; more are joined by
+// a launch of their own.
+constexpr int kFold = 4;
+
+// `maps`: the first runs, whose segments' states are made (the others read one of theirs).
+hipError_t run_all(AttendArgs a, int maps, hipStream_t st) {
     if (a.nseg > 1) {
+        const int runs = a.nrun;
+        a.nrun = maps;
         hipError_t e = walk(a, true, st);
         if (e != hipSuccess) return e;
-        int64_t D = 0;
-        for (int r = 0; r < a.nrun; ++r) D = (int64_t)a.run[r].dx * a.run[r].dz;  // the same in all
-        const int tiles = (int)((D + 255) / 256);
-        e = in_launches(a.batch * a.heads * tiles, [&](int64_t first, unsigned n) {
-            attend_join_kernel<<<dim3(n, (unsigned)a.nrun), 256, 0, st>>>(a, first, tiles);
-        });
-        if (e != hipSuccess) return e;
+        if (a.nseg > kFold) {
+            a.joined = 1;
+            const int D = a.run[0].dx * a.run[0].dz;  // the same in all
+            const int v = D % 4 == 0 ? 4 : 1, tiles = (D + 256 * v - 1) / (256 * v);
+            e = in_launches(a.batch * a.heads * tiles, [&](int64_t first, unsigned n) {
+                const dim3 grid(n, (unsigned)maps);
+                if (v == 4)
+                    attend_join_kernel<4><<<grid, 256, 0, st>>>(a, first, tiles);
+                else
+                    attend_join_kernel<1><<<grid, 256, 0, st>>>(a, first, tiles);
+            });
+            if (e != hipSuccess) return e;
+        }
+        a.nrun = runs;
     }
     return walk(a, false, st);
 }
@@ -141,6 +162,7 @@ void set_run(AttendRun& r, const Operand& x, const Operand& y, const Operand& z)
     r.z = z.p, r.zb = z.s[0], r.zt = z.s[1], r.zh = z.s[2], r.zg = z.group;
     r.dx = x.d;
     r.dz = z.d;
+    r.seg_i = z.d, r.seg_j = 1;
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
@@ -156,7 +178,7 @@ size_t part_bytes(const AttendDesc& d, int width) {
 }  // namespace
 
 size_t attend_ws_bytes(const AttendDesc& d, bool gradient) {
-    const size_t n = gradient ? 3 * seg_bytes(d, 3) + part_bytes(d, d.dk) + part_bytes(d, d.dv)
+    const size_t n = gradient ? 2 * seg_bytes(d, 3) + part_bytes(d, d.dk) + part_bytes(d, d.dv)
                               : seg_bytes(d, 1);
     return n ? n : 256;
 }
@@ -175,7 +197,7 @@ hipError_t launch_attend(const AttendCall& c, hipStream_t st) {
     r.s1_i = c.d.dv, r.s1_j = 1;
     r.out = c.o;
     r.seg = static_cast<float*>(c.ws);
-    return run_all(a, st);
+    return run_all(a, 1, st);
 }
 
 // dq runs forward with the transposed state, dk and dv backward in time:
@@ -190,8 +212,8 @@ hipError_t launch_attend_grad(const AttendCall& c, hipStream_t st) {
         d{c.dout, c.d.d, 1, dv};
     char* ws = static_cast<char*>(c.ws);
     const size_t seg = seg_bytes(c.d, 3), pk = part_bytes(c.d, dk);
-    float* part_k = reinterpret_cast<float*>(ws + 3 * seg);
-    float* part_v = reinterpret_cast<float*>(ws + 3 * seg + pk);
+    float* part_k = reinterpret_cast<float*>(ws + 2 * seg);
+    float* part_v = reinterpret_cast<float*>(ws + 2 * seg + pk);
 
     AttendRun& rq = a.run[0];
     set_run(rq, d, v, k);
@@ -224,8 +246,10 @@ hipError_t launch_attend_grad(const AttendCall& c, hipStream_t st) {
     rk.out = g > 1 ? static_cast<void*>(part_k) : c.dk;
     rk.out32 = g > 1;
 
-    for (int r = 0; r < 3; ++r) a.run[r].seg = reinterpret_cast<float*>(ws + r * seg);
-    hipError_t e = run_all(a, st);
+    rq.seg = reinterpret_cast<float*>(ws);
+    rv.seg = rk.seg = reinterpret_cast<float*>(ws + seg);  // the one state, and transposed
+    rk.seg_i = 1, rk.seg_j = dv;
+    hipError_t e = run_all(a, 2, st);
     if (e != hipSuccess || g == 1) return e;
     const int64_t rows = c.d.batch * c.d.steps * c.d.kv_heads;
     auto sum = [&](const float* part, void* out, int width) {

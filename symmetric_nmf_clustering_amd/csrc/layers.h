@@ -30,7 +30,8 @@ struct AttendRun {
     int32_t s1_i, s1_j;
     void* out;            // batch x steps x heads x dz, dense
     int32_t out32;        // out is float32 whatever the type
-    float* seg;           // nseg > 1: batch x heads x nseg x dx x dz
+    float* seg;           // nseg > 1: batch x heads x nseg x (dx dz), element (i, j) at
+    int32_t seg_i, seg_j;  // i seg_i + j seg_j
 };
 
 struct AttendArgs {
@@ -39,6 +40,7 @@ struct AttendArgs {
     const float* decay;      // heads: ln a
     const int32_t* lengths;  // nullable
     int32_t type, heads, nseg;
+    int32_t joined;  // the segments' slots hold the states they start from, not their own
     int64_t batch, steps, seg_len;
 };
 

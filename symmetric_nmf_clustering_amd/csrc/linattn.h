@@ -306,27 +306,44 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
 
     // the state at the segment's start
     floatx4 S[NX][WN];
-    {
-        const float* s = nullptr;
-        int si = 0, sj = 0;
-        if (OUT && a.nseg > 1) {
-            s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
-            si = R.dz;
-            sj = 1;
-        } else if (OUT && R.s0) {
-            s = R.s0 + bh * ((int64_t)R.dx * R.dz);
-            si = R.s0_i;
-            sj = R.s0_j;
-        }
+    auto element = [&](int i, int m, int r, int si, int sj) __attribute__((always_inline)) {  // where S[i][m][r] is, or -1
+        const int row = 16 * i + 4 * g + r, j = zw + 16 * m + l16;
+        return row < R.dx && j < R.dz ? row * si + j * sj : -1;
+    };
 #pragma unroll
-        for (int i = 0; i < NX; ++i)
+    for (int i = 0; i < NX; ++i)
 #pragma unroll
-            for (int m = 0; m < WN; ++m)
+        for (int m = 0; m < WN; ++m) S[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (OUT) {
+        const int64_t D = (int64_t)R.dx * R.dz;
+        const float keep = (float)exp(gd * (double)a.seg_len);
+        // S = what is joined, or s0 (m = -1) and then the segments before this one
+        const int last = a.joined ? -1 : seg - 1;
+        for (int m = -1; m <= last; ++m) {
+            const float* s = m >= 0 ? R.seg + (bh * a.nseg + m) * D
+                                    : (a.joined ? R.seg + (bh * a.nseg + seg) * D
+                                                : (R.s0 ? R.s0 + bh * D : nullptr));
+            if (!s) continue;
+            const int64_t left = len - m * a.seg_len;
+            if (m >= 0 && left <= 0) break;
+            const bool slot = m >= 0 || a.joined;
+            const int si = slot ? R.seg_i : R.s0_i, sj = slot ? R.seg_j : R.s0_j;
+            const float k = m < 0 ? 0.f
+                                  : (left >= a.seg_len ? keep : (float)exp(gd * (double)left));
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * i + 4 * g + r, j = zw + 16 * m + l16;
-                    S[i][m][r] = s && row < R.dx && j < R.dz ? s[(uint32_t)(row * si + j * sj)] : 0.f;
+            for (int i = 0; i < NX; ++i) {
+                float v[4 * WN];  // (asked for without branches: all in flight)
+#pragma unroll
+                for (int q = 0; q < 4 * WN; ++q)
+                    v[q] = s[(uint32_t)max(element(i, q >> 2, q & 3, si, sj), 0)];
+#pragma unroll
+                for (int q = 0; q < 4 * WN; ++q) {
+                    asm volatile("" : "+v"(v[q]));
+                    const float to = k * S[i][q >> 2][q & 3] + v[q];
+                    S[i][q >> 2][q & 3] = element(i, q >> 2, q & 3, si, sj) >= 0 ? to : 0.f;
                 }
+            }
+        }
     }
 
     if constexpr (OUT) {
@@ -340,14 +357,14 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
 
     typename Z::TX rx, ry;
     typename Z::TZ rz;
-    auto fetch = [&](int64_t u0) {
+    auto fetch = [&](int64_t u0) __attribute__((always_inline)) {
         const int n = (int)min(u_stop - u0, (int64_t)C);
         if (OUT) rx.load(mx, u0, n, 0);
         ry.load(my, u0, n, 0);
         rz.load(mz, u0, n, z0);
     };
     // A chunk of n steps from u0; FULL: n = C.
-    auto chunk = [&](auto full, int64_t u0, int n) {
+    auto chunk = [&](auto full, int64_t u0, int n) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
         if (!WIDE) fetch(u0);  // (many registers: not kept through a chunk)
         lds_barrier();         // the tiles of the last chunk are read
@@ -494,7 +511,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     }
 
     float* s = nullptr;
-    int si = R.dz, sj = 1;
+    int si = R.seg_i, sj = R.seg_j;
     if (!OUT) {
         s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
     } else if (seg == a.nseg - 1 && R.s1) {
@@ -509,8 +526,8 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             for (int m = 0; m < WN; ++m)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * i + 4 * g + r, j = zw + 16 * m + l16;
-                    if (row < R.dx && j < R.dz) s[(uint32_t)(row * si + j * sj)] = S[i][m][r];
+                    const int at = element(i, m, r, si, sj);
+                    if (at >= 0) s[(uint32_t)at] = S[i][m][r];
                 }
     }
 }
