@@ -11,16 +11,16 @@ namespace {
 
 // Few heads are cut in time: every segment's own state first (maps), then their
 // join, then all segments walk at once, each from its state. That reads y and z
-// twice, so time is cut only where heads and column tiles leave CUs without work,
-// and into no more segments than fill them.
-constexpr int kWant = 512;      // workgroups
-constexpr int64_t kLeast = 256;  // steps a segment has at least
+// twice, so time is cut only where heads and column tiles make less than one
+// workgroup a CU, and into no more segments than two a CU, which run at once.
+constexpr int kEnough = 256, kMost = 512;  // workgroups
+constexpr int64_t kLeast = 128;            // steps a segment has at least
 
 int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
-    const int wide = d.dk > d.dv ? d.dk : d.dv, cols = wide > 64 && wide <= 128 ? 128 : 64;
-    const int ztiles = (wide + cols - 1) / cols;
-    const int64_t items = d.batch * d.heads * ztiles * runs;
-    int64_t n = (kWant + items - 1) / items;
+    const int wide = d.dk > d.dv ? d.dk : d.dv;
+    const int cols = wide > 64 && wide <= 128 && d.type != kF32 ? 128 : 64;
+    const int64_t items = d.batch * d.heads * ((wide + cols - 1) / cols) * runs;
+    int64_t n = items >= kEnough ? 1 : kMost / items;
     const int64_t most = d.steps / kLeast;
     if (n > most) n = most;
     if (n < 1) n = 1;
@@ -108,10 +108,6 @@ hipError_t walk(const AttendArgs& a, bool maps, hipStream_t st) {
     }
 }
 
-// Up to this many segments, each adds up those before it as it starts; more are joined by
-// a launch of their own.
-constexpr int kFold = 4;
-
 // `maps`: the first runs, whose segments' states are made (the others read one of theirs).
 hipError_t run_all(AttendArgs a, int maps, hipStream_t st) {
     if (a.nseg > 1) {
@@ -119,19 +115,16 @@ hipError_t run_all(AttendArgs a, int maps, hipStream_t st) {
         a.nrun = maps;
         hipError_t e = walk(a, true, st);
         if (e != hipSuccess) return e;
-        if (a.nseg > kFold) {
-            a.joined = 1;
-            const int D = a.run[0].dx * a.run[0].dz;  // the same in all
-            const int v = D % 4 == 0 ? 4 : 1, tiles = (D + 256 * v - 1) / (256 * v);
-            e = in_launches(a.batch * a.heads * tiles, [&](int64_t first, unsigned n) {
-                const dim3 grid(n, (unsigned)maps);
-                if (v == 4)
-                    attend_join_kernel<4><<<grid, 256, 0, st>>>(a, first, tiles);
-                else
-                    attend_join_kernel<1><<<grid, 256, 0, st>>>(a, first, tiles);
-            });
-            if (e != hipSuccess) return e;
-        }
+        const int D = a.run[0].dx * a.run[0].dz;  // the same in all
+        const int v = D % 4 == 0 ? 4 : 1, tiles = (D + 256 * v - 1) / (256 * v);
+        e = in_launches(a.batch * a.heads * tiles, [&](int64_t first, unsigned n) {
+            const dim3 grid(n, (unsigned)maps);
+            if (v == 4)
+                attend_join_kernel<4><<<grid, 256, 0, st>>>(a, first, tiles);
+            else
+                attend_join_kernel<1><<<grid, 256, 0, st>>>(a, first, tiles);
+        });
+        if (e != hipSuccess) return e;
         a.nrun = runs;
     }
     return walk(a, false, st);

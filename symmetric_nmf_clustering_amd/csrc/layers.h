@@ -40,7 +40,6 @@ struct AttendArgs {
     const float* decay;      // heads: ln a
     const int32_t* lengths;  // nullable
     int32_t type, heads, nseg;
-    int32_t joined;  // the segments' slots hold the states they start from, not their own
     int64_t batch, steps, seg_len;
 };
 

@@ -13,11 +13,15 @@
 // Results come out transposed (a lane has 4 columns of one step): 8 or 16 bytes a
 // store. P alone passes through LDS, in the order its reader's lanes want it.
 //
-// bf16: products on the bf16 matrix cores. P and, in X S, the state are rounded to
-// bf16 (as the inputs and the output are: each costs the output at most what its
-// own rounding does). The state itself stays at float32's precision: the weights
-// go to z, and w z is split exactly into three bf16 parts, three products each.
-// fp32: 16x16x4 float32 products. fp16: widened to float32 as it is loaded.
+// All products run on the bf16 matrix cores, on bf16 parts ("planes") of their operands
+// whose products are summed in float32:
+//   bf16: one plane; P and, in X S, the state are rounded to bf16 (as the inputs and the
+//     output are: each costs the output at most what its own rounding does).
+//   fp16: two planes hold an element exactly; P and S, in two, lose 2^-18; three products.
+//   fp32: three planes (bf16split.h), six products, which is float32's precision; 16x16x4
+//     float32 products would take 2.7 times their cycles.
+// The state itself stays at float32's precision in every type: the weights go to z, and w z
+// is split into three planes (3, 5 and 6 products).
 #pragma once
 
 #include <type_traits>
@@ -38,120 +42,122 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Planes of an element type, and steps of a chunk.
 template <class T>
-struct InLds {  // how a tile is held
-    using type = float;
+struct Planes {
+    static constexpr int N = 3, C = 32;
 };
 template <>
-struct InLds<bf16_t> {
-    using type = bf16_t;
+struct Planes<f16_t> {
+    static constexpr int N = 2, C = 32;
+};
+template <>
+struct Planes<bf16_t> {
+    static constexpr int N = 1, C = 64;
 };
 
-// 32 deep operands of a product: 8 values a lane. rows(p): depth 8g + j, p at the
-// lane's own row; split(p): depth 4g + j and 16 + 4g + j (see above); column(t,
-// stride): the same depth order down the rows of a tile, lane l % 16's column.
-template <class LT>
-struct Op;
+// 32 deep operands of a product: a lane's 8 values, as N planes of bf16.
+template <int N>
+struct Frag {
+    u32x4 p[N];
+};
 
-template <>
-struct Op<bf16_t> {
-    using F = u32x4;
-    static __device__ __forceinline__ F rows(const bf16_t* p, int g) {
-        return *reinterpret_cast<const u32x4*>(p + 8 * g);
-    }
-    static __device__ __forceinline__ F split(const bf16_t* p, int g) {
-        const uint2 a = *reinterpret_cast<const uint2*>(p + 4 * g);
-        const uint2 b = *reinterpret_cast<const uint2*>(p + 16 + 4 * g);
-        return F{a.x, a.y, b.x, b.y};
-    }
-    static __device__ __forceinline__ F column(const bf16_t* t, int stride, int lane) {
-        // a 4 x 16 block for each 16 lanes, read transposed: lane i asks for 4 elements of row
-        // i / 4 and receives column i
-        const bf16_t* p = t + (4 * (lane >> 4) + ((lane & 15) >> 2)) * stride + 4 * (lane & 3);
-        typedef __attribute__((address_space(3))) s16x4 lds4;
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)p);
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + 16 * stride));
-        const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
-        return F{ua.x, ua.y, ub.x, ub.y};
-    }
-    // the lane's values of two 16-deep blocks of a result
-    static __device__ __forceinline__ F of(const floatx4& a, const floatx4& b) {
-        return F{pack(a[0], a[1]), pack(a[2], a[3]), pack(b[0], b[1]), pack(b[2], b[3])};
-    }
-    static __device__ __forceinline__ uint32_t pack(float a, float b) {
-        const f32x2 v = {a, b};
-        return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
-    }
-    static __device__ __forceinline__ floatx4 mma(const F& a, const F& b, floatx4 c) {
-        return mfma_bf16(a, b, c);
-    }
-    // a times (w . b) to float32's precision
-    struct W {
-        F p[3];
-    };
-    static __device__ __forceinline__ W weigh(const F& b, const float (&w)[8]) {
-        W o;
+// (a, b) -> the packed pairs of their first N planes
+template <int N>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t (&p)[N]) {
+    f32x2 v = {a, b};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t p1, p2, p3;
-            split3_pair(__uint_as_float(b[i] << 16) * w[2 * i],
-                        __uint_as_float(b[i] & 0xffff0000u) * w[2 * i + 1], p1, p2, p3);
-            o.p[0][i] = p1;
-            o.p[1][i] = p2;
-            o.p[2][i] = p3;
+    for (int i = 0; i < N; ++i) {
+        const bf16x2 h = __builtin_convertvector(v, bf16x2);
+        p[i] = __builtin_bit_cast(uint32_t, h);
+        if (i + 1 < N) v = v - __builtin_convertvector(h, f32x2);
+    }
+}
+template <int N>
+__device__ __forceinline__ Frag<N> split8(const float (&v)[8]) {
+    Frag<N> f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t p[N];
+        split_pair<N>(v[2 * i], v[2 * i + 1], p);
+#pragma unroll
+        for (int j = 0; j < N; ++j) f.p[j][i] = p[j];
+    }
+    return f;
+}
+// the lane's values of two 16-deep blocks of a result
+template <int N>
+__device__ __forceinline__ Frag<N> frag_of(const floatx4& a, const floatx4& b) {
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return split8<N>(v);
+}
+// w . f to float32's precision
+template <int N>
+__device__ __forceinline__ Frag<3> weigh(const Frag<N>& f, const float (&w)[8]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = v[2 * i + 1] = 0.f;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j) {
+            v[2 * i] += __uint_as_float(f.p[j][i] << 16);
+            v[2 * i + 1] += __uint_as_float(f.p[j][i] & 0xffff0000u);
         }
-        return o;
+        v[2 * i] *= w[2 * i];
+        v[2 * i + 1] *= w[2 * i + 1];
     }
-    static __device__ __forceinline__ floatx4 mma(const F& a, const W& b, floatx4 c) {
-        c = mfma_bf16(a, b.p[2], c);
-        c = mfma_bf16(a, b.p[1], c);
-        return mfma_bf16(a, b.p[0], c);
-    }
-    static __device__ __forceinline__ void put4(bf16_t* p, const floatx4& v) {
-        *reinterpret_cast<uint2*>(p) = uint2{pack(v[0], v[1]), pack(v[2], v[3])};
-    }
-};
+    return split8<3>(v);
+}
+// The products of planes i and j with i + j < K, smallest first.
+template <int K, int NA, int NB>
+__device__ __forceinline__ floatx4 mma(const Frag<NA>& a, const Frag<NB>& b, floatx4 c) {
+#pragma unroll
+    for (int s = K - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i <= s; ++i)
+            if (i < NA && s - i < NB) c = mfma_bf16(a.p[i], b.p[s - i], c);
+    return c;
+}
 
-template <>
-struct Op<float> {
-    struct F {
-        float v[8];
-    };
-    static __device__ __forceinline__ F two(const float* p, const float* q) {
-        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(q);
-        return F{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
-    }
-    static __device__ __forceinline__ F rows(const float* p, int g) {
-        return two(p + 8 * g, p + 8 * g + 4);
-    }
-    static __device__ __forceinline__ F split(const float* p, int g) {
-        return two(p + 4 * g, p + 16 + 4 * g);
-    }
-    static __device__ __forceinline__ F column(const float* t, int stride, int lane) {
-        F o;
-        const float* p = t + 4 * (lane >> 4) * stride + (lane & 15);
+// Reads of a tile (N planes, `plane` elements apart). rows: depth 8g + j of the lane's own
+// row p; split: depth 4g + j and 16 + 4g + j (see above); column: the same order down
+// the rows of a tile, lane l % 16's column.
+template <int N>
+__device__ __forceinline__ Frag<N> read_rows(const bf16_t* p, int plane, int g) {
+    Frag<N> f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = p[((j & 3) + (j >> 2) * 16) * stride];
-        return o;
-    }
-    static __device__ __forceinline__ F of(const floatx4& a, const floatx4& b) {
-        return F{{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]}};
-    }
-    static __device__ __forceinline__ floatx4 mma(const F& a, const F& b, floatx4 c) {
+    for (int i = 0; i < N; ++i)
+        f.p[i] = *reinterpret_cast<const u32x4*>(p + i * plane + 8 * g);
+    return f;
+}
+template <int N>
+__device__ __forceinline__ Frag<N> read_split(const bf16_t* p, int plane, int next, int g) {
+    Frag<N> f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) c = mfma16x16x4(a.v[j], b.v[j], c);
-        return c;
+    for (int i = 0; i < N; ++i) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p + i * plane + 4 * g);
+        const uint2 b = *reinterpret_cast<const uint2*>(p + i * plane + next + 4 * g);
+        f.p[i] = u32x4{a.x, a.y, b.x, b.y};
     }
-    static __device__ __forceinline__ F weigh(const F& b, const float (&w)[8]) {
-        F o;
+    return f;
+}
+template <int N>
+__device__ __forceinline__ Frag<N> read_column(const bf16_t* t, int plane, int stride, int lane) {
+    // a 4 x 16 block for each 16 lanes, read transposed: lane i asks for 4 elements of row
+    // i / 4 and receives column i
+    const bf16_t* p = t + (4 * (lane >> 4) + ((lane & 15) >> 2)) * stride + 4 * (lane & 3);
+    typedef __attribute__((address_space(3))) s16x4 lds4;
+    Frag<N> f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o.v[j] = b.v[j] * w[j];
-        return o;
+    for (int i = 0; i < N; ++i) {
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + i * plane));
+        const s16x4 b =
+            __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(p + i * plane + 16 * stride));
+        const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
+        f.p[i] = u32x4{ua.x, ua.y, ub.x, ub.y};
     }
-    static __device__ __forceinline__ void put4(float* p, const floatx4& v) {
-        *reinterpret_cast<f32x4*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-    }
-};
+    return f;
+}
 
 // The rows of one operand of a head, in the order of the walk.
 template <class T>
@@ -170,10 +176,10 @@ constexpr int64_t kNearStride = int64_t(1) << 24;
 // rows or columns read the last one, and store() clears them. (A branch around each
 // costs a wait for each: 2.4 times the time of the whole walk.) WIDE: 16 bytes a
 // lane, for d a multiple of that; otherwise one element a lane, neighbours together.
-template <class T, class LT, int C, int COLS, int NT, bool WIDE>
+template <class T, int C, int COLS, int NT, bool WIDE>
 struct Tile {
     static constexpr int V = WIDE ? 16 / sizeof(T) : 1, G = COLS / V, N = (C * G + NT - 1) / NT;
-    static constexpr int STRIDE = COLS + 16 / (int)sizeof(LT);
+    static constexpr int STRIDE = COLS + 8, PLANE = C * STRIDE, NP = Planes<T>::N;
     Vec<T, V> r[N];
 
     __device__ __forceinline__ void load(const Rows<T>& m, int64_t u0, int n, int c0) {
@@ -191,22 +197,38 @@ struct Tile {
     }
     // n: rows that count (C: all); d: columns that count, from c0 on
     template <bool FULL>
-    __device__ __forceinline__ void store(LT* t, int d, int n, int c0) const {
+    __device__ __forceinline__ void store(bf16_t* t, int d, int n, int c0) const {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = threadIdx.x + i * NT, row = at / G, c = at % G * V;
             if (C * G % NT && row >= C) continue;
             const bool in = c0 + c < d && (FULL || row < n);
-            if constexpr (sizeof(T) == sizeof(LT) && WIDE) {
+            bf16_t* q = t + row * STRIDE + c;
+            if constexpr (V == 1) {
+                float v = in ? to_f32(r[i].e[0]) : 0.f;
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    q[j * PLANE] = from_f32<bf16_t>(v);
+                    v -= to_f32(q[j * PLANE]);
+                }
+            } else if constexpr (NP == 1) {
                 u32x4 v = __builtin_bit_cast(u32x4, r[i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = in ? v[j] : 0u;
-                *reinterpret_cast<u32x4*>(t + row * STRIDE + c) = v;
-            } else if constexpr (sizeof(T) == sizeof(LT)) {
-                t[row * STRIDE + c] = in ? r[i].e[0] : LT{};
+                *reinterpret_cast<u32x4*>(q) = v;
             } else {
+                Vec<uint32_t, V / 2> w[NP];
 #pragma unroll
-                for (int j = 0; j < V; ++j) t[row * STRIDE + c + j] = in ? to_f32(r[i].e[j]) : 0.f;
+                for (int j = 0; j < V / 2; ++j) {
+                    uint32_t p[NP];
+                    split_pair<NP>(in ? to_f32(r[i].e[2 * j]) : 0.f,
+                                   in ? to_f32(r[i].e[2 * j + 1]) : 0.f, p);
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) w[k].e[j] = p[k];
+                }
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    *reinterpret_cast<Vec<uint32_t, V / 2>*>(q + k * PLANE) = w[k];
             }
         }
     }
@@ -214,16 +236,15 @@ struct Tile {
 
 template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
-    using LT = typename InLds<T>::type;
-    static constexpr int C = sizeof(LT) == 2 ? 64 : 32;
+    static constexpr int C = Planes<T>::C, NP = Planes<T>::N;
     static constexpr int NT = 64 * NW, ZC = 16 * WN * NW;
-    using TX = Tile<T, LT, C, DX, NT, WIDE>;
-    using TZ = Tile<T, LT, C, ZC, NT, WIDE>;
+    using TX = Tile<T, C, DX, NT, WIDE>;
+    using TZ = Tile<T, C, ZC, NT, WIDE>;
     struct Lds {
-        LT x[OUT ? C * TX::STRIDE : 8];
-        LT y[C * TX::STRIDE];
-        LT z[C * TZ::STRIDE];
-        LT p[OUT ? C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
+        bf16_t x[OUT ? NP * TX::PLANE : 8];
+        bf16_t y[NP * TX::PLANE];
+        bf16_t z[NP * TZ::PLANE];
+        bf16_t p[OUT ? NP * C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
         float wz[C];            // st_scale a^(C - in_pow - w): the weights of a whole chunk
         float wx[OUT ? C : 4];  // in_scale a^(u + in_pow)
         float wp[OUT ? C * 16 : 4];  // p_scale a^(u - w), as a lane holds a block, by bu - bw
@@ -255,9 +276,8 @@ template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     AttendArgs a, int64_t first, int64_t items, int ztiles) {
     using Z = WalkSizes<T, DX, NW, WN, OUT, WIDE>;
-    using LT = typename Z::LT;
-    using O = Op<LT>;
-    constexpr int C = Z::C, NX = DX / 16, NB = C / 16, XS = Z::TX::STRIDE, ZS = Z::TZ::STRIDE;
+    constexpr int C = Z::C, NP = Z::NP, NX = DX / 16, NB = C / 16;
+    constexpr int XS = Z::TX::STRIDE, ZS = Z::TZ::STRIDE, XP = Z::TX::PLANE, ZP = Z::TZ::PLANE;
     __shared__ alignas(16) typename Z::Lds lds;
 
     // items go round the XCDs; the column tiles of one item to the same XCD, whose L2
@@ -292,7 +312,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     for (int i = threadIdx.x; i < C; i += Z::NT)
         lds.wz[i] = R.st_scale * (float)exp(gd * (C - R.in_pow - i));
     if constexpr (OUT) {  // blocks above the diagonal that a 32-deep step reads
-        for (int i = threadIdx.x; i < C * C; i += Z::NT) lds.p[i] = LT{};
+        for (int i = threadIdx.x; i < NP * C * C; i += Z::NT) lds.p[i] = bf16_t{};
     }
 
     const int64_t dir = R.reverse ? -1 : 1, from = R.reverse ? len - 1 : 0;
@@ -316,20 +336,10 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
         for (int m = 0; m < WN; ++m) S[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
     if constexpr (OUT) {
         const int64_t D = (int64_t)R.dx * R.dz;
-        const float keep = (float)exp(gd * (double)a.seg_len);
-        // S = what is joined, or s0 (m = -1) and then the segments before this one
-        const int last = a.joined ? -1 : seg - 1;
-        for (int m = -1; m <= last; ++m) {
-            const float* s = m >= 0 ? R.seg + (bh * a.nseg + m) * D
-                                    : (a.joined ? R.seg + (bh * a.nseg + seg) * D
-                                                : (R.s0 ? R.s0 + bh * D : nullptr));
-            if (!s) continue;
-            const int64_t left = len - m * a.seg_len;
-            if (m >= 0 && left <= 0) break;
-            const bool slot = m >= 0 || a.joined;
-            const int si = slot ? R.seg_i : R.s0_i, sj = slot ? R.seg_j : R.s0_j;
-            const float k = m < 0 ? 0.f
-                                  : (left >= a.seg_len ? keep : (float)exp(gd * (double)left));
+        const bool cut = a.nseg > 1;  // the join has left the segment's state in its slot
+        const float* s = cut ? R.seg + (bh * a.nseg + seg) * D : (R.s0 ? R.s0 + bh * D : nullptr);
+        const int si = cut ? R.seg_i : R.s0_i, sj = cut ? R.seg_j : R.s0_j;
+        if (s) {
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
                 float v[4 * WN];  // (asked for without branches: all in flight)
@@ -339,8 +349,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
 #pragma unroll
                 for (int q = 0; q < 4 * WN; ++q) {
                     asm volatile("" : "+v"(v[q]));
-                    const float to = k * S[i][q >> 2][q & 3] + v[q];
-                    S[i][q >> 2][q & 3] = element(i, q >> 2, q & 3, si, sj) >= 0 ? to : 0.f;
+                    S[i][q >> 2][q & 3] = element(i, q >> 2, q & 3, si, sj) >= 0 ? v[q] : 0.f;
                 }
             }
         }
@@ -382,60 +391,62 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                 if (at >= BLOCKS) break;
                 const int bu = (at >= 1) + (at >= 3) + (at >= 6), bw = at - bu * (bu + 1) / 2;
                 floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-                const LT* py = lds.y + (16 * bw + l16) * XS;
-                const LT* px = lds.x + (16 * bu + l16) * XS;
+                const bf16_t* py = lds.y + (16 * bw + l16) * XS;
+                const bf16_t* px = lds.x + (16 * bu + l16) * XS;
 #pragma unroll
                 for (int k = 0; k < DX / 32; ++k)
-                    acc = O::mma(O::rows(py + 32 * k, g), O::rows(px + 32 * k, g), acc);
+                    acc = mma<NP>(read_rows<NP>(py + 32 * k, XP, g),
+                                  read_rows<NP>(px + 32 * k, XP, g), acc);
                 const f32x4 wp = *reinterpret_cast<const f32x4*>(lds.wp + ((bu - bw) * 64 + lane) * 4);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[r] = wp[r] != 0.f ? acc[r] * wp[r] : 0.f;
-                O::put4(lds.p + ((bu * NB + bw) * 64 + lane) * 4, acc);
+                uint32_t p0[NP], p1[NP];
+                split_pair<NP>(acc[0], acc[1], p0);
+                split_pair<NP>(acc[2], acc[3], p1);
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+                    *reinterpret_cast<uint2*>(lds.p + j * C * C + ((bu * NB + bw) * 64 + lane) * 4) =
+                        uint2{p0[j], p1[j]};
             }
             lds_barrier();
         }
 
-        typename O::F zf[C / 32][WN];
+        Frag<NP> zf[C / 32][WN];
 #pragma unroll
         for (int k = 0; k < C / 32; ++k)
 #pragma unroll
             for (int m = 0; m < WN; ++m)
-                zf[k][m] = O::column(lds.z + 32 * k * ZS + 16 * (WN * wave + m), ZS, lane);
+                zf[k][m] = read_column<NP>(lds.z + 32 * k * ZS + 16 * (WN * wave + m), ZP, ZS, lane);
 
         if constexpr (OUT) {
-            typename O::F sf[DX / 32][WN];
+            Frag<NP> sf[DX / 32][WN];
 #pragma unroll
             for (int k = 0; k < DX / 32; ++k)
 #pragma unroll
-                for (int m = 0; m < WN; ++m) sf[k][m] = O::of(S[2 * k][m], S[2 * k + 1][m]);
+                for (int m = 0; m < WN; ++m) sf[k][m] = frag_of<NP>(S[2 * k][m], S[2 * k + 1][m]);
             const int64_t e0 = ((b * a.steps + from + dir * (u0 + l16)) * a.heads + head) * R.dz + zw + 4 * g;
             const int64_t es = dir * 16 * a.heads * R.dz;
 #pragma unroll
             for (int bu = 0; bu < NB; ++bu) {
                 floatx4 acc[WN] = {};
-                const LT* px = lds.x + (16 * bu + l16) * XS;
+                const bf16_t* px = lds.x + (16 * bu + l16) * XS;
 #pragma unroll
                 for (int k = 0; k < DX / 32; ++k) {
-                    const auto xf = O::split(px + 32 * k, g);
+                    const auto xf = read_split<NP>(px + 32 * k, XP, 16, g);
 #pragma unroll
-                    for (int m = 0; m < WN; ++m) acc[m] = O::mma(sf[k][m], xf, acc[m]);
+                    for (int m = 0; m < WN; ++m) acc[m] = mma<NP>(sf[k][m], xf, acc[m]);
                 }
                 const float wx = lds.wx[16 * bu + l16];
 #pragma unroll
                 for (int m = 0; m < WN; ++m) acc[m] *= wx;
 #pragma unroll
                 for (int k = 0; k <= bu / 2; ++k) {
-                    typename O::F pf;
-                    const LT* pp = lds.p + ((bu * NB + 2 * k) * 64 + lane) * 4;
-                    if constexpr (sizeof(LT) == 2) {
-                        const uint2 p0 = *reinterpret_cast<const uint2*>(pp);
-                        const uint2 p1 = *reinterpret_cast<const uint2*>(pp + 256);
-                        pf = typename O::F{p0.x, p0.y, p1.x, p1.y};
-                    } else {
-                        pf = O::two(pp, pp + 256);
-                    }
+                    // (a lane's 4 values of a block lie at lane * 4; those of the next block
+                    // down 256 further)
+                    const auto pf = read_split<NP>(
+                        lds.p + ((bu * NB + 2 * k) * 64 + l16) * 4 + 60 * g, C * C, 256, g);
 #pragma unroll
-                    for (int m = 0; m < WN; ++m) acc[m] = O::mma(zf[k][m], pf, acc[m]);
+                    for (int m = 0; m < WN; ++m) acc[m] = mma<NP>(zf[k][m], pf, acc[m]);
                 }
                 if (FULL || 16 * bu + l16 < n) {
                     const int64_t e = e0 + bu * es;
@@ -479,14 +490,14 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                     w[j] = R.st_scale * lds.pw[at < 0 ? 0 : at];
                 }
             }
-            decltype(O::weigh(zf[0][0], w)) zw8[WN];
+            Frag<3> zw8[WN];
 #pragma unroll
-            for (int m = 0; m < WN; ++m) zw8[m] = O::weigh(zf[k][m], w);
+            for (int m = 0; m < WN; ++m) zw8[m] = weigh(zf[k][m], w);
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
-                const auto yf = O::column(lds.y + 32 * k * XS + 16 * i, XS, lane);
+                const auto yf = read_column<NP>(lds.y + 32 * k * XS + 16 * i, XP, XS, lane);
 #pragma unroll
-                for (int m = 0; m < WN; ++m) S[i][m] = O::mma(yf, zw8[m], S[i][m]);
+                for (int m = 0; m < WN; ++m) S[i][m] = mma<3>(yf, zw8[m], S[i][m]);
             }
         }
     };
@@ -573,8 +584,12 @@ hipError_t launch_attend_walk(const AttendArgs& a, bool maps, hipStream_t st) {
     if (dx <= 32) SYMNMF_WALK(32, 4, 1);
     if (dx <= 64 && dz <= 32) SYMNMF_WALK(64, 2, 1);
     if (dx <= 64) SYMNMF_WALK(64, 4, 1);
+    // (fp32's planes leave LDS for two workgroups a CU only with one column tile)
+    constexpr int W = Planes<T>::N < 3 ? 2 : 1;
+    if (dx <= 96 && dz <= 64) SYMNMF_WALK(96, 4, 1);
+    if (dx <= 96) SYMNMF_WALK(96, 4, W);
     if (dx <= 128 && dz <= 64) SYMNMF_WALK(128, 4, 1);
-    if (dx <= 128) SYMNMF_WALK(128, 4, 2);
+    if (dx <= 128) SYMNMF_WALK(128, 4, W);
     SYMNMF_WALK(256, 4, 1);
 #undef SYMNMF_WALK
 }
