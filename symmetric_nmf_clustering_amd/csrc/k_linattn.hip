@@ -11,10 +11,13 @@ namespace {
 
 // Few heads are cut in time: every segment's own state first (maps), then their
 // join, then all segments walk at once, each from its state. That reads y and z
-// twice, so time is cut only where heads and column tiles make less than one
-// workgroup a CU, and into no more segments than two a CU, which run at once.
-constexpr int kEnough = 256, kMost = 512;  // workgroups
-constexpr int64_t kLeast = 128;            // steps a segment has at least
+// twice, so time is cut only where heads and column tiles make less than 192
+// workgroups, and into no more segments than two workgroups a CU, which run at once
+// (192 workgroups of 2048 steps: 148 us whole, 168 cut in two; 128: 112 us cut in
+// four, 131 in two). Two segments do not pay for the launches (512 steps of 16 heads:
+// 25.4 us whole, 28.5 in two, 23.7 in four), nor do short ones.
+constexpr int kEnough = 192, kMost = 512;       // workgroups
+constexpr int64_t kLeast = 128, kFewest = 3;    // steps of a segment, segments
 
 int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
     const int wide = d.dk > d.dv ? d.dk : d.dv;
@@ -23,7 +26,7 @@ int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
     int64_t n = items >= kEnough ? 1 : kMost / items;
     const int64_t most = d.steps / kLeast;
     if (n > most) n = most;
-    if (n < 1) n = 1;
+    if (n < kFewest) n = 1;
     int64_t len = (d.steps + n - 1) / n;
     len = (len + 63) / 64 * 64;
     if (len < 64) len = 64;
