@@ -176,10 +176,10 @@ constexpr int64_t kNearStride = int64_t(1) << 24;
 // rows or columns read the last one, and store() clears them. (A branch around each
 // costs a wait for each: 2.4 times the time of the whole walk.) WIDE: 16 bytes a
 // lane, for d a multiple of that; otherwise one element a lane, neighbours together.
-template <class T, int C, int COLS, int NT, bool WIDE>
+template <class T, int C, int COLS, int NT, bool WIDE, int PAD>
 struct Tile {
     static constexpr int V = WIDE ? 16 / sizeof(T) : 1, G = COLS / V, N = (C * G + NT - 1) / NT;
-    static constexpr int STRIDE = COLS + 8, PLANE = C * STRIDE, NP = Planes<T>::N;
+    static constexpr int STRIDE = COLS + PAD, PLANE = C * STRIDE, NP = Planes<T>::N;
     Vec<T, V> r[N];
 
     __device__ __forceinline__ void load(const Rows<T>& m, int64_t u0, int n, int c0) {
@@ -238,11 +238,13 @@ template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
     static constexpr int C = Planes<T>::C, NP = Planes<T>::N;
     static constexpr int NT = 64 * NW, ZC = 16 * WN * NW;
-    using TX = Tile<T, C, DX, NT, WIDE>;
-    using TZ = Tile<T, C, ZC, NT, WIDE>;
+    // pads of 16 bytes keep reads of rows off one another's banks, of 32 those down columns
+    using TX = Tile<T, C, DX, NT, WIDE, 8>;
+    using TY = Tile<T, C, DX, NT, WIDE, 16>;
+    using TZ = Tile<T, C, ZC, NT, WIDE, 16>;
     struct Lds {
         bf16_t x[OUT ? NP * TX::PLANE : 8];
-        bf16_t y[NP * TX::PLANE];
+        bf16_t y[NP * TY::PLANE];
         bf16_t z[NP * TZ::PLANE];
         bf16_t p[OUT ? NP * C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
         float wz[C];            // st_scale a^(C - in_pow - w): the weights of a whole chunk
@@ -277,7 +279,8 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     AttendArgs a, int64_t first, int64_t items, int ztiles) {
     using Z = WalkSizes<T, DX, NW, WN, OUT, WIDE>;
     constexpr int C = Z::C, NP = Z::NP, NX = DX / 16, NB = C / 16;
-    constexpr int XS = Z::TX::STRIDE, ZS = Z::TZ::STRIDE, XP = Z::TX::PLANE, ZP = Z::TZ::PLANE;
+    constexpr int XS = Z::TX::STRIDE, YS = Z::TY::STRIDE, ZS = Z::TZ::STRIDE;
+    constexpr int XP = Z::TX::PLANE, YP = Z::TY::PLANE, ZP = Z::TZ::PLANE;
     __shared__ alignas(16) typename Z::Lds lds;
 
     // items go round the XCDs; the column tiles of one item to the same XCD, whose L2
@@ -364,7 +367,8 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
         }
     }
 
-    typename Z::TX rx, ry;
+    typename Z::TX rx;
+    typename Z::TY ry;
     typename Z::TZ rz;
     auto fetch = [&](int64_t u0) __attribute__((always_inline)) {
         const int n = (int)min(u_stop - u0, (int64_t)C);
@@ -391,11 +395,11 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                 if (at >= BLOCKS) break;
                 const int bu = (at >= 1) + (at >= 3) + (at >= 6), bw = at - bu * (bu + 1) / 2;
                 floatx4 acc = {0.f, 0.f, 0.f, 0.f};
-                const bf16_t* py = lds.y + (16 * bw + l16) * XS;
+                const bf16_t* py = lds.y + (16 * bw + l16) * YS;
                 const bf16_t* px = lds.x + (16 * bu + l16) * XS;
 #pragma unroll
                 for (int k = 0; k < DX / 32; ++k)
-                    acc = mma<NP>(read_rows<NP>(py + 32 * k, XP, g),
+                    acc = mma<NP>(read_rows<NP>(py + 32 * k, YP, g),
                                   read_rows<NP>(px + 32 * k, XP, g), acc);
                 const f32x4 wp = *reinterpret_cast<const f32x4*>(lds.wp + ((bu - bw) * 64 + lane) * 4);
 #pragma unroll
@@ -495,7 +499,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             for (int m = 0; m < WN; ++m) zw8[m] = weigh(zf[k][m], w);
 #pragma unroll
             for (int i = 0; i < NX; ++i) {
-                const auto yf = read_column<NP>(lds.y + 32 * k * XS + 16 * i, XP, XS, lane);
+                const auto yf = read_column<NP>(lds.y + 32 * k * YS + 16 * i, YP, YS, lane);
 #pragma unroll
                 for (int m = 0; m < WN; ++m) S[i][m] = mma<3>(yf, zw8[m], S[i][m]);
             }
