@@ -37,7 +37,7 @@ int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
 
 // Slot i of a head's segments holds the state that segment i makes from nothing, and
 // receives the state it starts from: X_0 = s0, X_{i+1} = a^n_i X_i + L_i. A thread
-// takes V neighbouring elements; eight segments' are asked for together.
+// takes V neighbouring elements; sixteen segments' are asked for together.
 template <int V>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int64_t first,
                                                           int tiles) {
@@ -62,14 +62,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int64_t 
         for (int j = 0; j < V; ++j)  // the slots' order is i dz + j
             X.e[j] = s[(e + j) / R.dz * R.s0_i + (e + j) % R.dz * R.s0_j];
     }
-    for (int i0 = 0; i0 < a.nseg; i0 += 8) {
-        Vec<float, V> L[8] = {};
+    for (int i0 = 0; i0 < a.nseg; i0 += 16) {
+        Vec<float, V> L[16] = {};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+        for (int k = 0; k < 16; ++k)
             if (i0 + k < a.nseg - 1 && (i0 + k) * a.seg_len < len)
                 L[k] = load_vec<float, V>(p + (int64_t)(i0 + k) * D);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 16; ++k) {
             const int i = i0 + k;
             if (i >= a.nseg) break;
             store_vec<float, V>(p + (int64_t)i * D, X);

@@ -311,13 +311,6 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     if (!OUT && (u_begin >= len || seg == a.nseg - 1)) return;  // the join does not read these
 
     const double gd = ln_decay(a.decay, head);
-    for (int i = threadIdx.x; i <= C; i += Z::NT) lds.pw[i] = (float)exp(gd * i);
-    for (int i = threadIdx.x; i < C; i += Z::NT)
-        lds.wz[i] = R.st_scale * (float)exp(gd * (C - R.in_pow - i));
-    if constexpr (OUT) {  // blocks above the diagonal that a 32-deep step reads
-        for (int i = threadIdx.x; i < NP * C * C; i += Z::NT) lds.p[i] = bf16_t{};
-    }
-
     const int64_t dir = R.reverse ? -1 : 1, from = R.reverse ? len - 1 : 0;
     auto rows_of = [&](const void* p, int64_t sb, int64_t st, int64_t sh, int grp_, int d) {
         return Rows<T>{static_cast<const T*>(p) + b * sb + from * st + (head / grp_) * sh, st,
@@ -327,6 +320,15 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     const Rows<T> my = rows_of(R.y, R.yb, R.yt, R.yh, R.yg, R.dx);
     const Rows<T> mz = rows_of(R.z, R.zb, R.zt, R.zh, R.zg, R.dz);
 
+    typename Z::TX rx;
+    typename Z::TY ry;
+    typename Z::TZ rz;
+    auto fetch = [&](int64_t u0) __attribute__((always_inline)) {
+        const int n = (int)min(u_stop - u0, (int64_t)C);
+        if (OUT) rx.load(mx, u0, n, 0);
+        ry.load(my, u0, n, 0);
+        rz.load(mz, u0, n, z0);
+    };
     // the state at the segment's start
     floatx4 S[NX][WN];
     auto element = [&](int i, int m, int r, int si, int sj) __attribute__((always_inline)) {  // where S[i][m][r] is, or -1
@@ -358,24 +360,24 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
         }
     }
 
+    if (WIDE && u_begin < u_stop) fetch(u_begin);
+    // the tables of weights, from one table of powers
+    for (int i = threadIdx.x; i <= C; i += Z::NT) lds.pw[i] = (float)exp(gd * i);
+    lds_barrier();
+    for (int i = threadIdx.x; i < C; i += Z::NT) {
+        lds.wz[i] = R.st_scale * lds.pw[C - R.in_pow - i];
+        if (OUT) lds.wx[i] = R.in_scale * lds.pw[i + R.in_pow];
+    }
     if constexpr (OUT) {
-        for (int i = threadIdx.x; i < C; i += Z::NT)
-            lds.wx[i] = R.in_scale * (float)exp(gd * (i + R.in_pow));
         for (int i = threadIdx.x; i < C * 16; i += Z::NT) {
             const int gap = 16 * (i >> 8) + (i >> 2 & 15) - (4 * (i >> 6 & 3) + (i & 3));
-            lds.wp[i] = gap >= 0 ? R.p_scale * (float)exp(gd * gap) : 0.f;
+            lds.wp[i] = gap >= 0 ? R.p_scale * lds.pw[gap] : 0.f;
         }
+        // blocks above the diagonal that a 32-deep step reads
+        for (int i = threadIdx.x; i < NP * C * C / 2; i += Z::NT)
+            reinterpret_cast<uint32_t*>(lds.p)[i] = 0;
     }
 
-    typename Z::TX rx;
-    typename Z::TY ry;
-    typename Z::TZ rz;
-    auto fetch = [&](int64_t u0) __attribute__((always_inline)) {
-        const int n = (int)min(u_stop - u0, (int64_t)C);
-        if (OUT) rx.load(mx, u0, n, 0);
-        ry.load(my, u0, n, 0);
-        rz.load(mz, u0, n, z0);
-    };
     // A chunk of n steps from u0; FULL: n = C.
     auto chunk = [&](auto full, int64_t u0, int n) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
@@ -403,7 +405,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                                   read_rows<NP>(px + 32 * k, XP, g), acc);
                 const f32x4 wp = *reinterpret_cast<const f32x4*>(lds.wp + ((bu - bw) * 64 + lane) * 4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] = wp[r] != 0.f ? acc[r] * wp[r] : 0.f;
+                for (int r = 0; r < 4; ++r) acc[r] *= wp[r];
                 uint32_t p0[NP], p1[NP];
                 split_pair<NP>(acc[0], acc[1], p0);
                 split_pair<NP>(acc[2], acc[3], p1);
@@ -505,7 +507,6 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             }
         }
     };
-    if (WIDE && u_begin < u_stop) fetch(u_begin);
     int64_t u0 = u_begin;
     for (; u0 + C <= u_stop; u0 += C) chunk(std::true_type{}, u0, C);
     if (u0 < u_stop) chunk(std::false_type{}, u0, (int)(u_stop - u0));
