@@ -12,28 +12,42 @@ namespace symnmf {
 
 namespace {
 
-template <class T, int P, bool INTER>  // P pairs a thread, next to one another
-__device__ __forceinline__ void turn(const T* x, T* y, int half, const float (&c)[P],
-                                     const float (&s)[P]) {
+// P pairs next to one another, of U heads: all asked for before the first is turned.
+template <class T, int P, bool INTER, int U>
+__device__ __forceinline__ void turn(const T* x, int64_t xs, T* y, int64_t ys, int half,
+                                     const float (&c)[P], const float (&s)[P]) {
     if constexpr (INTER) {
-        Vec<T, 2 * P> v = load_vec<T, 2 * P>(x);
+        Vec<T, 2 * P> v[U];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float a = to_f32(v.e[2 * i]), b = to_f32(v.e[2 * i + 1]);
-            v.e[2 * i] = from_f32<T>(a * c[i] - b * s[i]);
-            v.e[2 * i + 1] = from_f32<T>(b * c[i] + a * s[i]);
+        for (int u = 0; u < U; ++u) v[u] = load_vec<T, 2 * P>(x + u * xs);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float a = to_f32(v[u].e[2 * i]), b = to_f32(v[u].e[2 * i + 1]);
+                v[u].e[2 * i] = from_f32<T>(a * c[i] - b * s[i]);
+                v[u].e[2 * i + 1] = from_f32<T>(b * c[i] + a * s[i]);
+            }
+            store_vec<T, 2 * P>(y + u * ys, v[u]);
         }
-        store_vec<T, 2 * P>(y, v);
     } else {
-        Vec<T, P> u = load_vec<T, P>(x), v = load_vec<T, P>(x + half);
+        Vec<T, P> v[U], w[U];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float a = to_f32(u.e[i]), b = to_f32(v.e[i]);
-            u.e[i] = from_f32<T>(a * c[i] - b * s[i]);
-            v.e[i] = from_f32<T>(b * c[i] + a * s[i]);
+        for (int u = 0; u < U; ++u) {
+            v[u] = load_vec<T, P>(x + u * xs);
+            w[u] = load_vec<T, P>(x + u * xs + half);
         }
-        store_vec<T, P>(y, u);
-        store_vec<T, P>(y + half, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float a = to_f32(v[u].e[i]), b = to_f32(w[u].e[i]);
+                v[u].e[i] = from_f32<T>(a * c[i] - b * s[i]);
+                w[u].e[i] = from_f32<T>(b * c[i] + a * s[i]);
+            }
+            store_vec<T, P>(y + u * ys, v[u]);
+            store_vec<T, P>(y + u * ys + half, w[u]);
+        }
     }
 }
 
@@ -81,12 +95,14 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int64_t first
         s[i] *= a.inverse ? -a.amplitude : a.amplitude;
     }
     const int at_x = INTER ? 2 * p0 : p0;
-    int h = h0;
-    for (; h + 1 < h1; h += 2) {  // two heads in flight
-        turn<T, P, INTER>(x + h * a.x_h + at_x, y + h * a.o_h + at_x, half, c, s);
-        turn<T, P, INTER>(x + (h + 1) * a.x_h + at_x, y + (h + 1) * a.o_h + at_x, half, c, s);
-    }
-    if (h < h1) turn<T, P, INTER>(x + h * a.x_h + at_x, y + h * a.o_h + at_x, half, c, s);
+    x += h0 * a.x_h + at_x;
+    y += h0 * a.o_h + at_x;
+    int left = h1 - h0;
+    constexpr int U = 4;
+    for (; left >= U; left -= U, x += U * a.x_h, y += U * a.o_h)
+        turn<T, P, INTER, U>(x, a.x_h, y, a.o_h, half, c, s);
+    for (; left > 0; --left, x += a.x_h, y += a.o_h)
+        turn<T, P, INTER, 1>(x, a.x_h, y, a.o_h, half, c, s);
 }
 
 template <class T, int P>

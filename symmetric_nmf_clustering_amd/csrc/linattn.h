@@ -580,6 +580,10 @@ hipError_t launch_attend_walk(const AttendArgs& a, bool maps, hipStream_t st) {
         dx = a.run[r].dx > dx ? a.run[r].dx : dx;
         dz = a.run[r].dz > dz ? a.run[r].dz : dz;
     }
+    // a CU with one workgroup alone: eight waves with one column tile each rather than four
+    // with two (gradient of 4 x 2048 steps of 16 heads, 192 workgroups: 131 us against 145; two
+    // workgroups a CU, 512 for 32768 steps of 16 heads: 238 against 220)
+    const bool few = a.batch * a.heads * a.nseg * a.nrun <= 256;
     // small heads: two waves hold all columns of z; wide ones: two column tiles a wave, which
     // share what it reads of x and y
 #define SYMNMF_WALK(DX, NW, WN) \
@@ -594,6 +598,8 @@ hipError_t launch_attend_walk(const AttendArgs& a, bool maps, hipStream_t st) {
     if (dx <= 96 && dz <= 64) SYMNMF_WALK(96, 4, 1);
     if (dx <= 96) SYMNMF_WALK(96, 4, W);
     if (dx <= 128 && dz <= 64) SYMNMF_WALK(128, 4, 1);
+    if constexpr (W == 2)
+        if (dx <= 128 && few) SYMNMF_WALK(128, 8, 1);
     if (dx <= 128) SYMNMF_WALK(128, 4, W);
     SYMNMF_WALK(256, 4, 1);
 #undef SYMNMF_WALK
