@@ -12,48 +12,40 @@ namespace symnmf {
 
 namespace {
 
-// P pairs next to one another, of U heads: all asked for before the first is turned.
-template <class T, int P, bool INTER, int U>
-__device__ __forceinline__ void turn(const T* x, int64_t xs, T* y, int64_t ys, int half,
+// P pairs of each of U heads, all asked for before the first is turned: (CLOSE) 2 P elements
+// at x, or P at x and P at x + gap. copy: they stay as they are (0 times an infinity would
+// not).
+template <class T, int P, bool CLOSE, int U>
+__device__ __forceinline__ void turn(const T* x, int64_t xs, T* y, int64_t ys, int gap, bool copy,
                                      const float (&c)[P], const float (&s)[P]) {
-    if constexpr (INTER) {
-        Vec<T, 2 * P> v[U];
+    constexpr int V = CLOSE ? 2 * P : P;
+    Vec<T, V> v[U], w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) v[u] = load_vec<T, 2 * P>(x + u * xs);
+    for (int u = 0; u < U; ++u) {
+        v[u] = load_vec<T, V>(x + u * xs);
+        if (!CLOSE) w[u] = load_vec<T, V>(x + u * xs + gap);
+    }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float a = to_f32(v[u].e[2 * i]), b = to_f32(v[u].e[2 * i + 1]);
-                v[u].e[2 * i] = from_f32<T>(a * c[i] - b * s[i]);
-                v[u].e[2 * i + 1] = from_f32<T>(b * c[i] + a * s[i]);
-            }
-            store_vec<T, 2 * P>(y + u * ys, v[u]);
+        for (int i = 0; i < P; ++i) {
+            T& p = CLOSE ? v[u].e[2 * i] : v[u].e[i];
+            T& q = CLOSE ? v[u].e[(2 * i + 1) % V] : w[u].e[i];
+            const float a = to_f32(p), b = to_f32(q);
+            const T pt = from_f32<T>(a * c[i] - b * s[i]), qt = from_f32<T>(b * c[i] + a * s[i]);
+            p = copy ? p : pt;
+            q = copy ? q : qt;
         }
-    } else {
-        Vec<T, P> v[U], w[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            v[u] = load_vec<T, P>(x + u * xs);
-            w[u] = load_vec<T, P>(x + u * xs + half);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                const float a = to_f32(v[u].e[i]), b = to_f32(w[u].e[i]);
-                v[u].e[i] = from_f32<T>(a * c[i] - b * s[i]);
-                w[u].e[i] = from_f32<T>(b * c[i] + a * s[i]);
-            }
-            store_vec<T, P>(y + u * ys, v[u]);
-            store_vec<T, P>(y + u * ys + half, w[u]);
-        }
+        store_vec<T, V>(y + u * ys, v[u]);
+        if (!CLOSE) store_vec<T, V>(y + u * ys + gap, w[u]);
     }
 }
 
-// A thread: one step, `per` of its heads, and one group of P pairs (or, past the pairs,
-// 2 P channels that stay as they are). Threads of a step lie next to one another.
-template <class T, int P, bool INTER>
+// A thread: one step, `per` of its heads, and one group of P pairs or, past those, 2 P
+// channels that stay (one or two for P = 1). Threads of a step lie next to one another, and
+// all take the same path. Four heads in flight: 107 us for 32768 steps of 32 heads of 128
+// bf16 (5.0 TB/s, the copy's rate) against 118 with two.
+template <class T, int P, bool CLOSE>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int64_t first, int groups,
                                                      int splits, int per) {
     const int64_t id = (first + blockIdx.x) * 256 + threadIdx.x;
@@ -63,46 +55,39 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int64_t first
     const int64_t n = rest / splits;
     if (n >= a.batch * a.steps) return;
     const int64_t b = n / a.steps, t = n % a.steps;
-    const int half = a.dims / 2, turned = half / P;
-    const T* x = static_cast<const T*>(a.x) + b * a.x_b + t * a.x_t;
-    T* y = static_cast<T*>(a.out) + b * a.o_b + t * a.o_t;
-    const int h0 = split * per;
-    int h1 = h0 + per;
-    if (h1 > a.heads) h1 = a.heads;
-    if (grp >= turned) {
-        const int c = a.dims + (grp - turned) * 2 * P;
-        for (int h = h0; h < h1; ++h) {
-            if (c + 2 * P <= a.width) {
-                store_vec<T, 2 * P>(y + h * a.o_h + c, load_vec<T, 2 * P>(x + h * a.x_h + c));
-            } else {
-                for (int i = c; i < a.width; ++i) y[h * a.o_h + i] = x[h * a.x_h + i];
-            }
-        }
-        return;
-    }
-    const int64_t at = b * a.pos_b + t * a.pos_t;
-    const double pos = a.pos_type == kI32 ? (double)static_cast<const int32_t*>(a.pos)[at]
-                                          : (double)static_cast<const int64_t*>(a.pos)[at];
-    const int p0 = grp * P;
+    const int half = a.dims / 2, turned = half / P, p0 = grp * P;
+    const bool copy = grp >= turned;
+    int at = a.interleaved ? 2 * p0 : p0, gap = a.interleaved ? P : half;
     float c[P], s[P];
+    if (copy) {
+        at = 2 * p0;  // dims = 2 P turned
+        gap = at + P < a.width ? P : 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        constexpr double kTurn = 0.15915494309189533577;  // 1 / 2 pi
-        const double turns = pos * a.freqs[p0 + i] * kTurn;
-        const float f = (float)(turns - rint(turns));
-        sincospif(2.f * f, &s[i], &c[i]);
-        c[i] *= a.amplitude;
-        s[i] *= a.inverse ? -a.amplitude : a.amplitude;
+        for (int i = 0; i < P; ++i) c[i] = s[i] = 0.f;
+    } else {
+        const int64_t pa = b * a.pos_b + t * a.pos_t;
+        const double pos = a.pos_type == kI32 ? (double)static_cast<const int32_t*>(a.pos)[pa]
+                                              : (double)static_cast<const int64_t*>(a.pos)[pa];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            constexpr double kTurn = 0.15915494309189533577;  // 1 / 2 pi
+            const double turns = pos * a.freqs[p0 + i] * kTurn;
+            const float f = (float)(turns - rint(turns));
+            sincospif(2.f * f, &s[i], &c[i]);
+            c[i] *= a.amplitude;
+            s[i] *= a.inverse ? -a.amplitude : a.amplitude;
+        }
     }
-    const int at_x = INTER ? 2 * p0 : p0;
-    x += h0 * a.x_h + at_x;
-    y += h0 * a.o_h + at_x;
-    int left = h1 - h0;
+    const int h0 = split * per;
+    int left = a.heads - h0;
+    if (left > per) left = per;
+    const T* x = static_cast<const T*>(a.x) + b * a.x_b + t * a.x_t + h0 * a.x_h + at;
+    T* y = static_cast<T*>(a.out) + b * a.o_b + t * a.o_t + h0 * a.o_h + at;
     constexpr int U = 4;
     for (; left >= U; left -= U, x += U * a.x_h, y += U * a.o_h)
-        turn<T, P, INTER, U>(x, a.x_h, y, a.o_h, half, c, s);
+        turn<T, P, CLOSE, U>(x, a.x_h, y, a.o_h, gap, copy, c, s);
     for (; left > 0; --left, x += a.x_h, y += a.o_h)
-        turn<T, P, INTER, 1>(x, a.x_h, y, a.o_h, half, c, s);
+        turn<T, P, CLOSE, 1>(x, a.x_h, y, a.o_h, gap, copy, c, s);
 }
 
 template <class T, int P>
@@ -117,17 +102,20 @@ hipError_t rotary_as(const RotaryArgs& a, hipStream_t st) {
     splits = (a.heads + per - 1) / per;
     const int64_t blocks = (n * splits + 255) / 256;
     return in_launches(blocks, [&](int64_t first, unsigned k) {
-        if (a.interleaved)
-            rotary_kernel<T, P, true><<<k, 256, 0, st>>>(a, first, groups, (int)splits, per);
+        if (P > 1 && a.interleaved)
+            rotary_kernel<T, P, (P > 1)><<<k, 256, 0, st>>>(a, first, groups, (int)splits, per);
         else
             rotary_kernel<T, P, false><<<k, 256, 0, st>>>(a, first, groups, (int)splits, per);
     });
 }
 
+// 16 bytes of neighbouring pairs, or twice 8 of pairs apart, where dims and the rest of the
+// width allow it.
 template <class T>
 hipError_t rotary_type(const RotaryArgs& a, hipStream_t st) {
-    constexpr int P = 8 / sizeof(T);  // 16 bytes of interleaved pairs, twice 8 of halves
-    return a.dims / 2 % P == 0 ? rotary_as<T, P>(a, st) : rotary_as<T, 1>(a, st);
+    constexpr int P = 8 / sizeof(T);
+    return a.dims / 2 % P == 0 && (a.width - a.dims) % (2 * P) == 0 ? rotary_as<T, P>(a, st)
+                                                                    : rotary_as<T, 1>(a, st);
 }
 
 }  // namespace
