@@ -140,6 +140,7 @@ AttendArgs common(const AttendCall& c, int runs) {
     a.lengths = c.lengths;
     a.type = c.d.type;
     a.heads = c.d.heads;
+    a.group = c.d.heads / c.d.kv_heads;
     a.batch = c.d.batch;
     a.steps = c.d.steps;
     a.nseg = (int32_t)plan_segments(c.d, runs, &a.seg_len);

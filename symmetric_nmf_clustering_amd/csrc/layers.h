@@ -40,6 +40,7 @@ struct AttendArgs {
     const float* decay;      // heads: ln a
     const int32_t* lengths;  // nullable
     int32_t type, heads, nseg;
+    int32_t group;  // neighbouring heads that read the same rows: walked on one XCD
     int64_t batch, steps, seg_len;
 };
 

@@ -276,25 +276,30 @@ __device__ __forceinline__ void put_out(O* p, const floatx4& v, int cols) {
 // blockIdx.x (+ first): column tile, segment and head; blockIdx.y: the run.
 template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
-    AttendArgs a, int64_t first, int64_t items, int ztiles) {
+    AttendArgs a, int64_t first, int64_t units, int ztiles) {
     using Z = WalkSizes<T, DX, NW, WN, OUT, WIDE>;
     constexpr int C = Z::C, NP = Z::NP, NX = DX / 16, NB = C / 16;
     constexpr int XS = Z::TX::STRIDE, YS = Z::TY::STRIDE, ZS = Z::TZ::STRIDE;
     constexpr int XP = Z::TX::PLANE, YP = Z::TY::PLANE, ZP = Z::TZ::PLANE;
     __shared__ alignas(16) typename Z::Lds lds;
 
-    // items go round the XCDs; the column tiles of one item to the same XCD, whose L2
-    // then has x and y for all of them
-    const int64_t id = first + blockIdx.x;
-    const int64_t grp = id >> 3;
-    const int zt = (int)(grp % ztiles);
-    const int64_t item = (grp / ztiles) + (id & 7) * ((items + 7) >> 3);
-    if (grp / ztiles >= ((items + 7) >> 3) || item >= items) return;
+    // Workgroups go round the XCDs. An XCD takes whole units, the column tiles and the heads
+    // that share rows of one segment, whose L2 then serves them all: neighbouring units, or,
+    // where batch rows have lengths, every eighth one, so that the XCDs are loaded alike.
+    const int64_t id = first + blockIdx.x, mine = id >> 3, each = (units + 7) >> 3;
+    const int zt = (int)(mine % ztiles);
+    const int64_t at_head = mine / ztiles, nth = at_head / a.group;
+    const int64_t unit = a.lengths ? nth * 8 + (id & 7) : (id & 7) * each + nth;
+    if (nth >= each || unit >= units) return;
     const AttendRun R = a.run[blockIdx.y];
-    const int seg = (int)(item % a.nseg);
-    const int64_t bh = item / a.nseg;
-    const int64_t b = bh / a.heads;
-    const int head = (int)(bh % a.heads);
+    const int shared = a.heads / a.group;
+    const int64_t row = unit / a.nseg, b = row / shared;
+    const int head = (int)(row % shared) * a.group + (int)(at_head % a.group);
+    // Workgroups 256 apart meet on a CU. Every other 256 take their segments from the last to
+    // the first: short batch rows have no steps in their last ones.
+    const bool turn = row * a.nseg * a.group * ztiles >> 8 & 1;
+    const int seg = turn ? a.nseg - 1 - (int)(unit % a.nseg) : (int)(unit % a.nseg);
+    const int64_t bh = b * a.heads + head;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
     const int z0 = zt * Z::ZC, zw = z0 + wave * 16 * WN;
     if (z0 >= R.dz) return;  // the whole workgroup
@@ -339,7 +344,8 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     for (int i = 0; i < NX; ++i)
 #pragma unroll
         for (int m = 0; m < WN; ++m) S[i][m] = floatx4{0.f, 0.f, 0.f, 0.f};
-    if constexpr (OUT) {
+    const bool last = seg == a.nseg - 1;
+    if (OUT && (u_begin < len || last)) {  // (others clear their steps alone)
         const int64_t D = (int64_t)R.dx * R.dz;
         const bool cut = a.nseg > 1;  // the join has left the segment's state in its slot
         const float* s = cut ? R.seg + (bh * a.nseg + seg) * D : (R.s0 ? R.s0 + bh * D : nullptr);
@@ -362,7 +368,8 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
 
     if (WIDE && u_begin < u_stop) fetch(u_begin);
     // the tables of weights, from one table of powers
-    for (int i = threadIdx.x; i <= C; i += Z::NT) lds.pw[i] = (float)exp(gd * i);
+    if (u_begin < u_stop)
+        for (int i = threadIdx.x; i <= C; i += Z::NT) lds.pw[i] = (float)exp(gd * i);
     lds_barrier();
     for (int i = threadIdx.x; i < C; i += Z::NT) {
         lds.wz[i] = R.st_scale * lds.pw[C - R.in_pow - i];
@@ -514,15 +521,18 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     // steps past the length
     if constexpr (OUT) {
         const int64_t lo = u_begin > len ? u_begin : len;
-        const int64_t cells = u_end > lo ? (u_end - lo) * Z::ZC : 0;
-        for (int64_t i = threadIdx.x; i < cells; i += Z::NT) {
-            const int z = z0 + (int)(i % Z::ZC);
-            if (z >= R.dz) continue;
-            const int64_t e = ((b * a.steps + lo + i / Z::ZC) * a.heads + head) * R.dz + z;
-            if (R.out32)
-                static_cast<float*>(R.out)[e] = 0.f;
-            else
-                static_cast<T*>(R.out)[e] = from_f32<T>(0.f);
+        constexpr int V = WIDE ? 16 / sizeof(T) : 1, G = Z::ZC / V;
+        const int rows = u_end > lo ? (int)(u_end - lo) : 0;
+        const int z = z0 + threadIdx.x % G * V;  // (G divides the workgroup's threads)
+        if (z < R.dz) {
+            const int64_t e = ((b * a.steps + lo) * a.heads + head) * R.dz + z;
+            const int64_t es = (int64_t)a.heads * R.dz;
+            for (int row = threadIdx.x / G; row < rows; row += Z::NT / G) {
+                if (R.out32)
+                    store_vec<float, V>(static_cast<float*>(R.out) + e + row * es, Vec<float, V>{});
+                else
+                    store_vec<T, V>(static_cast<T*>(R.out) + e + row * es, Vec<T, V>{});
+            }
         }
     }
 
@@ -530,7 +540,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     int si = R.seg_i, sj = R.seg_j;
     if (!OUT) {
         s = R.seg + (bh * a.nseg + seg) * ((int64_t)R.dx * R.dz);
-    } else if (seg == a.nseg - 1 && R.s1) {
+    } else if (last && R.s1) {
         s = R.s1 + bh * ((int64_t)R.dx * R.dz);
         si = R.s1_i;
         sj = R.s1_j;
@@ -560,16 +570,16 @@ hipError_t attend_walk_as(const AttendArgs& a, hipStream_t st) {
                q.zt < kNearStride;
     }
     const int ztiles = (dz + ZC - 1) / ZC;
-    const int64_t items = a.batch * a.heads * a.nseg;
-    const int64_t blocks = (items + 7) / 8 * 8 * ztiles;
+    const int64_t units = a.batch * (a.heads / a.group) * a.nseg;
+    const int64_t blocks = (units + 7) / 8 * 8 * a.group * ztiles;
     return in_launches(blocks, [&](int64_t first, unsigned n) {
         const dim3 grid(n, (unsigned)a.nrun);
         if (wide)
             attend_walk_kernel<T, DX, NW, WN, OUT, true>
-                <<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
+                <<<grid, 64 * NW, 0, st>>>(a, first, units, ztiles);
         else
             attend_walk_kernel<T, DX, NW, WN, OUT, false>
-                <<<grid, 64 * NW, 0, st>>>(a, first, items, ztiles);
+                <<<grid, 64 * NW, 0, st>>>(a, first, units, ztiles);
     });
 }
 
