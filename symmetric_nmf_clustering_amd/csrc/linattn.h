@@ -167,8 +167,9 @@ struct Rows {
     int32_t reverse;
     int32_t d;        // columns
 };
-// WIDE tiles count a chunk's elements from its lowest row in 32 bits.
-constexpr int64_t kNearStride = int64_t(1) << 24;
+// WIDE tiles count a chunk's elements from its lowest row in 32 bits, with a product of signed
+// 24-bit factors.
+constexpr int64_t kNearStride = int64_t(1) << 23;
 
 // A chunk's C x COLS tile on its way from memory through registers to LDS, by NT
 // threads. Rows past n (at least 1) and columns past d are zeros. No access is
@@ -336,7 +337,8 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     };
     // the state at the segment's start
     floatx4 S[NX][WN];
-    auto element = [&](int i, int m, int r, int si, int sj) __attribute__((always_inline)) {  // where S[i][m][r] is, or -1
+    // where S[i][m][r] is, or -1
+    auto element = [&](int i, int m, int r, int si, int sj) __attribute__((always_inline)) {
         const int row = 16 * i + 4 * g + r, j = zw + 16 * m + l16;
         return row < R.dx && j < R.dz ? row * si + j * sj : -1;
     };

@@ -648,3 +648,57 @@ def test_binding_refusals():
     for kw in (dict(step=0), dict(lr=float("nan")), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1.0)):
         with pytest.raises(L.SymNMFError):
             api.adamw_step([p], [g], m32, v32, **{**dict(step=1), **kw})
+
+
+@pytest.mark.parametrize("far", [(1 << 23) - 8, 1 << 23, (1 << 23) + 8, (1 << 24) - 8, 1 << 24, (1 << 25) + 8])
+def test_far_steps(far):
+    """Steps far apart in memory, around where a walk's offsets change their arithmetic."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    T = 9
+    t, x = make(torch, "bf16", 1, T, 2, 2, 16, 16, 31)
+    buf = torch.zeros(4, far * (T - 1) + 32, dtype=torch.bfloat16, device="cuda")
+    v = {}
+    for i, name in enumerate(("q", "k", "v", "do")):
+        v[name] = torch.as_strided(buf, (1, T, 2, 16), (far * T, far, 16, 1), i * buf.shape[1])
+        v[name].copy_(t[name])
+    got = api.linear_attention(v["q"], v["k"], v["v"], t["decay"], state=t["state"])
+    want = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    kw = dict(dlast=t["dlast"], state=t["state"])
+    got = api.linear_attention_grad(v["q"], v["k"], v["v"], t["decay"], v["do"], **kw)
+    want = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp16", "fp32"])
+def test_lengths_over_many_heads(kind):
+    """Padded batches large enough to be cut, with shared heads, more batch rows than XCDs and more
+    workgroups than CUs: every row as when it is alone."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    B, T, H, G, d = 11, 520, 12, 4, 40
+    lengths = [520, 0, 1, 130, 519, 256, 64, 300, 5, 520, 128]
+    t, x = make(torch, kind, B, T, H, G, d, d, 41, lengths)
+    kw = dict(state=t["state"], lengths=t["lengths"])
+    got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], **kw)
+    grad = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"], **kw)
+    check_forward(got, x, kind, d ** -0.5)
+    check_grad(grad, x, kind, d ** -0.5)
+
+
+def test_two_streams_at_once():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    made = [make(torch, "bf16", 1, 3000, 2, 1, 64, 64, 50 + i)[0] for i in range(2)]
+    want = [api.linear_attention(t["q"], t["k"], t["v"], t["decay"]) for t in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, t in enumerate(made):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(api.linear_attention(t["q"], t["k"], t["v"], t["decay"]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
