@@ -709,11 +709,12 @@ def _head_rows(t: torch.Tensor, name: str, dims: int, like: Optional[torch.Tenso
     """(type code, strides of all but the last dimension) of rows of heads."""
     code = _seq_tensor(t, name, dtype=None if like is None else like.dtype,
                        device=None if like is None else like.device)
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
-    if t.shape[-1] > 1 and t.numel() and t.stride(-1) != 1:
+    strides = t.stride()
+    if len(strides) != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {len(strides)}")
+    if strides[-1] != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"{name} needs unit stride within a head")
-    return code, t.stride()[:-1]
+    return code, strides[:-1]
 
 
 def _attend_call(q, k, v, decay, scale, do=None):
@@ -763,12 +764,10 @@ def _bytes_scratch(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
-def _dense(shape, dtype, device) -> torch.Tensor:
-    strides, n = [], 1
-    for size in reversed(shape):
-        strides.append(n)
-        n *= max(size, 1)
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=device)
+def _heads_out(batch: int, steps: int, heads: int, width: int, dtype, device) -> torch.Tensor:
+    return torch.empty_strided((batch, steps, heads, width),
+                               (steps * heads * width, heads * width, width, 1), dtype=dtype,
+                               device=device)
 
 
 def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
@@ -789,8 +788,8 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
     shape = (desc.batch, desc.heads, desc.dk, desc.dv)
     lengths_p = _lengths_ptr(lengths, desc.batch, dev)
     state_p = _state_ptr(state, "state", shape, dev)
-    o = _dense((desc.batch, desc.steps, desc.heads, desc.dv), q.dtype, dev)
-    last = _dense(shape, torch.float32, dev)
+    o = _heads_out(desc.batch, desc.steps, desc.heads, desc.dv, q.dtype, dev)
+    last = _heads_out(*shape, torch.float32, dev)
     ws = _bytes_scratch(nbytes, dev)
     st = L.load().symnmf_linear_attention(
         ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), lengths_p,
@@ -815,8 +814,8 @@ def linear_attention_grad(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dec
     lengths_p = _lengths_ptr(lengths, desc.batch, dev)
     state_p = _state_ptr(state, "state", shape, dev)
     dlast_p = _state_ptr(dlast, "dlast", shape, dev)
-    dq, dk, dv = (_dense(tuple(x.shape), q.dtype, dev) for x in (q, k, v))
-    dstate = _dense(shape, torch.float32, dev)
+    dq, dk, dv = (_heads_out(*x.shape, q.dtype, dev) for x in (q, k, v))
+    dstate = _heads_out(*shape, torch.float32, dev)
     ws = _bytes_scratch(nbytes, dev)
     st = L.load().symnmf_linear_attention_grad(
         ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), lengths_p,
@@ -841,9 +840,12 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dec
     if state is None:
         raise ValueError("state is needed")
     state_p = _state_ptr(state, "state", shape, dev)
-    new = _dense(shape, torch.float32, dev) if out_state is None else out_state
-    new_p = _state_ptr(new, "out_state", shape, dev)
-    o = _dense((desc.batch, desc.heads, desc.dv), q.dtype, dev)
+    if out_state is None:
+        new = _heads_out(*shape, torch.float32, dev)
+        new_p = new.data_ptr()
+    else:
+        new, new_p = out_state, _state_ptr(out_state, "out_state", shape, dev)
+    o = _steps_out(desc.batch, desc.heads, desc.dv, q.dtype, dev)
     st = L.load().symnmf_linear_attention_step(
         ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), state_p,
         o.data_ptr(), new_p, _here(dev))
@@ -910,14 +912,15 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout
     if not math.isfinite(amplitude):
         raise ValueError("amplitude must be finite")
     if out is None:
-        out = _dense(tuple(x.shape), x.dtype, dev)
-    elif out is not x:
+        out = (_heads_out if x.dim() == 4 else _steps_out)(*x.shape, x.dtype, dev)
+        os_ = out.stride()[:-1]
+    else:
         _seq_tensor(out, "out", dtype=x.dtype, shape=x.shape, device=dev)
-    os_ = _head_rows(out, "out", x.dim())[1]
-    if out.data_ptr() == x.data_ptr() and os_ != xs and x.numel():
-        raise ValueError("out shares x's memory in another layout")
-    if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())) and x.numel():
-        raise ValueError("out has overlapping rows")
+        os_ = _head_rows(out, "out", x.dim())[1]
+        if out.data_ptr() == x.data_ptr() and os_ != xs and x.numel():
+            raise ValueError("out shares x's memory in another layout")
+        if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())) and x.numel():
+            raise ValueError("out has overlapping rows")
     ps = positions.stride()
     if x.dim() == 3:
         batch, steps, xs, os_, ps = 1, x.shape[0], (0, *xs), (0, *os_), (0, *ps)
@@ -994,35 +997,45 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
     dev = params[used[0]].device
     held = []  # dense copies live until the launch is made
     groups: dict = {}
-    seen = set()
+    written = []
+    state_type, state_types = (torch.float8_e4m3fn, _CODES) if low else (torch.float32, _FULL)
+
+    def fits(x, name, dtype, types, shape):
+        # (the quick test first: a step checks some hundred tensors)
+        if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.shape != shape or x.device != dev:
+            _seq_tensor(x, name, types, shape=shape, device=dev)
+        if not x.is_contiguous():
+            raise ValueError("params and states must be contiguous")
+        return x.data_ptr()
+
     for i in used:
         p, g = params[i], grads[i]
-        key = (_seq_tensor(p, "params", device=dev), _seq_tensor(g, "grads", shape=p.shape, device=dev))
+        shape = p.shape
+        pt = _seq_tensor(p, "params", device=dev)
+        gt = _seq_tensor(g, "grads", device=dev)
+        if g.shape != shape:
+            raise ValueError(f"grads must have shape {tuple(shape)}, not {tuple(g.shape)}")
         if not g.is_contiguous():
             g = g.contiguous()
             held.append(g)
-        written = [p, m[i], v[i]]
-        for name, x in (("m", m[i]), ("v", v[i])):
-            _seq_tensor(x, name, _CODES if low else _FULL, shape=p.shape, device=dev)
-        if masters is not None:
-            _seq_tensor(masters[i], "masters", _FULL, shape=p.shape, device=dev)
-            written.append(masters[i])
         n = p.numel()
+        at = [fits(p, "params", p.dtype, _DTYPES, shape), fits(m[i], "m", state_type, state_types, shape),
+              fits(v[i], "v", state_type, state_types, shape)]
+        ms = vs = master = None
+        if masters is not None:
+            master = fits(masters[i], "masters", torch.float32, _FULL, shape)
+            at.append(master)
         if low:
-            for name, x in (("m_scale", m_scale[i]), ("v_scale", v_scale[i])):
-                _seq_tensor(x, name, _FULL, shape=(-(-n // L.ADAM_BLOCK),), device=dev)
-            written += [m_scale[i], v_scale[i]]
+            blocks = (-(-n // L.ADAM_BLOCK),)
+            ms = fits(m_scale[i], "m_scale", torch.float32, _FULL, blocks)
+            vs = fits(v_scale[i], "v_scale", torch.float32, _FULL, blocks)
+            at += [ms, vs]
         if n == 0:
             continue
-        at = [x.data_ptr() for x in written]
-        if not all(x.is_contiguous() for x in written):
-            raise ValueError("params and states must be contiguous")
-        if len(seen.union(at)) != len(seen) + len(at):
-            raise ValueError("two of the tensors share memory")
-        seen.update(at)
-        groups.setdefault(key, []).append(
-            (at[0], g.data_ptr(), at[1], at[2], at[-2] if low else None, at[-1] if low else None,
-             at[3] if masters is not None else None, n))
+        written += at
+        groups.setdefault((pt, gt), []).append((at[0], g.data_ptr(), at[1], at[2], ms, vs, master, n))
+    if len(set(written)) != len(written):
+        raise ValueError("two of the tensors share memory")
     step, step_p = _device_scalar(step, "step", torch.int64, dev)
     lr, lr_p = _device_scalar(lr, "lr", torch.float32, dev)
     grad_scale, scale_p = _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
