@@ -11,9 +11,14 @@
 // rounded. Every block's largest element is held to float32, so that all of a block
 // decays with it; a code that is off by half a step puts a root at most 2^-4 off.
 //
+// Arithmetic is float32: about one code in 10^6 lies on the other side of a rounding's
+// border than in float64 (through float64 the 8-bit step takes 284 us instead of 228).
+//
 // Bound by memory: a workgroup takes 2048 elements of one tensor, a thread 8 that lie
 // next to one another; 32 lanes share an 8-bit block. Which tensor is found from the
-// tensors' first workgroups, in the kernel's arguments.
+// tensors' first workgroups, in the kernel's arguments. 108 million parameters: bf16 with
+// float32 masters and states (28 bytes each) 622 us, 4.8 TB/s; bf16 with 8-bit states (10
+// bytes) 220 us, 4.9 TB/s.
 #include "layers.h"
 
 namespace symnmf {
