@@ -13,7 +13,7 @@
 // come out transposed (a lane has 4 columns of one step): 8 or 16 bytes a store. P alone
 // passes through LDS, in the order its reader's lanes want it. Whole chunks and a last,
 // shorter one are two copies of the loop's body: bounds in the common one cost registers
-// that spill. The next chunk's rows are asked for before the state's update.
+// that spill. The next chunk's rows are asked for as soon as this one's are in LDS.
 //
 // What bounds it (bf16, heads of 128): with two workgroups a CU, issue. Of a SIMD's cycles
 // matrix products take 29%, other vector operations 33%, and the waves wait for LDS and
@@ -49,7 +49,7 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Planes of an element type, and steps of a chunk.
+// Planes of an element type, and steps of a chunk (at most).
 template <class T>
 struct Planes {
     static constexpr int N = 3, C = 32;
@@ -244,7 +244,9 @@ struct Tile {
 
 template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
-    static constexpr int C = Planes<T>::C, NP = Planes<T>::N;
+    // 64 steps of two column tiles a wave leave no registers to ask for the next chunk's rows
+    // early; 32 do (4 x 4096 x 32 heads of 128 bf16: 179 us against 190)
+    static constexpr int C = WN == 2 ? 32 : Planes<T>::C, NP = Planes<T>::N;
     static constexpr int NT = 64 * NW, ZC = 16 * WN * NW;
     // pads of 16 bytes keep reads of rows off one another's banks, of 32 those down columns
     using TX = Tile<T, C, DX, NT, WIDE, 8>;
@@ -403,6 +405,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
         ry.template store<FULL>(lds.y, R.dx, n, 0);
         rz.template store<FULL>(lds.z, R.dz, n, z0);
         lds_barrier();
+        if (WIDE && u0 + C < u_stop) fetch(u0 + C);
 
         if constexpr (OUT) {
             // P^T in 16 x 16 blocks on and below the diagonal, shared out among the waves
@@ -487,7 +490,6 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             }
         }
 
-        if (WIDE && u0 + C < u_stop) fetch(u0 + C);  // (earlier, its registers are wanted above)
         // S <- a^n S + Y^T (w Z); rows of z past n are zeros
         const float an = FULL ? lds.pw[C] : lds.pw[n];
 #pragma unroll
