@@ -17,8 +17,8 @@
 //
 // What bounds it (bf16, heads of 128): with two workgroups a CU, issue. Of a SIMD's cycles
 // matrix products take 29%, other vector operations 33%, and the waves wait for LDS and
-// barriers in a third of theirs. 32 x 2048 steps of 16 heads: 255 us, 4.2 TB/s; alone on its
-// CU a workgroup takes 4 us a chunk (16 x 2048: 148 us).
+// barriers in a third of theirs. 32 x 2048 steps of 16 heads: 245 us, 4.4 TB/s; alone on its
+// CU a workgroup takes 4 us for 64 steps (16 x 2048: 146 us).
 //
 // All products run on the bf16 matrix cores, on bf16 parts ("planes") of their operands
 // whose products are summed in float32:
