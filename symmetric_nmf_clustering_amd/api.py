@@ -845,6 +845,8 @@ def linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, dec
         new_p = new.data_ptr()
     else:
         new, new_p = out_state, _state_ptr(out_state, "out_state", shape, dev)
+        if 0 < abs(new_p - state_p) < 4 * state.numel():
+            raise ValueError("out_state overlaps state and is not the same")
     o = _steps_out(desc.batch, desc.heads, desc.dv, q.dtype, dev)
     st = L.load().symnmf_linear_attention_step(
         ctypes.byref(desc), q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), state_p,
@@ -894,7 +896,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout
     is read as it is). ``freqs`` (float64, see ``rotary_freqs``) turns the first 2 *
     len(freqs) channels as pairs: (i, i + len(freqs)) for layout "half", (2i, 2i + 1) for
     "interleaved"; the others stay. ``inverse`` turns back by the same ``amplitude``: the
-    gradient at x from the one at the result. ``out`` may be x."""
+    gradient at x from the one at the result. ``out`` may be x, or memory apart from it."""
     if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError("x must be a HIP device tensor, tokens x heads x width or batch x steps x "
                          "heads x width")
@@ -1006,7 +1008,9 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
             _seq_tensor(x, name, types, shape=shape, device=dev)
         if not x.is_contiguous():
             raise ValueError("params and states must be contiguous")
-        return x.data_ptr()
+        at = x.data_ptr()
+        written.append((at, at + x.numel() * x.element_size()))
+        return at
 
     for i in used:
         p, g = params[i], grads[i]
@@ -1019,23 +1023,24 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
             g = g.contiguous()
             held.append(g)
         n = p.numel()
-        at = [fits(p, "params", p.dtype, _DTYPES, shape), fits(m[i], "m", state_type, state_types, shape),
-              fits(v[i], "v", state_type, state_types, shape)]
+        pp = fits(p, "params", p.dtype, _DTYPES, shape)
+        mp = fits(m[i], "m", state_type, state_types, shape)
+        vp = fits(v[i], "v", state_type, state_types, shape)
         ms = vs = master = None
         if masters is not None:
             master = fits(masters[i], "masters", torch.float32, _FULL, shape)
-            at.append(master)
         if low:
             blocks = (-(-n // L.ADAM_BLOCK),)
             ms = fits(m_scale[i], "m_scale", torch.float32, _FULL, blocks)
             vs = fits(v_scale[i], "v_scale", torch.float32, _FULL, blocks)
-            at += [ms, vs]
-        if n == 0:
-            continue
-        written += at
-        groups.setdefault((pt, gt), []).append((at[0], g.data_ptr(), at[1], at[2], ms, vs, master, n))
-    if len(set(written)) != len(written):
-        raise ValueError("two of the tensors share memory")
+        if n:
+            groups.setdefault((pt, gt), []).append((pp, g.data_ptr(), mp, vp, ms, vs, master, n))
+    written.sort()
+    end = 0
+    for at, to in written:  # (empty tensors' ranges are empty)
+        if at < end and at < to:
+            raise ValueError("two of the tensors share memory")
+        end = max(end, to)
     step, step_p = _device_scalar(step, "step", torch.int64, dev)
     lr, lr_p = _device_scalar(lr, "lr", torch.float32, dev)
     grad_scale, scale_p = _device_scalar(grad_scale, "grad_scale", torch.float32, dev)

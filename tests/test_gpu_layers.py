@@ -702,3 +702,52 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+def test_many_rows(kind):
+    """More batch rows than a grid's smaller dimensions take, and heads past a CU's: each row as
+    when a few of them are alone."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    for B, T, H, G, d in ((70000, 2, 1, 1, 8), (3, 3, 600, 200, 16)):
+        g = torch.Generator(device="cuda").manual_seed(B)
+        dt = types(torch)[kind]
+        q, k, v, do = (torch.randn(B, T, h, d, generator=g, device="cuda").to(dt) for h in (H, G, G, H))
+        state, dlast = (torch.randn(B, H, d, d, generator=g, device="cuda") for _ in range(2))
+        decay = -torch.rand(H, generator=g, device="cuda")
+        lengths = torch.randint(0, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+
+        def run(at):
+            a = [x[at].contiguous() for x in (q, k, v)]
+            o = api.linear_attention(*a, decay, state=state[at], lengths=lengths[at].contiguous())
+            gr = api.linear_attention_grad(*a, decay, do[at], dlast=dlast[at], state=state[at],
+                                           lengths=lengths[at].contiguous())
+            st = api.linear_attention_step(*(x[:, 0] for x in a), decay, state[at])
+            return *o, *gr, *st
+
+        whole = run(slice(None))
+        some = torch.tensor([0, B // 2, B - 1], device="cuda")
+        for x, y in zip(whole, run(some)):
+            assert torch.equal(x[some], y)
+
+
+def test_overlapping_memory_is_refused():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    buf = torch.zeros(4, 2, 8, 8, device="cuda")
+    q = torch.ones(3, 2, 8, device="cuda")
+    decay = torch.zeros(2, device="cuda")
+    with pytest.raises(ValueError, match="overlaps"):
+        api.linear_attention_step(q, q, q, decay, buf[:3], out_state=buf[1:])
+    _, same = api.linear_attention_step(q, q, q, decay, buf[:3], out_state=buf[:3])
+    assert same.data_ptr() == buf.data_ptr()
+    flat = torch.zeros(100, device="cuda")
+    for params in ([flat[:60], flat[50:]], [flat, flat[99:]], [flat[10:20], flat]):
+        m, v, _, _ = api.adamw_states(params)
+        with pytest.raises(ValueError, match="share memory"):
+            api.adamw_step(params, [torch.ones_like(p) for p in params], m, v, 1)
+    params = [flat[:50], flat[50:], flat[:0]]  # neighbours in one buffer are apart
+    m, v, _, _ = api.adamw_states(params)
+    api.adamw_step(params, [torch.ones_like(p) for p in params], m, v, 1, lr=0.5, eps=0.0, weight_decay=0.0)
+    assert torch.allclose(flat, torch.full_like(flat, -0.5))
