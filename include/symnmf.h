@@ -484,7 +484,8 @@ typedef struct symnmf_attend_desc {
 } symnmf_attend_desc;
 
 /* Workspace of symnmf_linear_attention (gradient 0) and its gradient (1); 0 for
- * an invalid descriptor. */
+ * an invalid descriptor. 256 is the answer where none is touched: such calls may
+ * share one. */
 size_t symnmf_linear_attention_ws_bytes(const symnmf_attend_desc* d, int gradient);
 
 /* Linear attention with a decay for each head, per batch row and query head:

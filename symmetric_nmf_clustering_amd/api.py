@@ -756,6 +756,7 @@ def _attend_call(q, k, v, decay, scale, do=None):
 
 
 def _bytes_scratch(nbytes: int, device) -> torch.Tensor:
+    """As ``_scratch``, of a size asked for already."""
     if nbytes > 256:
         return torch.empty_strided((nbytes,), (1,), dtype=torch.uint8, device=device)
     ws = _no_scratch.get(device)

@@ -181,10 +181,12 @@ size_t part_bytes(const AttendDesc& d, int width) {
 
 }  // namespace
 
+// 256 says that the workspace is not touched (callers share one for all such calls), so a call
+// that does use it asks for more.
 size_t attend_ws_bytes(const AttendDesc& d, bool gradient) {
     const size_t n = gradient ? 2 * seg_bytes(d, 3) + part_bytes(d, d.dk) + part_bytes(d, d.dv)
                               : seg_bytes(d, 1);
-    return n ? n : 256;
+    return n == 0 ? 256 : (n < 512 ? 512 : n);
 }
 
 hipError_t launch_attend(const AttendCall& c, hipStream_t st) {

@@ -751,3 +751,32 @@ def test_overlapping_memory_is_refused():
     m, v, _, _ = api.adamw_states(params)
     api.adamw_step(params, [torch.ones_like(p) for p in params], m, v, 1, lr=0.5, eps=0.0, weight_decay=0.0)
     assert torch.allclose(flat, torch.full_like(flat, -0.5))
+
+
+def test_two_streams_of_small_heads():
+    """Calls whose segments' states are a few numbers have a workspace of their own too: many calls
+    at once on two streams, and a replayed graph beside them."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    for d, T in ((4, 512), (1, 4096), (2, 1024)):
+        made = [make(torch, "fp32", 1, T, 1, 1, d, d, 60 + i)[0] for i in range(3)]
+
+        def run(t):
+            return api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+
+        want = [run(t) for t in made]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            replayed = run(made[2])
+        got = [[], []]
+        for _ in range(30):
+            graph.replay()
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    got[i].append(run(made[i]))
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+        assert all(torch.equal(a, b) for a, b in zip(replayed, want[2]))

@@ -41,6 +41,16 @@ def test_workspace_sizes():
     assert f(desc(**long), 0) > 2 * 128 * 128 * 4
 
 
+@pytest.mark.parametrize("heads,d,steps", [(1, 4, 512), (2, 2, 1024), (1, 1, 4096), (1, 1, 512), (2, 3, 700)])
+def test_a_used_workspace_is_never_the_least(heads, d, steps):
+    """256 bytes stand for "not touched", and the binding's calls share them: a call that is cut in
+    time asks for more, however small its segments' states."""
+    f = L.load().symnmf_linear_attention_ws_bytes
+    small = dict(batch=1, heads=heads, kv_heads=heads, dk=d, dv=d)
+    assert f(desc(steps=steps, **small), 0) > 256 and f(desc(steps=steps, **small), 1) > 256
+    assert f(desc(steps=300, **small), 0) == 256 and f(desc(steps=300, **small), 1) == 256
+
+
 def test_linear_attention_refusals():
     f = L.load().symnmf_linear_attention
     good = [desc(), P, P, P, P, None, None, P, None, P, Z, None]
