@@ -665,14 +665,16 @@ hipError_t grad_vec(const ScanArgs& a, hipStream_t st) {
 }  // namespace
 
 // Two numbers per channel and time segment of the plan that has most (a plan that is
-// cut has as many segments whatever it is cut below).
+// cut has as many segments whatever it is cut below). 256 says that the workspace is not
+// touched, so a cut scan asks for more.
 size_t scan_ws_bytes(int64_t batch, int64_t steps, int64_t width) {
     int64_t nseg = 1;
     for (int v : {1, 2, 4}) {
         nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, kCut, kFill).nseg);
         nseg = std::max<int64_t>(nseg, plan(batch, steps, width, v, cut_grad(2), kFillGrad).nseg);
     }
-    return nseg > 1 ? 8 * (size_t)nseg * (size_t)batch * (size_t)width : 256;
+    const size_t n = 8 * (size_t)nseg * (size_t)batch * (size_t)width;
+    return nseg == 1 ? 256 : (n < 512 ? 512 : n);
 }
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t st) {

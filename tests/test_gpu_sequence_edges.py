@@ -411,3 +411,28 @@ def test_logit_gradient_of_near_and_far_rows_side_by_side(vocab, kind):
     wide.copy_(t)
     api.token_logprobs_grad(wide, dtok, f.lse, f.entropy, w, dentropy=q, out=wide)
     check_grad_anywhere(zv[full], tok[full], w[full], q[full], 1.0, wide[full], kind)
+
+
+@pytest.mark.parametrize("width,steps", [(8, 4096), (1, 65536)])
+def test_two_streams_of_narrow_scans(width, steps):
+    """Scans cut in time whose segments' numbers are few have a workspace of their own too."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    g = torch.Generator(device="cuda").manual_seed(width)
+    made = [[torch.randn(1, steps, width, generator=g, device="cuda") for _ in range(3)] for _ in range(2)]
+
+    def run(x, gate, dh):
+        h, last, states = api.gated_scan(x, gate, return_states=True)
+        return h, last, *api.gated_scan_grad(x, gate, states, dh)
+
+    want = [run(*m) for m in made]
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for i, m in enumerate(made):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(*m))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))

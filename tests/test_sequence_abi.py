@@ -31,6 +31,15 @@ def test_workspace_sizes():
         assert wb(op, n, k, T, None) == 0, (op, n, k, T)
 
 
+@pytest.mark.parametrize("width,batch,steps", [(8, 1, 4096), (1, 1, 65536), (2, 1, 32768), (1, 1, 32768)])
+def test_a_used_workspace_is_never_the_least(width, batch, steps):
+    """256 bytes stand for "not touched", and the binding's calls share them: a scan that is cut in
+    time asks for more, however few its channels."""
+    wb = L.load().symnmf_workspace_bytes
+    assert wb(L.OP_GATED_SCAN, width, batch, steps, None) > 256
+    assert wb(L.OP_GATED_SCAN, width, batch, 300, None) == 256
+
+
 def test_embed_refusals():
     f = L.load().symnmf_embed
     good = [P, 0, 10, 8, 8, P, 0, 4, 1.0, P, 0, 8, None]
