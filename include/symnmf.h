@@ -502,7 +502,8 @@ size_t symnmf_linear_attention_ws_bytes(const symnmf_attend_desc* d, int gradien
  * precision whatever the type (for bfloat16, what o takes from within a chunk
  * and from the state passes through one more rounding to bfloat16). Elements
  * must be finite: an infinite or NaN one may make all of its chunk (64 steps)
- * and what follows NaN. The same bits on every call.
+ * and what follows NaN. (A dot product of finite q_t and k_s that overflows counts
+ * only where s <= t and their weight is not 0.) The same bits on every call.
  * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
 int symnmf_linear_attention(const symnmf_attend_desc* d, const void* q, const void* k,
                             const void* v, const float* decay, const int32_t* lengths,

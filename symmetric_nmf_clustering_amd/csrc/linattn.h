@@ -396,6 +396,19 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             reinterpret_cast<uint32_t*>(lds.p)[i] = 0;
     }
 
+    constexpr int BLOCKS = NB * (NB + 1) / 2, MINE = (BLOCKS + NW - 1) / NW;
+    // of a lane's 4 values of its blocks of P, two by two: all bits of those on and below the
+    // diagonal
+    uint32_t keep[OUT ? MINE : 1][2];
+    if constexpr (OUT)
+#pragma unroll
+        for (int q = 0; q < MINE; ++q) {
+            const int at = wave + q * NW, row = l16 - 4 * g;
+            const bool below = at != 0 && at != 2 && at != 5 && at != 9;
+            keep[q][0] = below || row > 0 ? ~0u : (row == 0 ? 0xffffu : 0u);
+            keep[q][1] = below || row > 2 ? ~0u : (row == 2 ? 0xffffu : 0u);
+        }
+
     // A chunk of n steps from u0; FULL: n = C.
     auto chunk = [&](auto full, int64_t u0, int n) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
@@ -409,7 +422,6 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
 
         if constexpr (OUT) {
             // P^T in 16 x 16 blocks on and below the diagonal, shared out among the waves
-            constexpr int BLOCKS = NB * (NB + 1) / 2, MINE = (BLOCKS + NW - 1) / NW;
 #pragma unroll
             for (int q = 0; q < MINE; ++q) {
                 const int at = wave + q * NW;
@@ -424,14 +436,17 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                                   read_rows<NP>(px + 32 * k, XP, g), acc);
                 const f32x4 wp = *reinterpret_cast<const f32x4*>(lds.wp + ((bu - bw) * 64 + lane) * 4);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[r] *= wp[r];
+                for (int r = 0; r < 4; ++r) {
+                    acc[r] *= wp[r];
+                    if (!FULL) acc[r] = wp[r] == 0.f ? 0.f : acc[r];
+                }
                 uint32_t p0[NP], p1[NP];
                 split_pair<NP>(acc[0], acc[1], p0);
                 split_pair<NP>(acc[2], acc[3], p1);
 #pragma unroll
                 for (int j = 0; j < NP; ++j)
                     *reinterpret_cast<uint2*>(lds.p + j * C * C + ((bu * NB + bw) * 64 + lane) * 4) =
-                        uint2{p0[j], p1[j]};
+                        uint2{p0[j] & keep[q][0], p1[j] & keep[q][1]};
             }
             lds_barrier();
         }
@@ -464,6 +479,9 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                 const float wx = lds.wx[16 * bu + l16];
 #pragma unroll
                 for (int m = 0; m < WN; ++m) acc[m] *= wx;
+                if (!FULL && wx == 0.f)
+#pragma unroll
+                    for (int m = 0; m < WN; ++m) acc[m] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int k = 0; k <= bu / 2; ++k) {
                     // (a lane's 4 values of a block lie at lane * 4; those of the next block
@@ -525,9 +543,19 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             }
         }
     };
+    // Steps without weight for one another (the later of a pair, or far apart under a strong
+    // decay) may overflow in their product, which is cleared, not multiplied by 0. Below the
+    // diagonal a weight is 0 only where the least one is: such a head takes the copy with bounds
+    // for all chunks, which looks at each weight.
+    bool faint = false;
+    if (OUT && u_begin < u_stop) {
+        const float least = fminf(lds.pw[C], 1.f);
+        faint = R.p_scale * least == 0.f || R.in_scale * least == 0.f;
+    }
     int64_t u0 = u_begin;
-    for (; u0 + C <= u_stop; u0 += C) chunk(std::true_type{}, u0, C);
-    if (u0 < u_stop) chunk(std::false_type{}, u0, (int)(u_stop - u0));
+    if (!faint)
+        for (; u0 + C <= u_stop; u0 += C) chunk(std::true_type{}, u0, C);
+    for (; u0 < u_stop; u0 += C) chunk(std::false_type{}, u0, (int)min(u_stop - u0, (int64_t)C));
 
     // steps past the length
     if constexpr (OUT) {
