@@ -888,6 +888,59 @@ def rotary_freqs(dims: int, base: float = 10000.0, scaling: str = "none", factor
     return f.to(device), amplitude
 
 
+def _reaches(terms, target: int, left: list) -> bool:
+    """Whether the sum of c * stride over ``terms`` (stride, least c, greatest c; strides falling)
+    can be ``target``. Where ``left[0]`` tries do not tell, True."""
+    if not terms:
+        return target == 0
+    left[0] -= 1
+    if left[0] < 0:
+        return True
+    (s, lo, hi), rest = terms[0], terms[1:]
+    least, most = sum(t * a for t, a, _ in rest), sum(t * b for t, _, b in rest)
+    return any(_reaches(rest, target - c * s, left)
+               for c in range(max(lo, -((most - target) // s)), min(hi, (target - least) // s) + 1))
+
+
+@functools.lru_cache(maxsize=1024)
+def _elements_apart(shape, strides) -> bool:
+    """Whether no two elements of a view lie at one address."""
+    if 0 in shape:
+        return True
+    dims = sorted(((st, n) for n, st in zip(shape, strides) if n > 1), reverse=True)
+    if dims and dims[-1][0] == 0:
+        return False
+    for i, (s, n) in enumerate(dims):
+        span = sum(t * (m - 1) for t, m in dims[i + 1:])
+        if s > span:
+            continue
+        rest = [(t, 1 - m, m - 1) for t, m in dims[i + 1:]]
+        if any(_reaches(rest, c * s, [1000]) for c in range(1, min(n - 1, span // s) + 1)):
+            return False
+    return True
+
+
+def _share(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether two views of one type have an element at one address. Views that pass through one
+    another's rows, as slices of one projection do, need not."""
+    if not (a.numel() and b.numel()):
+        return False
+    size = a.element_size()
+    at, to = a.data_ptr(), b.data_ptr()
+    ends = [t.data_ptr() + size * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))) for t in (a, b)]
+    if at >= ends[1] or to >= ends[0]:
+        return False
+    if (to - at) % size:
+        return True
+    terms: dict = {}
+    for t, sign in ((a, 1), (b, -1)):
+        for n, s in zip(t.shape, t.stride()):
+            if s:
+                lo, hi = terms.get(s, (0, 0))
+                terms[s] = (lo, hi + n - 1) if sign > 0 else (lo - (n - 1), hi)
+    return _reaches(sorted(((s, *c) for s, c in terms.items()), reverse=True), (to - at) // size, [1000])
+
+
 def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout: str = "half",
            amplitude: float = 1.0, inverse: bool = False,
            out: Optional[torch.Tensor] = None) -> torch.Tensor:
@@ -897,7 +950,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout
     is read as it is). ``freqs`` (float64, see ``rotary_freqs``) turns the first 2 *
     len(freqs) channels as pairs: (i, i + len(freqs)) for layout "half", (2i, 2i + 1) for
     "interleaved"; the others stay. ``inverse`` turns back by the same ``amplitude``: the
-    gradient at x from the one at the result. ``out`` may be x, or memory apart from it."""
+    gradient at x from the one at the result. ``out`` may be x itself, or else shares no element
+    with it (other heads of the same rows do not)."""
     if not isinstance(x, torch.Tensor) or x.dim() not in (3, 4):
         raise ValueError("x must be a HIP device tensor, tokens x heads x width or batch x steps x "
                          "heads x width")
@@ -920,10 +974,10 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, freqs: torch.Tensor, layout
     else:
         _seq_tensor(out, "out", dtype=x.dtype, shape=x.shape, device=dev)
         os_ = _head_rows(out, "out", x.dim())[1]
-        if out.data_ptr() == x.data_ptr() and os_ != xs and x.numel():
-            raise ValueError("out shares x's memory in another layout")
-        if any(n > 1 and st == 0 for n, st in zip(out.shape, out.stride())) and x.numel():
+        if not _elements_apart(out.shape, out.stride()):
             raise ValueError("out has overlapping rows")
+        if (out.data_ptr() != x.data_ptr() or os_ != xs) and _share(x, out):
+            raise ValueError("out shares x's memory and is not x")
     ps = positions.stride()
     if x.dim() == 3:
         batch, steps, xs, os_, ps = 1, x.shape[0], (0, *xs), (0, *os_), (0, *ps)

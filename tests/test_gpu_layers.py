@@ -806,3 +806,26 @@ def test_pairs_that_do_not_count_may_overflow(kind, T, d):
     args = (t["q"], t["k"], t["v"], t["decay"])
     check_forward(api.linear_attention(*args, state=t["state"]), x, kind, d ** -0.5)
     check_grad(api.linear_attention_grad(*args, t["do"], dlast=t["dlast"], state=t["state"]), x, kind, d ** -0.5)
+
+
+def test_rotary_into_shared_memory():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    y = torch.randn(6, 9, 5, 24, device="cuda")
+    pos = torch.arange(9, device="cuda").expand(6, 9)
+    f = torch.ones(12, dtype=torch.float64, device="cuda")
+    flat = torch.zeros(6 * 9 * 5 * 24, device="cuda")
+    for x, out in ((y[:, :, :2], y[:, :, 1:3]), (y[:, :8], y[:, 1:]), (y[:5], y[1:]),
+                   (y.transpose(0, 1)[:6, :6], y[:6, :6]),
+                   (y, torch.as_strided(flat, y.shape, (24 * 9, 24, 12, 1))),
+                   (y, torch.as_strided(flat, y.shape, (9 * 60, 60, 24, 1)))):
+        with pytest.raises(ValueError, match="shares|overlapping"):
+            api.rotary(x, pos[:1, :1].expand(x.shape[:2]), f, out=out)
+    # other heads of the same rows, and other channels of the same heads, are memory apart
+    want = api.rotary(y[:, :, :2], pos, f)
+    mine = y.clone()
+    api.rotary(mine[:, :, :2], pos, f, out=mine[:, :, 3:])
+    assert torch.equal(mine[:, :, 3:], want) and torch.equal(mine[:, :, :3], y[:, :, :3])
+    mine = y.clone()
+    api.rotary(mine[..., :12], pos, f[:6], out=mine[..., 12:])
+    assert torch.equal(mine[..., 12:], api.rotary(y[..., :12], pos, f[:6])) and torch.equal(mine[..., :12], y[..., :12])
