@@ -574,7 +574,7 @@ typedef struct symnmf_adamw_tensor {
  * step_dev (nullable, one device int64) instead, lr_dev (nullable, one device
  * float32) instead of lr, grad_scale_dev (nullable, one device float32) times
  * grad_scale: read when the launch runs, so that a captured call can be replayed
- * with other values. No two tensors may share memory.
+ * with other values. What is written shares memory with no other tensor.
  * Errors: E_INVALID, E_HIP. */
 int symnmf_adamw(int param_type, int grad_type, int state_bits, const symnmf_adamw_tensor* tensors,
                  int32_t count, double lr, double beta1, double beta2, double eps,

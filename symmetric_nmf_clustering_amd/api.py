@@ -7,6 +7,7 @@ only supplies device memory and the stream.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import functools
 import math
@@ -1026,6 +1027,20 @@ def _device_scalar(x, name: str, dtype, device):
     return x, None
 
 
+def _check_apart(written, read) -> None:
+    """Refuses ranges (start, end) to write that meet, or that meet one (start, bytes) to read."""
+    written.sort()
+    end = 0
+    for at, to in written:
+        if at < end:
+            raise ValueError("two of the tensors share memory")
+        end = to
+    for at, nbytes in read:
+        i = bisect.bisect_left(written, (at + nbytes,)) - 1  # the last to start below its end
+        if i >= 0 and written[i][1] > at:
+            raise ValueError("a tensor that is read shares memory with one that is written")
+
+
 def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999,
                eps: float = 1e-8, weight_decay: float = 0.01, masters=None, m_scale=None,
                v_scale=None, grad_scale=1.0) -> None:
@@ -1038,7 +1053,8 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
         p = p (1 - lr weight_decay) - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
     ``step`` is 1 for the first one. step (int64), lr and grad_scale (float32) may be device
     tensors of one element, read when the step runs: a captured step follows them. A
-    parameter whose gradient is None is left alone. No two tensors may share memory."""
+    parameter whose gradient is None is left alone. What is written shares memory with
+    no other tensor of the call (gradients may be one another's)."""
     lists = {"grads": grads, "m": m, "v": v, "masters": masters, "m_scale": m_scale, "v_scale": v_scale}
     for name, x in lists.items():
         if x is None and name in ("masters", "m_scale", "v_scale"):
@@ -1054,7 +1070,7 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
     dev = params[used[0]].device
     held = []  # dense copies live until the launch is made
     groups: dict = {}
-    written = []
+    written, read = [], []
     state_type, state_types = (torch.float8_e4m3fn, _CODES) if low else (torch.float32, _FULL)
 
     def fits(x, name, dtype, types, shape):
@@ -1063,8 +1079,9 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
             _seq_tensor(x, name, types, shape=shape, device=dev)
         if not x.is_contiguous():
             raise ValueError("params and states must be contiguous")
-        at = x.data_ptr()
-        written.append((at, at + x.numel() * x.element_size()))
+        at, nbytes = x.data_ptr(), x.numel() * x.element_size()
+        if nbytes:
+            written.append((at, at + nbytes))
         return at
 
     for i in used:
@@ -1074,10 +1091,12 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
         gt = _seq_tensor(g, "grads", device=dev)
         if g.shape != shape:
             raise ValueError(f"grads must have shape {tuple(shape)}, not {tuple(g.shape)}")
+        n = p.numel()
         if not g.is_contiguous():
             g = g.contiguous()
             held.append(g)
-        n = p.numel()
+        elif n:
+            read.append((g.data_ptr(), n * g.element_size()))
         pp = fits(p, "params", p.dtype, _DTYPES, shape)
         mp = fits(m[i], "m", state_type, state_types, shape)
         vp = fits(v[i], "v", state_type, state_types, shape)
@@ -1090,15 +1109,11 @@ def adamw_step(params, grads, m, v, step, lr=1e-3, beta1: float = 0.9, beta2: fl
             vs = fits(v_scale[i], "v_scale", torch.float32, _FULL, blocks)
         if n:
             groups.setdefault((pt, gt), []).append((pp, g.data_ptr(), mp, vp, ms, vs, master, n))
-    written.sort()
-    end = 0
-    for at, to in written:  # (empty tensors' ranges are empty)
-        if at < end and at < to:
-            raise ValueError("two of the tensors share memory")
-        end = max(end, to)
     step, step_p = _device_scalar(step, "step", torch.int64, dev)
     lr, lr_p = _device_scalar(lr, "lr", torch.float32, dev)
     grad_scale, scale_p = _device_scalar(grad_scale, "grad_scale", torch.float32, dev)
+    read += [(at, n) for at, n in ((step_p, 8), (lr_p, 4), (scale_p, 4)) if at]
+    _check_apart(written, read)
     stream = _here(dev)
     for (pt, gt), rows in groups.items():
         table = (L.AdamwTensor * len(rows))(*rows)

@@ -829,3 +829,23 @@ def test_rotary_into_shared_memory():
     mine = y.clone()
     api.rotary(mine[..., :12], pos, f[:6], out=mine[..., 12:])
     assert torch.equal(mine[..., 12:], api.rotary(y[..., :12], pos, f[:6])) and torch.equal(mine[..., :12], y[..., :12])
+
+
+def test_what_adamw_reads_is_apart_from_what_it_writes():
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    flat = torch.zeros(1000, device="cuda")
+    p, rest = flat[:100], torch.ones(100, device="cuda")
+    m, v, _, _ = api.adamw_states([p])
+    for grad in (p, flat[60:160], m[0], v[0]):
+        with pytest.raises(ValueError, match="shares memory"):
+            api.adamw_step([p], [grad], m, v, 1)
+    for kw in (dict(lr=p[7]), dict(grad_scale=m[0][:1])):
+        with pytest.raises(ValueError, match="shares memory"):
+            api.adamw_step([p], [rest], m, v, 1, **kw)
+    assert not flat.any()  # refused before anything ran
+    q = torch.zeros(100, device="cuda")
+    m, v, _, _ = api.adamw_states([p, q])
+    grad = flat[100:200].fill_(1.0)  # a neighbour, and one gradient for two parameters
+    api.adamw_step([p, q], [grad, grad], m, v, 1, lr=0.5, eps=0.0, weight_decay=0.0)
+    assert torch.allclose(p, torch.full_like(p, -0.5)) and torch.equal(p, q) and not flat[200:].any()

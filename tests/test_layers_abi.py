@@ -210,3 +210,16 @@ def test_shared_elements_of_views():
     wide = torch.zeros(64, 7 * 128).unflatten(1, (7, 128))  # heads of one projection
     assert not api._share(wide[:, :3], wide[:, 3:6]) and api._share(wide[:, :3], wide[:, 2:5])
     assert api._elements_apart(wide.shape, wide.stride()) and not api._share(wide[:0], wide[:0])
+
+
+def test_ranges_that_meet_are_refused():
+    from symmetric_nmf_clustering_amd import api
+    apart = [(100, 140), (140, 180), (300, 301)]
+    for read in ([], [(60, 40), (180, 120), (301, 9)], [(200, 8), (200, 8)]):
+        api._check_apart(apart[::-1], read)
+    for written in ([(100, 140), (139, 180)], [(0, 50), (10, 20), (60, 70)], [(5, 9), (5, 9)]):
+        with pytest.raises(ValueError, match="share memory"):
+            api._check_apart(written, [])
+    for read in ((99, 2), (100, 40), (179, 1), (0, 1000), (290, 11), (120, 4), (150, 100)):
+        with pytest.raises(ValueError, match="shares memory"):
+            api._check_apart(list(apart), [(0, 10), read])
