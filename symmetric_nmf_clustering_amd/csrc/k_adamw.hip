@@ -11,6 +11,10 @@
 // rounded. Every block's largest element is held to float32, so that all of a block
 // decays with it; a code that is off by half a step puts a root at most 2^-4 off.
 //
+// The betas and 1 - lr wd are not rounded to float32, whose error every step would repeat: the
+// memory of beta2 = 0.99999 would be 0.14% off, a weight decay of 1e-6 a step 1.3%. (A beta goes
+// in as two numbers, the decay as p - lr wd p.)
+//
 // Arithmetic is float32: about one code in 10^6 lies on the other side of a rounding's
 // border than in float64 (through float64 the 8-bit step takes 284 us instead of 228, and 278
 // where only waves with a value near a border go there).
@@ -20,6 +24,8 @@
 // tensors' first workgroups, in the kernel's arguments. 108 million parameters: bf16 with
 // float32 masters and states (28 bytes each) 622 us, 4.8 TB/s; bf16 with 8-bit states (10
 // bytes) 220 us, 4.9 TB/s.
+#include <cfloat>
+
 #include "layers.h"
 
 namespace symnmf {
@@ -33,8 +39,9 @@ struct AdamLaunch {
     AdamTensor t[kTensors];
     uint32_t first[kTensors];  // workgroup
     int32_t count;
-    float b1, c1, b2, c2;    // betas and 1 - betas
-    float decay, rate, root;  // 1 - lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
+    float b1, c1, b2, c2;     // betas and 1 - betas
+    float b1_rest, b2_rest;   // what float32 leaves of the betas
+    float decay, rate, root;  // lr wd, lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
     float eps, grad_scale;
     double beta1, beta2, lr, weight_decay, step;
     const int64_t* step_dev;
@@ -46,7 +53,7 @@ static_assert(sizeof(AdamLaunch) <= 4000, "kernel arguments");
 // The three factors of the update that depend on the step and the rate.
 __host__ __device__ inline void factors(double step, double lr, double beta1, double beta2,
                                         double wd, float* decay, float* rate, float* root) {
-    *decay = (float)(1.0 - lr * wd);
+    *decay = (float)(lr * wd);
     *rate = (float)(lr / (1.0 - pow(beta1, step)));
     *root = (float)(1.0 / sqrt(1.0 - pow(beta2, step)));
 }
@@ -84,7 +91,7 @@ __device__ __forceinline__ void store8(T* p, int n, const float (&v)[8]) {
     }
 }
 
-__device__ __forceinline__ void load_codes(const uint8_t* p, int n, float scale, float (&v)[8]) {
+__device__ __forceinline__ void load_codes(const uint8_t* p, int n, float (&v)[8]) {
     uint32_t w[2] = {0, 0};
     if (n == 8) {
         const Vec<uint8_t, 8> u = load_vec<uint8_t, 8>(p);
@@ -99,10 +106,10 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, int n, float scale,
     for (int q = 0; q < 2; ++q) {
         const f32p a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[q], false);
         const f32p b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[q], true);
-        v[4 * q + 0] = a[0] * scale;
-        v[4 * q + 1] = a[1] * scale;
-        v[4 * q + 2] = b[0] * scale;
-        v[4 * q + 3] = b[1] * scale;
+        v[4 * q + 0] = a[0];
+        v[4 * q + 1] = a[1];
+        v[4 * q + 2] = b[0];
+        v[4 * q + 3] = b[1];
     }
 }
 
@@ -180,12 +187,19 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamLaunch a, uint32_t first
     float g[8], m[8], v[8], p[8];
     P* pp = static_cast<P*>(t.param) + at;
     load8<G>(static_cast<const G*>(t.grad) + at, n, g);
+    // what m and v are kept with, as two numbers; of codes, by their scale (of v's, its square)
+    float k1 = a.b1, k1_rest = a.b1_rest, k2 = a.b2, k2_rest = a.b2_rest;
     if (LOW) {
         const float ms = n ? t.m_scale[block] : 0.f, vs = n ? t.v_scale[block] : 0.f;
-        load_codes(static_cast<const uint8_t*>(t.m) + at, n, ms, m);
-        load_codes(static_cast<const uint8_t*>(t.v) + at, n, vs, v);
+        load_codes(static_cast<const uint8_t*>(t.m) + at, n, m);
+        load_codes(static_cast<const uint8_t*>(t.v) + at, n, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= v[j];
+        for (int j = 0; j < 8; ++j) v[j] *= v[j];  // exact
+        k1 = a.b1 * ms;
+        k1_rest = fmaf(a.b1, ms, -k1) + a.b1_rest * ms;
+        const float v2 = vs * vs, v2_rest = fmaf(vs, vs, -v2);
+        k2 = a.b2 * v2;
+        k2_rest = fmaf(a.b2, v2, -k2) + fmaf(a.b2, v2_rest, a.b2_rest * v2);
     } else {
         load8<float>(static_cast<const float*>(t.m) + at, n, m);
         load8<float>(static_cast<const float*>(t.v) + at, n, v);
@@ -198,10 +212,12 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamLaunch a, uint32_t first
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float x = g[j] * gs;
-        m[j] = a.b1 * m[j] + a.c1 * x;
-        v[j] = a.b2 * v[j] + a.c2 * (x * x);
+        m[j] = fmaf(k1, m[j], fmaf(k1_rest, m[j], a.c1 * x));
+        // (a second moment past float32's range stays infinite; no code is)
+        const float rest = LOW ? v[j] : fminf(v[j], FLT_MAX);
+        v[j] = fmaf(k2, v[j], fmaf(k2_rest, rest, a.c2 * (x * x)));
         r[j] = sqrtf(v[j]);
-        p[j] = decay * p[j] - rate * (m[j] / (r[j] * root + a.eps));
+        p[j] = fmaf(-rate, m[j] / (r[j] * root + a.eps), fmaf(-decay, p[j], p[j]));
     }
     if (n) store8<P>(pp, n, p);
     if (t.master && n) store8<float>(t.master + at, n, p);
@@ -240,8 +256,8 @@ hipError_t launch_adamw(const AdamArgs& a, hipStream_t st) {
     AdamLaunch l{};
     l.beta1 = a.beta1, l.beta2 = a.beta2, l.lr = a.lr, l.weight_decay = a.weight_decay;
     l.step = a.step;
-    l.b1 = (float)a.beta1, l.c1 = (float)(1.0 - a.beta1);
-    l.b2 = (float)a.beta2, l.c2 = (float)(1.0 - a.beta2);
+    l.b1 = (float)a.beta1, l.c1 = (float)(1.0 - a.beta1), l.b1_rest = (float)(a.beta1 - l.b1);
+    l.b2 = (float)a.beta2, l.c2 = (float)(1.0 - a.beta2), l.b2_rest = (float)(a.beta2 - l.b2);
     l.eps = (float)a.eps;
     l.grad_scale = a.grad_scale;
     l.step_dev = a.step_dev, l.lr_dev = a.lr_dev, l.grad_scale_dev = a.grad_scale_dev;

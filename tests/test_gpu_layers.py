@@ -849,3 +849,36 @@ def test_what_adamw_reads_is_apart_from_what_it_writes():
     grad = flat[100:200].fill_(1.0)  # a neighbour, and one gradient for two parameters
     api.adamw_step([p, q], [grad, grad], m, v, 1, lr=0.5, eps=0.0, weight_decay=0.0)
     assert torch.allclose(p, torch.full_like(p, -0.5)) and torch.equal(p, q) and not flat[200:].any()
+
+
+@pytest.mark.parametrize("low", [False, True])
+def test_adamw_factors_are_not_rounded(low):
+    """What a step keeps of m, v and p, averaged over many values: one of its own roundings is at
+    most u and goes either way, the betas' and the decay's would all go one way (up to u / 2)."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    n = 1 << 20
+    # factors half a step of float32 away from its numbers: each rounds by u / 2 or nearly
+    beta1, beta2, lw = 1 - 2.0 ** -4 - 2.0 ** -25.1, 1 - 2.0 ** -12 + 2.0 ** -25.1, 2.0 ** -13 + 2.0 ** -25.1
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def values():
+        return torch.rand(n, generator=g, device="cuda") + 1.0
+
+    p, m, v, zero = values(), values(), values(), torch.zeros(n, device="cuda")
+    hyper = dict(lr=lw, beta1=beta1, beta2=beta2, weight_decay=1.0)
+    before = [x.double() for x in (p, m, v)]
+    if low:  # (held in 8 bits, the states show no more than 2^-4)
+        api.adamw_step([p], [zero], *api.adamw_states([p], 8)[:2], 1, **hyper,
+                       **dict(zip(("m_scale", "v_scale"), api.adamw_states([p], 8)[2:])))
+        pairs = [(p, before[0], 1 - lw)]
+    else:
+        api.adamw_step([p], [zero], [zero.clone()], [zero.clone()], 1, **hyper)
+        api.adamw_step([zero.clone()], [zero], [m], [v], 1, **hyper)
+        pairs = list(zip((p, m, v), before, (1 - lw, beta1, beta2)))
+    for got, was, factor in pairs:
+        off = (got.double() / was - factor) / factor
+        # p: one rounding; m, v: two, of which the first is of a number 2^-24 as large
+        assert off.abs().max() <= 1.01 * U
+        # the mean of n roundings uniform in +-u: u / sqrt(3 n), five times that
+        assert abs(off.mean()) <= 5 * U / (3 * n) ** 0.5
