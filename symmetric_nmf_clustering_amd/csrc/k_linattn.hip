@@ -300,7 +300,9 @@ __global__ __launch_bounds__(256) void attend_step_kernel(StepArgs a, int64_t fi
         qs[threadIdx.x] = to_f32(q[threadIdx.x]);
         ks[threadIdx.x] = to_f32(k[threadIdx.x]);
     }
-    const float decay = (float)exp(ln_decay(a.decay, head));
+    // (as two numbers: the rounding of one would be made again at every step of a stream)
+    const double kept = exp(ln_decay(a.decay, head));
+    const float decay = (float)kept, decay_rest = (float)(kept - decay);
     float vc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) vc[j] = in ? to_f32(v[c + j]) : 0.f;
@@ -319,7 +321,7 @@ __global__ __launch_bounds__(256) void attend_step_kernel(StepArgs a, int64_t fi
             if (!in || i >= a.dk) break;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                s[r].e[j] = decay * s[r].e[j] + ks[i] * vc[j];
+                s[r].e[j] = fmaf(decay, s[r].e[j], fmaf(decay_rest, s[r].e[j], ks[i] * vc[j]));
                 acc[j] += qs[i] * s[r].e[j];
             }
             store_vec<float, V>(s1 + i * a.dv, s[r]);

@@ -882,3 +882,25 @@ def test_adamw_factors_are_not_rounded(low):
         assert off.abs().max() <= 1.01 * U
         # the mean of n roundings uniform in +-u: u / sqrt(3 n), five times that
         assert abs(off.mean()) <= 5 * U / (3 * n) ** 0.5
+
+
+def test_live_decay_is_not_rounded():
+    """What a step keeps of the state, averaged over many values: the step's own rounding goes
+    either way, the decay's would go one way (up to u / 2) at every step."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    g = -np.arange(1, 4000, dtype=np.float32) * np.float32(2.0 ** -14)
+    a = np.exp(g.astype(np.float64))
+    off = (a - a.astype(np.float32)) / a  # what float32 loses of each decay
+    at = [int(off.argmax()), int(off.argmin())]
+    decay = torch.from_numpy(g[at]).cuda()
+    B, d = 16, 256
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    q, k, v = (torch.zeros(B, 2, d, device="cuda") for _ in range(3))
+    state = torch.rand(B, 2, d, d, generator=gen, device="cuda") + 1.0
+    _, new = api.linear_attention_step(q, k, v, decay, state)
+    for h in range(2):
+        e = new[:, h].double() / state[:, h].double() / a[at[h]] - 1.0
+        # one rounding (and one of a number 2^-24 as large); the mean of n, uniform in +-u
+        assert e.abs().max() <= 1.01 * U
+        assert abs(e.mean()) <= 5 * U / (3 * e.numel()) ** 0.5 < 0.1 * abs(off[at[h]])
