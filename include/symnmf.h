@@ -540,8 +540,9 @@ int symnmf_linear_attention_step(const symnmf_attend_desc* d, const void* q, con
  * the others are copied. inverse = 1 turns back, with the same amplitude: the
  * gradient at x from that at out. positions: int32 or int64 (any value), element
  * (b, t) at b * pos_batch + t * pos_step; freqs: dims / 2 float64, radians a
- * position; the angle is taken in float64, so far positions lose nothing. out may
- * be x itself, with the same strides.
+ * position; whole turns are taken off the angle exactly, so far positions lose
+ * nothing. out may be x itself, with the same strides; otherwise the two share no
+ * element.
  * Errors: E_INVALID, E_HIP. */
 int symnmf_rotary(int type, int64_t batch, int64_t steps, int32_t heads, int32_t width,
                   int32_t dims, int interleaved, int inverse, float amplitude, const void* x,

@@ -1,9 +1,8 @@
 // Rotary positions: pairs of channels of every head turned by position times
 // frequency.
 //
-// y1 = amp (x1 cos - x2 sin), y2 = amp (x2 cos + x1 sin), the angle in 64 bits: as
-// turns (position times frequency over 2 pi) less their whole part, whose cosine
-// and sine float32 then has to a few 2^-24 at any position. One angle serves all
+// y1 = amp (x1 cos - x2 sin), y2 = amp (x2 cos + x1 sin), the angle reduced exactly (turn_of):
+// cosine and sine are right to a few 2^-24 at any position. One angle serves all
 // heads of a step: a thread takes some pairs of a step and goes through its heads
 // with their cosines in registers. Bound by memory: x is read and written once.
 #include "layers.h"
@@ -11,6 +10,23 @@
 namespace symnmf {
 
 namespace {
+
+// Sine and cosine of pos times freq (radians). The turns' whole part is taken off exactly: pos as
+// two numbers that float64 holds (52 and 11 bits), freq / 2 pi as two, the large product by an fma
+// that adds what is left of it unrounded. What is left is right to 2^-42 turns at any position (freq up to 1) and
+// goes to float32 with its remainder, whose first order is added to the functions' values.
+__device__ __forceinline__ void turn_of(int64_t pos, double freq, float* sine, float* cosine) {
+    constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18;  // 1 / 2 pi
+    const double f = freq * kTurn, f_rest = fma(freq, kTurn, -f) + freq * kTurnRest;
+    const double far = (double)(pos & ~int64_t(2047)), near = (double)(pos & 2047);
+    double turns = fma(far, f, -rint(far * f)) + fma(near, f, far * f_rest);
+    turns -= rint(turns);
+    const float u = (float)turns, du = (float)((turns - u) * 6.283185307179586);
+    float s, c;
+    sincospif(2.f * u, &s, &c);
+    *sine = fmaf(c, du, s);
+    *cosine = fmaf(-s, du, c);
+}
 
 // P pairs of each of U heads, all asked for before the first is turned: (CLOSE) 2 P elements
 // at x, or P at x and P at x + gap. copy: they stay as they are (0 times an infinity would
@@ -66,14 +82,11 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a, int64_t first
         for (int i = 0; i < P; ++i) c[i] = s[i] = 0.f;
     } else {
         const int64_t pa = b * a.pos_b + t * a.pos_t;
-        const double pos = a.pos_type == kI32 ? (double)static_cast<const int32_t*>(a.pos)[pa]
-                                              : (double)static_cast<const int64_t*>(a.pos)[pa];
+        const int64_t pos = a.pos_type == kI32 ? static_cast<const int32_t*>(a.pos)[pa]
+                                               : static_cast<const int64_t*>(a.pos)[pa];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            constexpr double kTurn = 0.15915494309189533577;  // 1 / 2 pi
-            const double turns = pos * a.freqs[p0 + i] * kTurn;
-            const float f = (float)(turns - rint(turns));
-            sincospif(2.f * f, &s[i], &c[i]);
+            turn_of(pos, a.freqs[p0 + i], &s[i], &c[i]);
             c[i] *= a.amplitude;
             s[i] *= a.inverse ? -a.amplitude : a.amplitude;
         }

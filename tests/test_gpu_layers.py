@@ -904,3 +904,27 @@ def test_live_decay_is_not_rounded():
         # one rounding (and one of a number 2^-24 as large); the mean of n, uniform in +-u
         assert e.abs().max() <= 1.01 * U
         assert abs(e.mean()) <= 5 * U / (3 * e.numel()) ** 0.5 < 0.1 * abs(off[at[h]])
+
+
+def test_rotary_at_any_position():
+    """Angles reduced in exact arithmetic: positions up to the ends of int64 are as precise as near ones."""
+    from decimal import Decimal, getcontext
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    getcontext().prec = 90  # 2^63 radians have 19 digits before the point
+    turn = Decimal("6.283185307179586476925286766559005768394338798750211641949889184615632812572417997256069650684")
+    rng = np.random.default_rng(8)
+    ends = [0, -1, 2047, 2048, -2048, 2 ** 53 + 1, -2 ** 53 - 1, 2 ** 63 - 1, -2 ** 63, 2 ** 63 - 1025]
+    pos = np.array(ends + [int(x) * (-1) ** i for i, x in enumerate(2.0 ** rng.uniform(20, 63, 40))])
+    f = np.concatenate([1000.0 ** (-np.arange(6) / 6), [np.pi, 0.1]])
+    angle = np.array([[float(Decimal(int(p)) * Decimal(float(w)) % turn) for w in f] for p in pos])
+    cos, sin = np.cos(angle)[:, None, :], np.sin(angle)[:, None, :]
+    tp, tf = torch.from_numpy(pos).cuda(), torch.from_numpy(f).cuda()
+    for kind in ("fp32", "bf16"):
+        x, xv = dev(torch, rng.standard_normal((len(pos), 3, 16)), kind)
+        a, b = xv[..., :8], xv[..., 8:]
+        for inverse in (False, True):
+            s = -sin if inverse else sin
+            ref = np.concatenate([a * cos - b * s, b * cos + a * s], -1)
+            got = api.rotary(x, tp, tf, inverse=inverse)
+            close(got, ref, rotary_bound(xv, 8, False, 1.0), kind)
