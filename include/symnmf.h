@@ -498,9 +498,9 @@ size_t symnmf_linear_attention_ws_bytes(const symnmf_attend_desc* d, int gradien
  *   state (nullable: zeros), last (nullable): batch x heads x dk x dv float32,
  *     dense, the state before the first step and after the last; they may not
  *     overlap.
- * Computed in chunks of steps as matrix products; the state to float32's
- * precision whatever the type (for bfloat16, what o takes from within a chunk
- * and from the state passes through one more rounding to bfloat16). Elements
+ * Computed in chunks of steps as matrix products, the state to float32's
+ * precision whatever the type, o to 2^-16 of its terms before its rounding (in
+ * float32, to float32's precision). Elements
  * must be finite: an infinite or NaN one may make all of its chunk (64 steps)
  * and what follows NaN. (A dot product of finite q_t and k_s that overflows counts
  * only where s <= t and their weight is not 0.) The same bits on every call.

@@ -22,9 +22,10 @@
 //
 // All products run on the bf16 matrix cores, on bf16 parts ("planes") of their operands
 // whose products are summed in float32:
-//   bf16: one plane; P and, in X S, the state are rounded to bf16 (as the inputs and the
-//     output are: each costs the output at most what its own rounding does).
-//   fp16: two planes hold an element exactly; P and S, in two, lose 2^-18; three products.
+//   bf16: one plane; P and, in X S, the state are two, which hold them to 2^-16 (in one, o's error
+//     against float64 is 2.35e-3 of its size, not the 1.66e-3 of its own rounding, for 8% of the time:
+//     1 x 32768 x 16 heads 230 us against 212), two products.
+//   fp16: two planes hold an element exactly; P and S, in two, lose 2^-16; three products.
 //   fp32: three planes (bf16split.h), six products, which is float32's precision; 16x16x4
 //     float32 products would take 2.7 times their cycles.
 // The state itself stays at float32's precision in every type: the weights go to z, and w z
@@ -49,18 +50,18 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Planes of an element type, and steps of a chunk (at most).
+// Planes of an element, of P and the state as an operand, and steps of a chunk (at most).
 template <class T>
 struct Planes {
-    static constexpr int N = 3, C = 32;
+    static constexpr int N = 3, S = 3, C = 32;
 };
 template <>
 struct Planes<f16_t> {
-    static constexpr int N = 2, C = 32;
+    static constexpr int N = 2, S = 2, C = 32;
 };
 template <>
 struct Planes<bf16_t> {
-    static constexpr int N = 1, C = 64;
+    static constexpr int N = 1, S = 2, C = 64;
 };
 
 // 32 deep operands of a product: a lane's 8 values, as N planes of bf16.
@@ -246,7 +247,8 @@ template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
     // 64 steps of two column tiles a wave leave no registers to ask for the next chunk's rows
     // early; 32 do (4 x 4096 x 32 heads of 128 bf16: 179 us against 190)
-    static constexpr int C = WN == 2 ? 32 : Planes<T>::C, NP = Planes<T>::N;
+    static constexpr int C = WN == 2 ? 32 : Planes<T>::C;
+    static constexpr int NP = Planes<T>::N, NS = Planes<T>::S;
     static constexpr int NT = 64 * NW, ZC = 16 * WN * NW;
     // pads of 16 bytes keep reads of rows off one another's banks, of 32 those down columns
     using TX = Tile<T, C, DX, NT, WIDE, 8>;
@@ -256,7 +258,7 @@ struct WalkSizes {
         bf16_t x[OUT ? NP * TX::PLANE : 8];
         bf16_t y[NP * TY::PLANE];
         bf16_t z[NP * TZ::PLANE];
-        bf16_t p[OUT ? NP * C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
+        bf16_t p[OUT ? NS * C * C : 8];  // 16 x 16 blocks (u, w): a lane's 4 values of w together
         float wz[C];            // st_scale a^(C - in_pow - w): the weights of a whole chunk
         float wx[OUT ? C : 4];  // in_scale a^(u + in_pow)
         float wp[OUT ? C * 16 : 4];  // p_scale a^(u - w), as a lane holds a block, by bu - bw
@@ -288,7 +290,7 @@ template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     AttendArgs a, int64_t first, int64_t units, int ztiles) {
     using Z = WalkSizes<T, DX, NW, WN, OUT, WIDE>;
-    constexpr int C = Z::C, NP = Z::NP, NX = DX / 16, NB = C / 16;
+    constexpr int C = Z::C, NP = Z::NP, NS = Z::NS, NX = DX / 16, NB = C / 16;
     constexpr int XS = Z::TX::STRIDE, YS = Z::TY::STRIDE, ZS = Z::TZ::STRIDE;
     constexpr int XP = Z::TX::PLANE, YP = Z::TY::PLANE, ZP = Z::TZ::PLANE;
     __shared__ alignas(16) typename Z::Lds lds;
@@ -392,7 +394,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
             lds.wp[i] = gap >= 0 ? R.p_scale * lds.pw[gap] : 0.f;
         }
         // blocks above the diagonal that a 32-deep step reads
-        for (int i = threadIdx.x; i < NP * C * C / 2; i += Z::NT)
+        for (int i = threadIdx.x; i < NS * C * C / 2; i += Z::NT)
             reinterpret_cast<uint32_t*>(lds.p)[i] = 0;
     }
 
@@ -440,11 +442,11 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                     acc[r] *= wp[r];
                     if (!FULL) acc[r] = wp[r] == 0.f ? 0.f : acc[r];
                 }
-                uint32_t p0[NP], p1[NP];
-                split_pair<NP>(acc[0], acc[1], p0);
-                split_pair<NP>(acc[2], acc[3], p1);
+                uint32_t p0[NS], p1[NS];
+                split_pair<NS>(acc[0], acc[1], p0);
+                split_pair<NS>(acc[2], acc[3], p1);
 #pragma unroll
-                for (int j = 0; j < NP; ++j)
+                for (int j = 0; j < NS; ++j)
                     *reinterpret_cast<uint2*>(lds.p + j * C * C + ((bu * NB + bw) * 64 + lane) * 4) =
                         uint2{p0[j] & keep[q][0], p1[j] & keep[q][1]};
             }
@@ -459,11 +461,11 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                 zf[k][m] = read_column<NP>(lds.z + 32 * k * ZS + 16 * (WN * wave + m), ZP, ZS, lane);
 
         if constexpr (OUT) {
-            Frag<NP> sf[DX / 32][WN];
+            Frag<NS> sf[DX / 32][WN];
 #pragma unroll
             for (int k = 0; k < DX / 32; ++k)
 #pragma unroll
-                for (int m = 0; m < WN; ++m) sf[k][m] = frag_of<NP>(S[2 * k][m], S[2 * k + 1][m]);
+                for (int m = 0; m < WN; ++m) sf[k][m] = frag_of<NS>(S[2 * k][m], S[2 * k + 1][m]);
             const int64_t e0 = ((b * a.steps + from + dir * (u0 + l16)) * a.heads + head) * R.dz + zw + 4 * g;
             const int64_t es = dir * 16 * a.heads * R.dz;
 #pragma unroll
@@ -474,7 +476,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                 for (int k = 0; k < DX / 32; ++k) {
                     const auto xf = read_split<NP>(px + 32 * k, XP, 16, g);
 #pragma unroll
-                    for (int m = 0; m < WN; ++m) acc[m] = mma<NP>(sf[k][m], xf, acc[m]);
+                    for (int m = 0; m < WN; ++m) acc[m] = mma<NS>(sf[k][m], xf, acc[m]);
                 }
                 const float wx = lds.wx[16 * bu + l16];
 #pragma unroll
@@ -486,10 +488,10 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
                 for (int k = 0; k <= bu / 2; ++k) {
                     // (a lane's 4 values of a block lie at lane * 4; those of the next block
                     // down 256 further)
-                    const auto pf = read_split<NP>(
+                    const auto pf = read_split<NS>(
                         lds.p + ((bu * NB + 2 * k) * 64 + l16) * 4 + 60 * g, C * C, 256, g);
 #pragma unroll
-                    for (int m = 0; m < WN; ++m) acc[m] = mma<NP>(zf[k][m], pf, acc[m]);
+                    for (int m = 0; m < WN; ++m) acc[m] = mma<NS>(zf[k][m], pf, acc[m]);
                 }
                 if (FULL || 16 * bu + l16 < n) {
                     const int64_t e = e0 + bu * es;

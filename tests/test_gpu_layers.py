@@ -928,3 +928,26 @@ def test_rotary_at_any_position():
             ref = np.concatenate([a * cos - b * s, b * cos + a * s], -1)
             got = api.rotary(x, tp, tf, inverse=inverse)
             close(got, ref, rotary_bound(xv, 8, False, 1.0), kind)
+
+
+@pytest.mark.parametrize("B,T,H,G,dk,dv", [(2, 300, 2, 1, 128, 128), (1, 130, 2, 2, 64, 48), (1, 70, 1, 1, 256, 256),
+                                           (20, 70, 16, 4, 128, 96), (1, 1500, 1, 1, 40, 33), (3, 64, 4, 2, 24, 24)])
+def test_bf16_rounds_its_outputs_alone(B, T, H, G, dk, dv):
+    """What is inside goes through two bfloat16 parts (2^-8 of 2^-8), not through one: besides the
+    output's own rounding, 2^-16 of the terms and float32's share."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, x = make(torch, "bf16", B, T, H, G, dk, dv, 70 + dk)
+    scale = dk ** -0.5
+    args = [x[n] for n in "qkv"]
+    mags = [abs(a) for a in args]
+    c = attend_bound("fp32", T, dk, dv) + 2.0 ** -16
+    got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], state=t["state"])
+    ref = lo.linear_attention(*args, x["decay"], x["state"], None, scale)
+    mag = lo.linear_attention(*mags, x["decay"], abs(x["state"]), None, scale)
+    close(got[0], ref[0], c * mag[0], "bf16")
+    got = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"], state=t["state"])
+    ref = lo.linear_attention_grad(*args, x["decay"], x["do"], x["dlast"], x["state"], None, scale)
+    mag = lo.linear_attention_grad(*mags, x["decay"], abs(x["do"]), abs(x["dlast"]), abs(x["state"]), None, scale)
+    for i in range(3):
+        close(got[i], ref[i], (c + 2 * U * H) * mag[i], "bf16")
