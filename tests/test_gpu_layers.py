@@ -951,3 +951,133 @@ def test_bf16_rounds_its_outputs_alone(B, T, H, G, dk, dv):
     mag = lo.linear_attention_grad(*mags, x["decay"], abs(x["do"]), abs(x["dlast"]), abs(x["state"]), None, scale)
     for i in range(3):
         close(got[i], ref[i], (c + 2 * U * H) * mag[i], "bf16")
+
+
+# ---- every walk: two column tiles a wave, cut and whole, with and without lengths ---------
+
+def device_definition(torch, t, scale, gradient):
+    """The definitions in float64 on the device (the oracle's loops, all batch rows at once)."""
+    q, k, v, do = (t[n].double() for n in ("q", "k", "v", "do"))
+    B, T, H, dk = q.shape
+    shared = H // k.shape[2]
+    k, v = (x.repeat_interleave(shared, 2) for x in (k, v))
+    a = t["decay"].double().exp()[None, :, None, None]
+    n = torch.full((B,), T, device="cuda") if t["lengths"] is None else t["lengths"].long().clamp(0, T)
+    inside = (torch.arange(T, device="cuda")[:, None] < n)[:, :, None, None, None]
+    S, o, dq = t["state"].double(), torch.zeros_like(do), torch.zeros_like(q)
+    for i in range(T):
+        new = a * S + k[:, i, :, :, None] * v[:, i, :, None, :]
+        S = torch.where(inside[i], new, S)
+        o[:, i] = torch.where(inside[i, ..., 0], scale * (q[:, i, :, :, None] * S).sum(2), 0.0)
+        if gradient:
+            dq[:, i] = torch.where(inside[i, ..., 0], scale * (S * do[:, i, :, None, :]).sum(3), 0.0)
+    if not gradient:
+        return o, S
+    R, dk_, dv_ = t["dlast"].double(), torch.zeros_like(k), torch.zeros_like(v)
+    for i in range(T - 1, -1, -1):
+        new = R + scale * q[:, i, :, :, None] * do[:, i, :, None, :]
+        dk_[:, i] = torch.where(inside[i, ..., 0], (new * v[:, i, :, None, :]).sum(3), 0.0)
+        dv_[:, i] = torch.where(inside[i, ..., 0], (new * k[:, i, :, :, None]).sum(2), 0.0)
+        R = torch.where(inside[i], a * new, R)
+    dk_, dv_ = (x.unflatten(2, (-1, shared)).sum(3) for x in (dk_, dv_))
+    return dq, dk_, dv_, R
+
+
+def check_on_device(torch, t, clean, kind, gradient):
+    """The library's outputs on t against the definition on the same tensors, ``clean`` of masked NaN."""
+    from symmetric_nmf_clustering_amd import api
+    B, T, H, dk = t["q"].shape
+    dv = t["v"].shape[3]
+    scale = dk ** -0.5
+    kw = dict(state=t["state"], lengths=t["lengths"])
+    if gradient:
+        got = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"], **kw)
+    else:
+        got = api.linear_attention(t["q"], t["k"], t["v"], t["decay"], **kw)
+    ref = device_definition(torch, clean, scale, gradient)
+    sizes = {n: x if x is None or n in ("decay", "lengths") else x.abs() for n, x in clean.items()}
+    mag = device_definition(torch, sizes, scale, gradient)
+    inner = attend_bound("fp32", T, dk, dv) + (2 * U * H if gradient else 0.0)
+    for i, (g, r, m) in enumerate(zip(got, ref, mag)):
+        state = i == len(got) - 1
+        c = inner + (0.0 if state or kind == "fp32" else 2.0 ** -16)
+        close(g, r.cpu().numpy(), (c * m).cpu().numpy(), "fp32" if state else kind)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("B,T,H,G,dk,dv", [
+    (1, 1100, 64, 16, 128, 128),  # cut in six, more than 256 workgroups' worth of heads
+    (1, 700, 32, 8, 128, 128),    # its gradient cut in four, likewise
+    (1, 601, 96, 96, 88, 96),     # cut in five, heads of 96
+    (20, 70, 16, 4, 128, 128),    # whole
+    (24, 75, 12, 3, 104, 72),     # whole, columns missing from the last tile
+    (6, 33, 48, 48, 96, 96),      # whole, heads of 96
+    (1, 700, 3, 1, 256, 256),     # a cut history of wide heads
+    (2, 520, 3, 3, 256, 64), (2, 520, 3, 3, 40, 256), (1, 650, 2, 2, 255, 130),
+])
+def test_every_walk(kind, ragged, B, T, H, G, dk, dv):
+    torch = require_gpu()
+    lengths = None
+    if ragged:
+        lengths = [(T - 1, T, T // 2, 0, 1, 64, T // 3)[(b + (0 if B > 1 else 2)) % 7] for b in range(B)]
+    t, _ = make(torch, kind, B, T, H, G, dk, dv, B + T, lengths)
+    clean = dict(t)
+    for name in ("q", "k", "v", "do") if ragged else ():
+        clean[name] = t[name].clone()
+        for b, n in enumerate(lengths):
+            t[name][b, n:] = float("nan")
+            clean[name][b, n:] = 0.0
+    for gradient in (False, True):
+        check_on_device(torch, t, clean, kind, gradient)
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_definition_on_the_device(ragged):
+    """The device's float64 definition is the oracle's."""
+    torch = require_gpu()
+    t, x = make(torch, "fp32", 3, 20, 4, 2, 5, 7, 90, [20, 0, 11] if ragged else None)
+    args = [x[n] for n in "qkv"]
+    for got, want in ((device_definition(torch, t, 0.3, False),
+                       lo.linear_attention(*args, x["decay"], x["state"], x["lengths"], 0.3)),
+                      (device_definition(torch, t, 0.3, True),
+                       lo.linear_attention_grad(*args, x["decay"], x["do"], x["dlast"], x["state"],
+                                                x["lengths"], 0.3))):
+        for a, b in zip(got, want):
+            assert np.abs(a.cpu().numpy() - b).max() <= 1e-12 * np.abs(b).max()
+
+
+def test_gradient_along_itself():
+    """The outputs are linear in each of q, k, v and the state, so differences of any size are exact
+    but for rounding. Along the gradient itself (of one head, too) they are far above what rounding
+    can make: a gradient that is scaled, turned or 0 fails."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    t, _ = make(torch, "fp32", 2, 300, 4, 2, 40, 24, 13, lengths=[300, 171])
+    kw = dict(lengths=t["lengths"], scale=0.2)
+    grads = api.linear_attention_grad(t["q"], t["k"], t["v"], t["decay"], t["do"], dlast=t["dlast"],
+                                      state=t["state"], **kw)
+
+    def value(at):
+        o, last = api.linear_attention(at["q"], at["k"], at["v"], t["decay"], state=at["state"], **kw)
+        return ((t["do"].double() * o.double()).sum() + (t["dlast"].double() * last.double()).sum()).item()
+
+    def terms(at):
+        o, last = device_definition(torch, {n: x if n in ("decay", "lengths") else x.abs() for n, x in at.items()},
+                                    0.2, False)
+        return ((t["do"].double().abs() * o).sum() + (t["dlast"].double().abs() * last).sum()).item()
+
+    for name, grad in zip(("q", "k", "v", "state"), grads):
+        head = torch.zeros_like(grad)
+        if name == "state":
+            head[:, 1] = grad[:, 1]
+        else:
+            head[:, :, 1] = grad[:, :, 1]
+        for along in (grad, head):
+            d = along * (30.0 / along.square().mean().sqrt())
+            hi, lo_ = ({**t, name: t[name] + sign * d} for sign in (1, -1))
+            want = (grad.double() * d.double()).sum().item()
+            # the kernels' share of the terms, the inputs' sums and the gradient's own rounding
+            limit = (attend_bound("fp32", 300, 40, 24) + 2 * U) * (terms(hi) + terms(lo_))
+            assert limit < 0.05 * want
+            assert abs((value(hi) - value(lo_)) / 2 - want) <= limit
