@@ -246,8 +246,9 @@ struct Tile {
 template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
     // 64 steps of two column tiles a wave leave no registers to ask for the next chunk's rows
-    // early; 32 do (4 x 4096 x 32 heads of 128 bf16: 179 us against 190)
-    static constexpr int C = WN == 2 ? 32 : Planes<T>::C;
+    // early; 32 do (4 x 4096 x 32 heads of 128 bf16: 179 us against 190). Element loads of 64
+    // steps spill (2 x 2048 x 8 heads of 33 and 24: 79 us, of 32 steps 32).
+    static constexpr int C = WN == 2 || !WIDE ? 32 : Planes<T>::C;
     static constexpr int NP = Planes<T>::N, NS = Planes<T>::S;
     static constexpr int NT = 64 * NW, ZC = 16 * WN * NW;
     // pads of 16 bytes keep reads of rows off one another's banks, of 32 those down columns
