@@ -193,9 +193,10 @@ class HistoryModel:
                 [api.embed_grad(dx, ids, self.E.shape[0], scale=self.scale),
                  x.flatten(0, 1).t() @ dy.flatten(0, 1), xo.flatten(0, 1).t() @ dz])
 
-    def train_step(self, ids, next_labels, lengths=None, lr: float = 0.01,
+    def train_step(self, ids, next_labels, lengths=None, lr: float = 0.001,
                    weight_decay: float = 0.01):
-        """One AdamW step on the table and the projections; returns the loss before it."""
+        """One AdamW step on the table and the projections; returns the loss before it. (AdamW's
+        first steps move every element by lr: at 0.01 the loss more than doubles before it falls.)"""
         from . import api
 
         loss, grads = self.gradients(ids, next_labels, lengths)
