@@ -501,9 +501,11 @@ size_t symnmf_linear_attention_ws_bytes(const symnmf_attend_desc* d, int gradien
  * Computed in chunks of steps as matrix products, the state to float32's
  * precision whatever the type, o to 2^-16 of its terms before its rounding (in
  * float32, to float32's precision). Elements
- * must be finite: an infinite or NaN one may make all of its chunk (64 steps)
- * and what follows NaN. (A dot product of finite q_t and k_s that overflows counts
- * only where s <= t and their weight is not 0.) The same bits on every call.
+ * must be finite: an infinite or NaN one may make all of its chunk (up to 64 steps)
+ * and what follows NaN (float32 ones and states also above 3.38e38; below 1e-31 they
+ * keep fewer bits). A dot product of q_t with k_s or with a state of before that
+ * overflows float32 counts only where s <= t and their weight is not 0. The same
+ * bits on every call.
  * Errors: E_INVALID, E_WORKSPACE, E_HIP. */
 int symnmf_linear_attention(const symnmf_attend_desc* d, const void* q, const void* k,
                             const void* v, const float* decay, const int32_t* lengths,

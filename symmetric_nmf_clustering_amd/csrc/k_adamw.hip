@@ -15,15 +15,16 @@
 // memory of beta2 = 0.99999 would be 0.14% off, a weight decay of 1e-6 a step 1.3%. (A beta goes
 // in as two numbers, the decay as p - lr wd p.)
 //
-// Arithmetic is float32: about one code in 10^6 lies on the other side of a rounding's
-// border than in float64 (through float64 the 8-bit step takes 284 us instead of 228, and 278
-// where only waves with a value near a border go there).
+// Arithmetic is float32: six codes of m in 10^7 lie on the other side of a rounding's border than
+// in float64 (of v's root less than one; m rounded once to float32 alone makes four). Through
+// float64 the 8-bit step takes 284 us instead of 228, and 278 where only waves with a value near a
+// border go there.
 //
 // Bound by memory: a workgroup takes 2048 elements of one tensor, a thread 8 that lie
 // next to one another; 32 lanes share an 8-bit block. Which tensor is found from the
 // tensors' first workgroups, in the kernel's arguments. 108 million parameters: bf16 with
 // float32 masters and states (28 bytes each) 622 us, 4.8 TB/s; bf16 with 8-bit states (10
-// bytes) 220 us, 4.9 TB/s.
+// bytes) 223 us, 4.9 TB/s.
 #include <cfloat>
 
 #include "layers.h"

@@ -13,9 +13,9 @@ namespace {
 // join, then all segments walk at once, each from its state. That reads y and z
 // twice, so time is cut only where heads and column tiles make less than 192
 // workgroups, and into no more segments than two workgroups a CU, which run at once
-// (192 workgroups of 2048 steps: 148 us whole, 168 cut in two; 128: 112 us cut in
-// four, 131 in two). Two segments do not pay for the launches (512 steps of 16 heads:
-// 25.4 us whole, 28.5 in two, 23.7 in four), nor do short ones.
+// (192 workgroups of 2048 steps: 156 us whole, 197 cut in two; 160: 148 us whole or in
+// three; 128: 125 us in four, 147 whole). Two segments do not pay for the launches (2 x 512
+// steps of 8 heads of 64: 26 us whole, 30 in two, 23 in four), nor do short ones.
 constexpr int kEnough = 192, kMost = 512;       // workgroups
 constexpr int64_t kLeast = 128, kFewest = 3;    // steps of a segment, segments
 
@@ -38,7 +38,7 @@ int64_t plan_segments(const AttendDesc& d, int runs, int64_t* seg_len) {
 // Slot i of a head's segments holds the state that segment i makes from nothing, and
 // receives the state it starts from: X_0 = s0, X_{i+1} = a^n_i X_i + L_i. A thread
 // takes V neighbouring elements; sixteen segments' are asked for together (32 segments of
-// 16 heads of 128 x 128, 67 MB: 14.5 us).
+// 16 heads of 128 x 128, 67 MB: 14.2 us).
 template <int V>
 __global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int64_t first,
                                                           int tiles) {
@@ -283,7 +283,9 @@ struct StepArgs {
 
 // S' = a S + k v^T, o = scale q S'. The state is read and written once: 16 lanes take
 // V columns each, 16 such groups the rows, every thread with R rows in flight. Bound by
-// memory: 128 streams of 32 heads of 128 x 128 in 105 us (5.1 TB/s, the copy's rate).
+// memory: 128 streams of 32 heads of 128 x 128 in 106.5 us (5.1 TB/s, the copy's rate). Where
+// dv is no multiple of 4 a lane takes one column: 2048 x 16 heads of 50 x 50 in 296 us, of
+// 50 x 52 in 145.
 template <class T, int V>
 __global__ __launch_bounds__(256) void attend_step_kernel(StepArgs a, int64_t first, int tiles) {
     constexpr int R = 8;

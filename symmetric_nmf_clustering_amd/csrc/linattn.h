@@ -16,9 +16,9 @@
 // that spill. The next chunk's rows are asked for as soon as this one's are in LDS.
 //
 // What bounds it (bf16, heads of 128): with two workgroups a CU, issue. Of a SIMD's cycles
-// matrix products take 29%, other vector operations 33%, and the waves wait for LDS and
-// barriers in a third of theirs. 32 x 2048 steps of 16 heads: 245 us, 4.4 TB/s; alone on its
-// CU a workgroup takes 4 us for 64 steps (16 x 2048: 146 us).
+// matrix products take 34% and other vector operations 51% (548 for 32 steps and a wave), and
+// waves wait for LDS and barriers in 29% of theirs. 32 x 2048 steps of 16 heads: 286 us,
+// 4.0 TB/s; alone on its CU a workgroup takes 5 us for 64 steps (16 x 2048: 168 us).
 //
 // All products run on the bf16 matrix cores, on bf16 parts ("planes") of their operands
 // whose products are summed in float32:
@@ -246,7 +246,7 @@ struct Tile {
 template <class T, int DX, int NW, int WN, bool OUT, bool WIDE>
 struct WalkSizes {
     // 64 steps of two column tiles a wave leave no registers to ask for the next chunk's rows
-    // early; 32 do (4 x 4096 x 32 heads of 128 bf16: 179 us against 190). Element loads of 64
+    // early; 32 do (4 x 4096 x 32 heads of 128 bf16: 203 us against 271). Element loads of 64
     // steps spill (2 x 2048 x 8 heads of 33 and 24: 79 us, of 32 steps 32).
     static constexpr int C = WN == 2 || !WIDE ? 32 : Planes<T>::C;
     static constexpr int NP = Planes<T>::N, NS = Planes<T>::S;
@@ -415,7 +415,7 @@ __global__ __launch_bounds__(64 * NW, DX > 128 ? 1 : 2) void attend_walk_kernel(
     // A chunk of n steps from u0; FULL: n = C.
     auto chunk = [&](auto full, int64_t u0, int n) __attribute__((always_inline)) {
         constexpr bool FULL = decltype(full)::value;
-        if (!WIDE) fetch(u0);  // (many registers: not kept through a chunk)
+        if (!WIDE) fetch(u0);  // (an element a register: they would spill if kept for a chunk)
         lds_barrier();         // the tiles of the last chunk are read
         if (OUT) rx.template store<FULL>(lds.x, R.dx, n, 0);
         ry.template store<FULL>(lds.y, R.dx, n, 0);
@@ -633,8 +633,8 @@ hipError_t launch_attend_walk(const AttendArgs& a, bool maps, hipStream_t st) {
         dz = a.run[r].dz > dz ? a.run[r].dz : dz;
     }
     // a CU with one workgroup alone: eight waves with one column tile each rather than four
-    // with two (gradient of 4 x 2048 steps of 16 heads, 192 workgroups: 131 us against 145; two
-    // workgroups a CU, 512 for 32768 steps of 16 heads: 238 against 220)
+    // with two (gradient of 4 x 2048 steps of 16 heads, 192 workgroups: 146 us against 163; two
+    // workgroups a CU, 512 for 32768 steps of 16 heads: 252 against 233)
     const bool few = a.batch * a.heads * a.nseg * a.nrun <= 256;
     // small heads: two waves hold all columns of z; wide ones: two column tiles a wave, which
     // share what it reads of x and y
