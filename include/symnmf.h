@@ -528,8 +528,8 @@ int symnmf_linear_attention_grad(const symnmf_attend_desc* d, const void* q, con
                                  void* hip_stream);
 
 /* One step of a live stream: steps = 1 in the descriptor (the strides of a step
- * are not used); state -> new_state, which may be the same buffer; o (batch x
- * heads x dv, dense). Every product and sum in float32.
+ * are not used); state -> new_state, which may be the same buffer and is apart
+ * from all else; o (batch x heads x dv, dense). Every product and sum in float32.
  * Errors: E_INVALID, E_HIP. */
 int symnmf_linear_attention_step(const symnmf_attend_desc* d, const void* q, const void* k,
                                  const void* v, const float* decay, const float* state, void* o,
