@@ -188,19 +188,19 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamLaunch a, uint32_t first
     float g[8], m[8], v[8], p[8];
     P* pp = static_cast<P*>(t.param) + at;
     load8<G>(static_cast<const G*>(t.grad) + at, n, g);
-    // what m and v are kept with, as two numbers; of codes, by their scale (of v's, its square)
-    float k1 = a.b1, k1_rest = a.b1_rest, k2 = a.b2, k2_rest = a.b2_rest;
+    // what m is kept with, as two numbers; of codes, by their scale
+    float k1 = a.b1, k1_rest = a.b1_rest;
     if (LOW) {
         const float ms = n ? t.m_scale[block] : 0.f, vs = n ? t.v_scale[block] : 0.f;
         load_codes(static_cast<const uint8_t*>(t.m) + at, n, m);
         load_codes(static_cast<const uint8_t*>(t.v) + at, n, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= v[j];  // exact
+        for (int j = 0; j < 8; ++j) {
+            v[j] *= vs;  // (not vs * vs, which is 0 where the roots' squares are not yet)
+            v[j] *= v[j];
+        }
         k1 = a.b1 * ms;
         k1_rest = fmaf(a.b1, ms, -k1) + a.b1_rest * ms;
-        const float v2 = vs * vs, v2_rest = fmaf(vs, vs, -v2);
-        k2 = a.b2 * v2;
-        k2_rest = fmaf(a.b2, v2, -k2) + fmaf(a.b2, v2_rest, a.b2_rest * v2);
     } else {
         load8<float>(static_cast<const float*>(t.m) + at, n, m);
         load8<float>(static_cast<const float*>(t.v) + at, n, v);
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamLaunch a, uint32_t first
         m[j] = fmaf(k1, m[j], fmaf(k1_rest, m[j], a.c1 * x));
         // (a second moment past float32's range stays infinite; no code is)
         const float rest = LOW ? v[j] : fminf(v[j], FLT_MAX);
-        v[j] = fmaf(k2, v[j], fmaf(k2_rest, rest, a.c2 * (x * x)));
+        v[j] = fmaf(a.b2, v[j], fmaf(a.b2_rest, rest, a.c2 * (x * x)));
         r[j] = sqrtf(v[j]);
         p[j] = fmaf(-rate, m[j] / (r[j] * root + a.eps), fmaf(-decay, p[j], p[j]));
     }

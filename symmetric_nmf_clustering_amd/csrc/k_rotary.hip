@@ -13,8 +13,9 @@ namespace {
 
 // Sine and cosine of pos times freq (radians). The turns' whole part is taken off exactly: pos as
 // two numbers that float64 holds (52 and 11 bits), freq / 2 pi as two, the large product by an fma
-// that adds what is left of it unrounded. What is left is right to 2^-42 turns at any position (freq up to 1) and
-// goes to float32 with its remainder, whose first order is added to the functions' values.
+// that takes its own whole turns off before it rounds. What is left is right to 2^-42 turns at any
+// position (freq up to 1) and goes to float32 with its remainder, whose first order is added to the
+// functions' values.
 __device__ __forceinline__ void turn_of(int64_t pos, double freq, float* sine, float* cosine) {
     constexpr double kTurn = 0.15915494309189535, kTurnRest = -9.839338337591243e-18;  // 1 / 2 pi
     const double f = freq * kTurn, f_rest = fma(freq, kTurn, -f) + freq * kTurnRest;

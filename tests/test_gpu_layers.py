@@ -953,6 +953,25 @@ def test_bf16_rounds_its_outputs_alone(B, T, H, G, dk, dv):
         close(got[i], ref[i], (c + 2 * U * H) * mag[i], "bf16")
 
 
+def test_adamw_8_keeps_tiny_roots():
+    """Roots whose squares are among float32's smallest numbers survive a step without gradients."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    p = torch.zeros(512, device="cuda")
+    g = torch.full_like(p, 1e-19)
+    g[256:] = torch.logspace(-19, -17, 256, device="cuda")
+    m, v, ms, vs = api.adamw_states([p], bits=8)
+    hyper = {**HYPER, "beta2": 0.99, "eps": 1e-8}
+    api.adamw_step([p], [g], m, v, 1, m_scale=ms, v_scale=vs, **hyper)
+    first = decode(torch, v[0], vs[0])
+    api.adamw_step([p], [torch.zeros_like(g)], m, v, 2, m_scale=ms, v_scale=vs, **hyper)
+    second = decode(torch, v[0], vs[0])
+    assert (first > 0).all() and (second > 0).all()
+    # the code's half step, and 2^-149 on a square of at least 1e-40 or so
+    want = first * 0.99 ** 0.5
+    assert ((second - want).abs() <= want * (2.0 ** -4 + 1e-4) + vs[0].double().repeat_interleave(256) * 2.0 ** -9).all()
+
+
 # ---- every walk: two column tiles a wave, cut and whole, with and without lengths ---------
 
 def device_definition(torch, t, scale, gradient):
