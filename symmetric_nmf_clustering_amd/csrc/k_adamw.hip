@@ -218,7 +218,9 @@ __global__ __launch_bounds__(256) void adamw_kernel(AdamLaunch a, uint32_t first
         const float rest = LOW ? v[j] : fminf(v[j], FLT_MAX);
         v[j] = fmaf(a.b2, v[j], fmaf(a.b2_rest, rest, a.c2 * (x * x)));
         r[j] = sqrtf(v[j]);
-        p[j] = fmaf(-rate, m[j] / (r[j] * root + a.eps), fmaf(-decay, p[j], p[j]));
+        // (an infinite parameter, a mask's, stays)
+        const float kept = fmaf(-decay, __builtin_amdgcn_fmed3f(p[j], -FLT_MAX, FLT_MAX), p[j]);
+        p[j] = fmaf(-rate, m[j] / (r[j] * root + a.eps), kept);
     }
     if (n) store8<P>(pp, n, p);
     if (t.master && n) store8<float>(t.master + at, n, p);

@@ -972,6 +972,23 @@ def test_adamw_8_keeps_tiny_roots():
     assert ((second - want).abs() <= want * (2.0 ** -4 + 1e-4) + vs[0].double().repeat_interleave(256) * 2.0 ** -9).all()
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_infinite_parameters_stay(kind, bits):
+    """A parameter that holds a mask's infinities keeps them, with and without weight decay."""
+    torch = require_gpu()
+    from symmetric_nmf_clustering_amd import api
+    for decay in (0.0, 0.1):
+        p = torch.ones(300, device="cuda").to(types(torch)[kind])
+        p[3::7], p[5::7], p[6::7] = float("-inf"), float("inf"), float("nan")
+        keep = p.clone()
+        m, v, ms, vs = api.adamw_states([p], bits)
+        api.adamw_step([p], [torch.ones_like(p)], m, v, 1, lr=0.01, weight_decay=decay, m_scale=ms, v_scale=vs)
+        odd = ~torch.isfinite(keep)
+        assert torch.equal(torch.nan_to_num(p[odd].float(), nan=7.0), torch.nan_to_num(keep[odd].float(), nan=7.0))
+        assert torch.isfinite(p[~odd]).all() and (p[~odd] < 1).all()
+
+
 # ---- every walk: two column tiles a wave, cut and whole, with and without lengths ---------
 
 def device_definition(torch, t, scale, gradient):
