@@ -24,7 +24,7 @@
 // next to one another; 32 lanes share an 8-bit block. Which tensor is found from the
 // tensors' first workgroups, in the kernel's arguments. 108 million parameters: bf16 with
 // float32 masters and states (28 bytes each) 622 us, 4.8 TB/s; bf16 with 8-bit states (10
-// bytes) 223 us, 4.9 TB/s.
+// bytes) 226 us, 4.8 TB/s.
 #include <cfloat>
 
 #include "layers.h"
